@@ -287,7 +287,7 @@ def _framework(st):
                                             max_group_rows=st["max_rows"])
         return dict(y=y, dx=dx)
     plan = lh.lh_moe_sort(st["ids"], case["groups"])
-    xs = lh.lh_moe_dispatch(st["x"], plan["order"], case["top_k"])
+    xs = lh.lh_moe_dispatch(st["x"], plan["position"])
     y = lh.lh_moe_combine(st["ys"], plan["position"], st["weights"])
     out = dict(offsets=plan["offsets"], order=plan["order"], position=plan["position"], xs=xs, y=y)
     if kind == "moe_train":

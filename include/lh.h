@@ -538,6 +538,186 @@ lh_status lh_gptq_quantize(const void *w, int w_dtype, int64_t c_out, int64_t c_
                            int64_t ld_u, float *w_q, int64_t ld_q, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * What a language model does with the calibrated weights: activations
+ * quantised on the fly ("What is Local-Hessian": NVFP4 blocks of 16 with an
+ * E4M3 scale; max scaling maps the block's largest value to 6), products with
+ * the packed weights and their gradient, and the way of tokens to the experts
+ * of an MoE layer and back.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Activations to NVFP4 in one pass over x [n_groups][rows][ld_x] (fp32 or
+ * bf16; c_in % 16 == 0), with the per-tensor amax of the calibration (or of
+ * lh_absmax; tokens given as groups get a scale each).  Per 16 values:
+ *   code = the E4M3 code of LH_RULE_MAX, r = Cast(x / s), s = fl32(c * S_g),
+ * bit for bit as lh_select_scales(LH_RULE_MAX) and lh_fake_quant_nvfp4.
+ *   values       v_dtype (fp32 or bf16) [n_groups][rows][c_in]: r * c, the
+ *                quantised value in units of S_g, exact in either type (so
+ *                Q = values * S_g; lh_linear_nvfp4 takes S_g as x_scale)
+ *   packed_e2m1, scale_e4m3, global_scale: as lh_fake_quant_nvfp4.
+ * Outputs are dense, each optional, at least one given; values 16-byte,
+ * packed_e2m1 8-byte aligned.  x may have any alignment of its own type.
+ * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_ARG, LH_ERR_HIP.
+ */
+lh_status lh_quantize_nvfp4(const void *x, int x_dtype, int64_t rows, int64_t c_in, int64_t ld_x,
+                            int64_t n_groups, int64_t group_stride_x, const float *amax, void *values,
+                            int v_dtype, uint8_t *packed_e2m1, uint8_t *scale_e4m3, float *global_scale,
+                            void *stream);
+
+/*
+ * Scratch bytes with which lh_linear_nvfp4, lh_linear_nvfp4_grad and their
+ * ragged forms run fastest, from the sizes and types alone (n_rows: the rows
+ * per group, or all rows of a ragged call; grad: 0 for the product, 1 for the
+ * gradient; ragged: 0 or 1; max_group_rows as passed to a ragged call).  0
+ * bytes (NULL) is always accepted: other kernels then do the same work.
+ */
+size_t lh_linear_nvfp4_workspace_bytes(int grad, int ragged, int x_dtype, int64_t n_rows, int64_t c_in,
+                                       int64_t c_out, int64_t n_groups, int64_t max_group_rows);
+
+/*
+ * Product with NVFP4 weights (Y = W X of "Algorithm principle", token-major):
+ *   y[g][t][o] = global_scale[g] * x_scale[g]
+ *                * sum_c x[g][t][c] * r[g][o][c] * c[g][o][c / 16]
+ * for every group g, token t < n_tokens, output o < c_out; weights as
+ * lh_fake_quant_nvfp4 and lh_calibrate_nvfp4 write them (dense
+ * packed_e2m1 [n_groups][c_out][c_in/2], low nibble = even column, and
+ * scale_e4m3 [n_groups][c_out][c_in/16]; codes 0x01..0x7E).
+ * r * c is exact in bf16 and bf16 activations enter as they are; fp32
+ * activations as three bf16 values that add up to them exactly.  Products
+ * are exact, sums fp32 on matrix cores; one rounding to y_dtype at the end.
+ * The order of a sum depends only on the arguments, never on the run.
+ *   x            fp32 or bf16, [n_tokens][ld_x] per group, ld_x >= c_in.
+ *   global_scale fp32 [n_groups] (S_g).  x_scale: fp32 [n_groups] or NULL
+ *                (1): the S_g of activations given as lh_quantize_nvfp4 values.
+ *   y            fp32 or bf16, [n_tokens][ld_y] per group, ld_y >= c_out;
+ *                must not overlap x.  n_groups > 1: group_stride_y >=
+ *                n_tokens * ld_y.
+ *   workspace    NULL/0, or at least lh_linear_nvfp4_workspace_bytes(0, 0,
+ *                x_dtype, n_tokens, c_in, c_out, n_groups, 0) bytes, 256-byte
+ *                aligned.
+ * c_in % 16 == 0, c_out any.  c_in = 0 writes zeros.
+ * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_WORKSPACE,
+ * LH_ERR_ARG, LH_ERR_HIP.
+ */
+lh_status lh_linear_nvfp4(const void *x, int x_dtype, int64_t n_tokens, int64_t c_in, int64_t ld_x,
+                          int64_t group_stride_x, const uint8_t *packed_e2m1, const uint8_t *scale_e4m3,
+                          const float *global_scale, int64_t c_out, int64_t n_groups, const float *x_scale,
+                          void *y, int y_dtype, int64_t ld_y, int64_t group_stride_y, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * The product's gradient to its input, the weights being frozen:
+ *   dx[g][t][c] = global_scale[g] * sum_o dy[g][t][o] * r[g][o][c] * c[g][o][c / 16]
+ * (with activations that went through lh_quantize_nvfp4: the straight-through
+ * gradient to them).  dy [n_tokens][ld_dy] with c_out columns, dx
+ * [n_tokens][ld_dx] with c_in; types, exactness, aliasing, workspace (grad =
+ * 1) and errors as lh_linear_nvfp4.  c_out = 0 writes zeros.
+ */
+lh_status lh_linear_nvfp4_grad(const void *dy, int dy_dtype, int64_t n_tokens, int64_t c_out, int64_t ld_dy,
+                               int64_t group_stride_dy, const uint8_t *packed_e2m1,
+                               const uint8_t *scale_e4m3, const float *global_scale, int64_t c_in,
+                               int64_t n_groups, void *dx, int dx_dtype, int64_t ld_dx,
+                               int64_t group_stride_dx, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * lh_linear_nvfp4 for rows sorted by expert: rows token_offsets[g] ..
+ * token_offsets[g+1]-1 of x [n_rows][ld_x] meet the weights of group g, and
+ * the result goes to the same rows of y.  Rows of no group are not written.
+ *   token_offsets  device int64 [n_groups + 1], 8-byte aligned, expected
+ *                  non-decreasing within [0, n_rows]; offsets are clamped
+ *                  and a decreasing pair gives an empty group, so that no
+ *                  offset can lead outside x or y (as
+ *                  lh_accumulate_hessian_ragged).
+ *   max_group_rows host bound on any group's rows, or 0 if unknown; it only
+ *                  shapes the work split.
+ * Everything else as lh_linear_nvfp4 (ragged = 1 in the workspace query).
+ */
+lh_status lh_linear_nvfp4_ragged(const void *x, int x_dtype, int64_t n_rows, int64_t c_in, int64_t ld_x,
+                                 const int64_t *token_offsets, int64_t n_groups, int64_t max_group_rows,
+                                 const uint8_t *packed_e2m1, const uint8_t *scale_e4m3,
+                                 const float *global_scale, int64_t c_out, const float *x_scale, void *y,
+                                 int y_dtype, int64_t ld_y, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* lh_linear_nvfp4_grad for rows sorted by expert, as lh_linear_nvfp4_ragged. */
+lh_status lh_linear_nvfp4_ragged_grad(const void *dy, int dy_dtype, int64_t n_rows, int64_t c_out,
+                                      int64_t ld_dy, const int64_t *token_offsets, int64_t n_groups,
+                                      int64_t max_group_rows, const uint8_t *packed_e2m1,
+                                      const uint8_t *scale_e4m3, const float *global_scale, int64_t c_in,
+                                      void *dx, int dx_dtype, int64_t ld_dx, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+typedef enum lh_index {
+    LH_INDEX_I32 = 0, /* int32 */
+    LH_INDEX_I64 = 1  /* int64 */
+} lh_index;
+
+/* Scratch bytes lh_moe_sort needs for n_tokens * top_k assignments (0 for few). */
+size_t lh_moe_sort_workspace_bytes(int64_t n_tokens, int64_t top_k, int64_t n_groups);
+
+/*
+ * Assignments sorted by expert.  Assignment a = t * top_k + k sends token t to
+ * expert expert_ids[a]; an id outside [0, n_groups) means none (dropped, for
+ * instance over the expert's capacity).  The sort is stable:
+ *   offsets  int64 [n_groups + 1]: expert g owns rows offsets[g] ..
+ *            offsets[g+1]-1; offsets[n_groups] = the rows with an expert.
+ *   position int32 [n_tokens][top_k]: the row p of assignment a; without an
+ *            expert -1 - p, p being its row past offsets[n_groups].
+ *   order    int32 [n_tokens * top_k], or NULL: the assignment of row p;
+ *            -1 - a for one without an expert.
+ * offsets is what lh_accumulate_hessian_ragged and lh_linear_nvfp4_ragged
+ * take.  n_groups <= 1024, n_tokens * top_k < 2^31.
+ *   expert_ids  ids_type (an lh_index), [n_tokens][top_k], contiguous.
+ *   workspace   at least lh_moe_sort_workspace_bytes() bytes, 4-byte aligned
+ *               (may be NULL where that is 0).
+ * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_WORKSPACE,
+ * LH_ERR_ARG, LH_ERR_HIP.
+ */
+lh_status lh_moe_sort(const void *expert_ids, int ids_type, int64_t n_tokens, int64_t top_k,
+                      int64_t n_groups, int64_t *offsets, int32_t *position, int32_t *order,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Tokens' rows to their experts: xs[position[t][k]] = x[t] for every
+ * assignment with an expert; the rows of the others are set to zero.  Its
+ * gradient is lh_moe_combine without weights.
+ *   x  [n_tokens][ld_x], xs [n_rows][ld_xs], both dtype (fp32 or bf16) with
+ *   `cols` columns (any number), n_rows >= n_tokens * top_k; entries of
+ *   position beyond n_rows are ignored.
+ * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_ARG, LH_ERR_HIP.
+ */
+lh_status lh_moe_dispatch(const void *x, int dtype, int64_t n_tokens, int64_t cols, int64_t ld_x,
+                          const int32_t *position, int64_t top_k, void *xs, int64_t n_rows, int64_t ld_xs,
+                          void *stream);
+
+/*
+ * Rows back to their tokens: y[t] = sum_k weights[t][k] * ys[position[t][k]]
+ * over the assignments with an expert (a token without any gets zero), fp32
+ * sums in the order of k, rounded once.  weights: fp32 [n_tokens][top_k], or
+ * NULL for 1.  Sizes, types and errors as lh_moe_dispatch.
+ */
+lh_status lh_moe_combine(const void *ys, int dtype, int64_t n_rows, int64_t cols, int64_t ld_ys,
+                         const int32_t *position, const float *weights, int64_t n_tokens, int64_t top_k,
+                         void *y, int64_t ld_y, void *stream);
+
+/*
+ * The gradients of lh_moe_combine:
+ *   dys[position[t][k]] = weights[t][k] * dy[t]   (zero rows for assignments
+ *                         without an expert), dtype, [n_rows][ld_dys]
+ *   dweights[t][k]      = <dy[t], ys[position[t][k]]> (0 without an expert),
+ *                         fp32 [n_tokens][top_k]
+ * Either may be NULL, not both; weights NULL: 1.  ys may be NULL when
+ * dweights is.  dys must not overlap dy or ys.  Sums in a fixed order.
+ */
+lh_status lh_moe_combine_grad(const void *dy, int dtype, int64_t n_tokens, int64_t cols, int64_t ld_dy,
+                              const void *ys, int64_t n_rows, int64_t ld_ys, const int32_t *position,
+                              int64_t top_k, const float *weights, void *dys, int64_t ld_dys,
+                              float *dweights, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,7 @@ LIB_PATH = os.path.join(_PKG, "liblh.so")
 
 LH_DTYPE_F32, LH_DTYPE_BF16 = 0, 1
 LH_LAYOUT_CHANNEL_MAJOR, LH_LAYOUT_TOKEN_MAJOR = 0, 1
+LH_INDEX_I32, LH_INDEX_I64 = 0, 1
 LH_RULE_SWEEP, LH_RULE_MAX, LH_RULE_FOUR_OVER_SIX, LH_RULE_AMAX_SEARCH = 0, 1, 2, 3
 N_CANDIDATES = 126
 BLOCK = 16
@@ -95,6 +96,28 @@ def _load() -> ctypes.CDLL:
     lib.lh_gptq_quantize.restype = I
     lib.lh_fake_quant_nvfp4.argtypes = [P, I, I64, I64, I64, I64, I64, P, P, P, P, P, P, P]
     lib.lh_fake_quant_nvfp4.restype = I
+    lib.lh_quantize_nvfp4.argtypes = [P, I, I64, I64, I64, I64, I64, P, P, I, P, P, P, P]
+    lib.lh_quantize_nvfp4.restype = I
+    lib.lh_linear_nvfp4_workspace_bytes.argtypes = [I, I, I, I64, I64, I64, I64, I64]
+    lib.lh_linear_nvfp4_workspace_bytes.restype = SZ
+    lib.lh_linear_nvfp4.argtypes = [P, I, I64, I64, I64, I64, P, P, P, I64, I64, P, P, I, I64, I64, P, SZ, P]
+    lib.lh_linear_nvfp4.restype = I
+    lib.lh_linear_nvfp4_grad.argtypes = [P, I, I64, I64, I64, I64, P, P, P, I64, I64, P, I, I64, I64, P, SZ, P]
+    lib.lh_linear_nvfp4_grad.restype = I
+    lib.lh_linear_nvfp4_ragged.argtypes = [P, I, I64, I64, I64, P, I64, I64, P, P, P, I64, P, P, I, I64, P, SZ, P]
+    lib.lh_linear_nvfp4_ragged.restype = I
+    lib.lh_linear_nvfp4_ragged_grad.argtypes = [P, I, I64, I64, I64, P, I64, I64, P, P, P, I64, P, I, I64, P, SZ, P]
+    lib.lh_linear_nvfp4_ragged_grad.restype = I
+    lib.lh_moe_sort_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.lh_moe_sort_workspace_bytes.restype = SZ
+    lib.lh_moe_sort.argtypes = [P, I, I64, I64, I64, P, P, P, P, SZ, P]
+    lib.lh_moe_sort.restype = I
+    lib.lh_moe_dispatch.argtypes = [P, I, I64, I64, I64, P, I64, P, I64, I64, P]
+    lib.lh_moe_dispatch.restype = I
+    lib.lh_moe_combine.argtypes = [P, I, I64, I64, I64, P, P, I64, I64, P, I64, P]
+    lib.lh_moe_combine.restype = I
+    lib.lh_moe_combine_grad.argtypes = [P, I, I64, I64, I64, P, I64, I64, P, I64, P, P, I64, P, P]
+    lib.lh_moe_combine_grad.restype = I
     return lib
 
 
@@ -105,7 +128,9 @@ EXPORTS = ("lh_abi_version", "lh_status_string", "lh_last_error_message", "lh_ab
            "lh_scale_sweep_fake_quant", "lh_calibrate_workspace_bytes", "lh_calibrate_nvfp4",
            "lh_calibrate_prologue", "lh_calibrate_sweep", "lh_calibrate_nvfp4_noalloc", "lh_select_scales", "lh_fake_quant_nvfp4", "lh_full_hessian", "lh_output_error_workspace_bytes",
            "lh_output_error", "lh_scaled_histogram", "lh_gptq_workspace_bytes", "lh_gptq_prepare",
-           "lh_gptq_quantize")
+           "lh_gptq_quantize", "lh_quantize_nvfp4", "lh_linear_nvfp4_workspace_bytes", "lh_linear_nvfp4",
+           "lh_linear_nvfp4_grad", "lh_linear_nvfp4_ragged", "lh_linear_nvfp4_ragged_grad",
+           "lh_moe_sort_workspace_bytes", "lh_moe_sort", "lh_moe_dispatch", "lh_moe_combine", "lh_moe_combine_grad")
 
 
 def _check(status: int) -> None:
@@ -611,3 +636,291 @@ def lh_gptq_quantize(w: torch.Tensor, best_idx: torch.Tensor, amax: torch.Tensor
                                 u.stride(0), _ptr(w_q), w_q.stride(0) if c_out > 1 else c_in, _ptr(ws),
                                 ws.numel() * ws.element_size(), _stream(w)))
     return w_q
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor (a single row has no meaningful one)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _dense(t: torch.Tensor | None, name: str, dtype, shape=None) -> None:
+    """The library takes these as dense arrays of one type."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors on different devices (%s and %s)" % (first.device, t.device))
+
+
+def lh_quantize_nvfp4(x: torch.Tensor, amax: torch.Tensor, values: bool | torch.Tensor = True,
+                      packed: bool | torch.Tensor = False, scale_e4m3: bool | torch.Tensor = False,
+                      global_scale: bool | torch.Tensor = False, values_dtype: torch.dtype | None = None) -> dict:
+    """Activations to NVFP4 in one pass, block scales by the max rule.  x
+    [rows, c_in] or [n_groups, rows, c_in]; amax fp32 [n_groups] (device),
+    from the calibration or lh_absmax.  Returns a dict with the requested
+    outputs: values [g, rows, c_in] = r * c in units of S_g (exact; x's dtype
+    unless values_dtype says otherwise), packed, scale_e4m3, global_scale as
+    lh_fake_quant_nvfp4."""
+    _require_device(x, amax)
+    x3 = _as3(x)
+    if x3.shape[-1] > 0 and x3.stride(-1) != 1:
+        raise ValueError("last dim of x must be contiguous")
+    g, rows, c_in = x3.shape
+    _same_device(x, amax)
+    _dense(amax, "amax", torch.float32, (g,))
+    dev = x.device
+
+    def out(req, shape, dtype, name):
+        if isinstance(req, torch.Tensor):
+            _require_device(req)
+            _same_device(x, req)
+            _dense(req, name, dtype, shape)
+            return req
+        return torch.empty(shape, dtype=dtype, device=dev) if req else None
+
+    vdt = values.dtype if isinstance(values, torch.Tensor) else values_dtype or x.dtype
+    res = dict(values=out(values, (g, rows, c_in), vdt, "values"),
+               packed=out(packed, (g, rows, c_in // 2), torch.uint8, "packed"),
+               scale_e4m3=out(scale_e4m3, (g, rows, c_in // BLOCK), torch.uint8, "scale_e4m3"),
+               global_scale=out(global_scale, (g,), torch.float32, "global_scale"))
+    v = res["values"]
+    _check(lib.lh_quantize_nvfp4(_ptr(x3), _dtype(x3), rows, c_in, _ld(x3), g, _group_stride(x3), _ptr(amax),
+                                 _ptr(v), LH_DTYPE_F32 if v is None else _dtype(v), _ptr(res["packed"]),
+                                 _ptr(res["scale_e4m3"]), _ptr(res["global_scale"]), _stream(x)))
+    return {k: t for k, t in res.items() if t is not None}
+
+
+def lh_linear_nvfp4_workspace_bytes(n_rows: int, c_in: int, c_out: int, n_groups: int = 1,
+                                    dtype: torch.dtype = torch.bfloat16, grad: bool = False, ragged: bool = False,
+                                    max_group_rows: int = 0) -> int:
+    code = LH_DTYPE_BF16 if dtype == torch.bfloat16 else LH_DTYPE_F32
+    return int(lib.lh_linear_nvfp4_workspace_bytes(int(grad), int(ragged), code, n_rows, c_in, c_out, n_groups,
+                                                   max_group_rows))
+
+
+def _linear(x, offsets, packed, scale_e4m3, global_scale, x_scale, y, out_dtype, max_group_rows, workspace, grad):
+    """The four product calls: x [rows, .] or [g, rows, .]; offsets None or int64 [g + 1]."""
+    _require_device(x, offsets, packed, scale_e4m3, global_scale, x_scale, y)
+    _same_device(x, offsets, packed, scale_e4m3, global_scale, x_scale, y)
+    x3, p3, s3 = _as3(x), _as3(packed), _as3(scale_e4m3)
+    g, c_out, half = p3.shape
+    c_in = 2 * half
+    _dense(p3, "packed", torch.uint8)
+    _dense(s3, "scale_e4m3", torch.uint8, (g, c_out, c_in // BLOCK))
+    _dense(global_scale, "global_scale", torch.float32)
+    _dense(x_scale, "x_scale", torch.float32)
+    if global_scale.numel() != g or x_scale is not None and x_scale.numel() != g:
+        raise ValueError("global_scale and x_scale need one value for each of the %d groups" % g)
+    k, m = (c_out, c_in) if grad else (c_in, c_out)
+    rows = x3.shape[1]
+    if x3.shape[2] != k:
+        raise ValueError("the input has %d columns, the weights need %d" % (x3.shape[2], k))
+    if x3.shape[2] > 0 and x3.stride(-1) != 1:
+        raise ValueError("last dim of the input must be contiguous")
+    if offsets is None:
+        if x3.shape[0] != g:
+            raise ValueError("the input has %d groups, the weights %d" % (x3.shape[0], g))
+    else:
+        if x.dim() != 2:
+            raise ValueError("ragged rows are a 2-D tensor")
+        _dense(offsets, "offsets", torch.int64, (g + 1,))
+    shape = tuple(x.shape[:-1]) + (m,)
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif tuple(y.shape) != shape or (m > 0 and y.stride(-1) != 1):
+        raise ValueError("the output must have shape %s and a contiguous last dim" % (shape,))
+    y3 = _as3(y)
+    ws, ws_bytes = None, 0
+    if workspace is True:
+        ws_bytes = lh_linear_nvfp4_workspace_bytes(rows, c_in, c_out, g, x.dtype, grad, offsets is not None,
+                                                   max_group_rows)
+        if ws_bytes:
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
+    elif isinstance(workspace, torch.Tensor):
+        ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
+    xa = (_ptr(x3), _dtype(x3), rows, k, _ld(x3))
+    wa = (_ptr(p3), _ptr(s3), _ptr(global_scale), m)
+    ya = (_ptr(y3), _dtype(y3), _ld(y3))
+    end = (_ptr(ws), ws_bytes, _stream(x))
+    xs = () if grad else (_ptr(x_scale),)
+    if offsets is None:
+        f = lib.lh_linear_nvfp4_grad if grad else lib.lh_linear_nvfp4
+        _check(f(*xa, _group_stride(x3), *wa, g, *xs, *ya, _group_stride(y3), *end))
+    else:
+        f = lib.lh_linear_nvfp4_ragged_grad if grad else lib.lh_linear_nvfp4_ragged
+        _check(f(*xa, _ptr(offsets), g, int(max_group_rows), *wa, *xs, *ya, *end))
+    return y
+
+
+def lh_linear_nvfp4(x: torch.Tensor, packed: torch.Tensor, scale_e4m3: torch.Tensor, global_scale: torch.Tensor,
+                    x_scale: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                    out_dtype: torch.dtype | None = None,
+                    workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """y = x W^T with NVFP4 weights as lh_fake_quant_nvfp4 / lh_calibrate_nvfp4
+    return them (packed [g, c_out, c_in/2], scale_e4m3 [g, c_out, c_in/16],
+    global_scale [g]).  x [n_tokens, c_in] (one group) or [g, n_tokens, c_in],
+    bf16 or fp32; y in x's dtype unless out_dtype or y says otherwise.
+    x_scale: S_g of activations given as lh_quantize_nvfp4 values."""
+    return _linear(x, None, packed, scale_e4m3, global_scale, x_scale, y, out_dtype, 0, workspace, False)
+
+
+def lh_linear_nvfp4_grad(dy: torch.Tensor, packed: torch.Tensor, scale_e4m3: torch.Tensor,
+                         global_scale: torch.Tensor, dx: torch.Tensor | None = None,
+                         out_dtype: torch.dtype | None = None,
+                         workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """dx = dy W, the gradient of lh_linear_nvfp4 to its input (frozen weights)."""
+    return _linear(dy, None, packed, scale_e4m3, global_scale, None, dx, out_dtype, 0, workspace, True)
+
+
+def lh_linear_nvfp4_ragged(x: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor, scale_e4m3: torch.Tensor,
+                           global_scale: torch.Tensor, x_scale: torch.Tensor | None = None,
+                           y: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                           max_group_rows: int = 0, workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """lh_linear_nvfp4 for x [n_rows, c_in] whose rows offsets[g] ..
+    offsets[g+1]-1 (device int64 [g + 1]) meet the weights of group g; rows of
+    no group are not written."""
+    return _linear(x, offsets, packed, scale_e4m3, global_scale, x_scale, y, out_dtype, max_group_rows, workspace,
+                   False)
+
+
+def lh_linear_nvfp4_ragged_grad(dy: torch.Tensor, offsets: torch.Tensor, packed: torch.Tensor,
+                                scale_e4m3: torch.Tensor, global_scale: torch.Tensor,
+                                dx: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                                max_group_rows: int = 0,
+                                workspace: torch.Tensor | bool | None = True) -> torch.Tensor:
+    """dx = dy W row by row, the gradient of lh_linear_nvfp4_ragged to its input."""
+    return _linear(dy, offsets, packed, scale_e4m3, global_scale, None, dx, out_dtype, max_group_rows, workspace,
+                   True)
+
+
+def lh_moe_sort_workspace_bytes(n_tokens: int, top_k: int, n_groups: int) -> int:
+    return int(lib.lh_moe_sort_workspace_bytes(n_tokens, top_k, n_groups))
+
+
+def lh_moe_sort(expert_ids: torch.Tensor, n_groups: int, order: bool = True,
+                workspace: torch.Tensor | None = None) -> dict:
+    """Assignments [n_tokens, top_k] (int32 or int64 expert ids; outside
+    [0, n_groups): dropped) sorted by expert, stable.  Returns offsets int64
+    [n_groups + 1], position int32 [n_tokens, top_k] (the row, or -1 - row of
+    a dropped one) and, with order=True, order int32 [n_tokens * top_k] (the
+    assignment of each row, or -1 - it)."""
+    _require_device(expert_ids, workspace)
+    if expert_ids.dim() != 2:
+        raise ValueError("expert_ids must be [n_tokens, top_k]")
+    if expert_ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("expert_ids must be int32 or int64, got %s" % expert_ids.dtype)
+    if not expert_ids.is_contiguous():
+        raise ValueError("expert_ids must be contiguous")
+    t, k = expert_ids.shape
+    i32 = dict(dtype=torch.int32, device=expert_ids.device)
+    res = dict(offsets=torch.empty(n_groups + 1, dtype=torch.int64, device=expert_ids.device),
+               position=torch.empty((t, k), **i32), order=torch.empty(t * k, **i32) if order else None)
+    if workspace is None:
+        n = lh_moe_sort_workspace_bytes(t, k, n_groups)
+        workspace = torch.empty(n, dtype=torch.uint8, device=expert_ids.device) if n else None
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.lh_moe_sort(_ptr(expert_ids), LH_INDEX_I64 if expert_ids.dtype == torch.int64 else LH_INDEX_I32, t, k,
+                           n_groups, _ptr(res["offsets"]), _ptr(res["position"]), _ptr(res["order"]),
+                           _ptr(workspace), nbytes, _stream(expert_ids)))
+    return {key: v for key, v in res.items() if v is not None}
+
+
+def _rows2(t: torch.Tensor, name: str, cols: int | None = None, like: torch.Tensor | None = None) -> torch.Tensor:
+    if t.dim() != 2 or (t.shape[1] > 0 and t.stride(1) != 1):
+        raise ValueError("%s must be 2-D with contiguous rows" % name)
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError("%s has %d columns, expected %d" % (name, t.shape[1], cols))
+    if like is not None and t.dtype != like.dtype:
+        raise TypeError("%s must be %s, got %s" % (name, like.dtype, t.dtype))
+    return t
+
+
+def lh_moe_dispatch(x: torch.Tensor, position: torch.Tensor, xs: torch.Tensor | None = None) -> torch.Tensor:
+    """Tokens' rows to their experts: xs[position[t, k]] = x[t], zero rows for
+    dropped assignments; xs [n_tokens * top_k, cols] unless given."""
+    _require_device(x, position, xs)
+    _same_device(x, position, xs)
+    _rows2(x, "x")
+    t, cols = x.shape
+    _dense(position, "position", torch.int32)
+    if position.dim() != 2 or position.shape[0] != t:
+        raise ValueError("position must be [n_tokens, top_k]")
+    k = position.shape[1]
+    if xs is None:
+        xs = torch.empty((t * k, cols), dtype=x.dtype, device=x.device)
+    _rows2(xs, "xs", cols, x)
+    _check(lib.lh_moe_dispatch(_ptr(x), _dtype(x), t, cols, _row_stride(x), _ptr(position), k, _ptr(xs), xs.shape[0],
+                               _row_stride(xs), _stream(x)))
+    return xs
+
+
+def lh_moe_combine(ys: torch.Tensor, position: torch.Tensor, weights: torch.Tensor | None = None,
+                   y: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows back to their tokens: y[t] = sum_k weights[t, k] ys[position[t, k]]
+    over the assignments that have an expert (weights fp32, None: 1)."""
+    _require_device(ys, position, weights, y)
+    _same_device(ys, position, weights, y)
+    _rows2(ys, "ys")
+    _dense(position, "position", torch.int32)
+    if position.dim() != 2:
+        raise ValueError("position must be [n_tokens, top_k]")
+    t, k = position.shape
+    _dense(weights, "weights", torch.float32, (t, k))
+    cols = ys.shape[1]
+    if y is None:
+        y = torch.empty((t, cols), dtype=ys.dtype, device=ys.device)
+    _rows2(y, "y", cols, ys)
+    if y.shape[0] != t:
+        raise ValueError("y must have one row per token")
+    _check(lib.lh_moe_combine(_ptr(ys), _dtype(ys), ys.shape[0], cols, _row_stride(ys), _ptr(position),
+                              _ptr(weights), t, k, _ptr(y), _row_stride(y), _stream(ys)))
+    return y
+
+
+def lh_moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, position: torch.Tensor,
+                        weights: torch.Tensor | None = None, dys: torch.Tensor | bool = True,
+                        dweights: torch.Tensor | bool = True):
+    """Gradients of lh_moe_combine: (dys, dweights) with dys[position[t, k]] =
+    weights[t, k] dy[t] (zero rows for dropped assignments) and dweights[t, k]
+    = <dy[t], ys[position[t, k]]>; None where not requested (False)."""
+    _require_device(dy, ys, position, weights)
+    _same_device(dy, ys, position, weights)
+    _rows2(dy, "dy")
+    t, cols = dy.shape
+    _rows2(ys, "ys", cols, dy)
+    _dense(position, "position", torch.int32)
+    if position.dim() != 2 or position.shape[0] != t:
+        raise ValueError("position must be [n_tokens, top_k]")
+    k = position.shape[1]
+    _dense(weights, "weights", torch.float32, (t, k))
+    if dys is True:
+        dys = torch.empty(ys.shape, dtype=ys.dtype, device=ys.device)
+    elif dys is False:
+        dys = None
+    if dys is not None:
+        _require_device(dys)
+        _same_device(dy, dys)
+        _rows2(dys, "dys", cols, dy)
+        if dys.shape[0] != ys.shape[0]:
+            raise ValueError("dys must have ys's rows")
+    if dweights is True:
+        dweights = torch.empty((t, k), dtype=torch.float32, device=dy.device)
+    elif dweights is False:
+        dweights = None
+    if dweights is not None:
+        _require_device(dweights)
+        _same_device(dy, dweights)
+        _dense(dweights, "dweights", torch.float32, (t, k))
+    _check(lib.lh_moe_combine_grad(_ptr(dy), _dtype(dy), t, cols, _row_stride(dy), _ptr(ys), ys.shape[0],
+                                   _row_stride(ys), _ptr(position), k, _ptr(weights), _ptr(dys),
+                                   0 if dys is None else _row_stride(dys), _ptr(dweights), _stream(dy)))
+    return dys, dweights

@@ -15,8 +15,18 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblh.so")
-SOURCES = ["lh_api.hip", "lh_hessian.hip", "lh_sweep.hip", "lh_quant.hip", "lh_dense.hip"]
-HEADERS = ["lh_device.h", "lh_internal.h"]
+# object -> its sources: lh_quant.o holds everything that reads or writes the
+# packed format or feeds such a kernel (one relocatable object from three
+# sources, so that the library links from the same five objects)
+OBJECTS = {
+    "lh_api.o": ["lh_api.hip"],
+    "lh_hessian.o": ["lh_hessian.hip"],
+    "lh_sweep.o": ["lh_sweep.hip"],
+    "lh_quant.o": ["lh_quant.hip", "lh_linear.hip", "lh_moe.hip"],
+    "lh_dense.o": ["lh_dense.hip"],
+}
+SOURCES = [src for parts in OBJECTS.values() for src in parts]
+HEADERS = ["lh_device.h", "lh_internal.h", "lh_rows.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -35,21 +45,26 @@ def build(force: bool = True, verbose: bool = False, resource_usage: bool = Fals
     os.makedirs(obj_dir, exist_ok=True)
     procs = []
     for src in SOURCES:
-        obj = os.path.join(obj_dir, src.replace(".hip", ".o"))
+        whole = src.replace(".hip", ".o")
+        obj = os.path.join(obj_dir, whole if OBJECTS.get(whole) == [src] else src.replace(".hip", ".part.o"))
         cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         if resource_usage:
             cmd.append("-Rpass-analysis=kernel-resource-usage")
         procs.append((src, obj, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    objs, failed = [], []
+    made, failed = {}, []
     for src, obj, p in procs:
         out, _ = p.communicate()
         if verbose or p.returncode != 0 or resource_usage:
             sys.stderr.write(out)
         if p.returncode != 0:
             failed.append(src)
-        objs.append(obj)
+        made[src] = obj
     if failed:
         raise RuntimeError("hipcc failed for: " + ", ".join(failed))
+    objs = [os.path.join(obj_dir, name) for name in OBJECTS]
+    for name, parts in OBJECTS.items():
+        if len(parts) > 1:
+            subprocess.run(["ld", "-r", "-o", os.path.join(obj_dir, name), *(made[src] for src in parts)], check=True)
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)

@@ -547,6 +547,228 @@ lh_status lh_gptq_quantize(const void* w, int w_dtype, int64_t c_out, int64_t c_
   return e == hipSuccess ? LH_OK : hip_fail(e, fn);
 }
 
+// ---------------------------------------------------------------------------
+// Activation quantisation, products with packed weights, expert routing.
+// ---------------------------------------------------------------------------
+lh_status lh_quantize_nvfp4(const void* x, int x_dtype, int64_t rows, int64_t c_in, int64_t ld_x, int64_t n_groups,
+                            int64_t group_stride_x, const float* amax, void* values, int v_dtype,
+                            uint8_t* packed_e2m1, uint8_t* scale_e4m3, float* global_scale, void* stream) {
+  const char* fn = "lh_quantize_nvfp4";
+  g_msg[0] = '\0';
+  if (!valid_dtype(x_dtype)) return fail(LH_ERR_DTYPE, "%s: x_dtype must be 0 (f32) or 1 (bf16)", fn);
+  if (values && !valid_dtype(v_dtype)) return fail(LH_ERR_DTYPE, "%s: v_dtype must be 0 (f32) or 1 (bf16)", fn);
+  if (rows < 0 || c_in < 0 || n_groups < 0 || group_stride_x < 0)
+    return fail(LH_ERR_SHAPE, "%s: negative size or stride", fn);
+  if (c_in % 16 != 0) return fail(LH_ERR_SHAPE, "%s: c_in must be a multiple of 16", fn);
+  if (ld_x < c_in) return fail(LH_ERR_SHAPE, "%s: ld_x < c_in", fn);
+  if (!values && !packed_e2m1 && !scale_e4m3 && !global_scale)
+    return fail(LH_ERR_ARG, "%s: no output requested", fn);
+  if (n_groups > 0 && amax == nullptr) return fail(LH_ERR_NULL, "%s: amax is NULL", fn);
+  if (n_groups > 0 && rows > 0 && c_in > 0 && x == nullptr) return fail(LH_ERR_NULL, "%s: x is NULL", fn);
+  if (!aligned(x, elem_size(x_dtype)) || !aligned(amax, 4) || !aligned(global_scale, 4) || !aligned(values, 16) ||
+      !aligned(packed_e2m1, 8))
+    return fail(LH_ERR_ARG, "%s: misaligned pointer (values needs 16 bytes, packed_e2m1 8)", fn);
+  if (n_groups == 0) return LH_OK;
+  lh::QuantizeArgs a{x, x_dtype, rows, c_in, ld_x, n_groups, group_stride_x, amax, values, v_dtype, packed_e2m1,
+                     scale_e4m3, global_scale};
+  hipError_t e = lh::launch_quantize(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+size_t lh_linear_nvfp4_workspace_bytes(int grad, int ragged, int x_dtype, int64_t n_rows, int64_t c_in, int64_t c_out,
+                                       int64_t n_groups, int64_t max_group_rows) {
+  if (!valid_dtype(x_dtype) || n_rows <= 0 || c_in <= 0 || c_out <= 0 || n_groups <= 0 || c_in % 16 != 0 ||
+      max_group_rows < 0)
+    return 0;
+  lh::LinearArgs a{};
+  a.grad = grad != 0;
+  a.ragged = ragged != 0;
+  a.x_dtype = x_dtype;
+  a.rows = n_rows;
+  a.c_in = c_in;
+  a.c_out = c_out;
+  a.n_groups = n_groups;
+  a.max_group_rows = max_group_rows;
+  return lh::linear_ws_bytes(a);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks that the four product entry points share; a holds their
+// arguments, x_len and y_len the columns of x and y.
+lh_status run_linear(const char* fn, lh::LinearArgs& a, int64_t x_len, int64_t y_len, void* stream) {
+  g_msg[0] = '\0';
+  if (!valid_dtype(a.x_dtype) || !valid_dtype(a.y_dtype))
+    return fail(LH_ERR_DTYPE, "%s: the types of input and output must be 0 (f32) or 1 (bf16)", fn);
+  if (a.rows < 0 || a.c_in < 0 || a.c_out < 0 || a.n_groups < 0 || a.gstride_x < 0 || a.gstride_y < 0 ||
+      a.max_group_rows < 0)
+    return fail(LH_ERR_SHAPE, "%s: negative size or stride", fn);
+  if (a.c_in % 16 != 0) return fail(LH_ERR_SHAPE, "%s: c_in must be a multiple of 16", fn);
+  if (a.ld_x < x_len || a.ld_y < y_len) return fail(LH_ERR_SHAPE, "%s: a leading dimension is smaller than its row", fn);
+  if (!a.ragged && a.n_groups > 1 && a.gstride_y < a.rows * a.ld_y)
+    return fail(LH_ERR_SHAPE, "%s: the output's group stride would overlap groups", fn);
+  const bool work = a.rows > 0 && a.n_groups > 0 && y_len > 0;
+  const bool reads = work && x_len > 0;
+  if (work && a.y == nullptr) return fail(LH_ERR_NULL, "%s: the output is NULL", fn);
+  if (work && a.gscale == nullptr) return fail(LH_ERR_NULL, "%s: global_scale is NULL", fn);
+  if (work && a.ragged && a.offsets == nullptr) return fail(LH_ERR_NULL, "%s: token_offsets is NULL", fn);
+  if (reads && (a.x == nullptr || a.packed == nullptr || a.codes == nullptr))
+    return fail(LH_ERR_NULL, "%s: the input, packed_e2m1 and scale_e4m3 are required", fn);
+  if (a.ws == nullptr && a.ws_bytes > 0) return fail(LH_ERR_NULL, "%s: workspace is NULL but workspace_bytes > 0", fn);
+  if (!aligned(a.x, elem_size(a.x_dtype)) || !aligned(a.y, elem_size(a.y_dtype)) || !aligned(a.packed, 8) ||
+      !aligned(a.gscale, 4) || !aligned(a.x_scale, 4) || !aligned(a.offsets, 8) || !aligned(a.ws, 256))
+    return fail(LH_ERR_ARG, "%s: misaligned pointer (packed_e2m1 needs 8 bytes, workspace 256)", fn);
+  if (work && a.ws != nullptr && a.ws_bytes < lh::linear_ws_bytes(a))
+    return fail(LH_ERR_WORKSPACE, "%s: workspace smaller than lh_linear_nvfp4_workspace_bytes()", fn);
+  if (!work) return LH_OK;
+  hipError_t e = lh::launch_linear(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+// The checks that the three row movers share: tok rows are tokens, row rows
+// are sorted assignments; need_*: which buffers the call reads or writes.
+lh_status check_moe_rows(const char* fn, const lh::MoeRowsArgs& a, const void* tok, int64_t ld_tok, const void* rows,
+                         int64_t ld_rows) {
+  if (!valid_dtype(a.dtype)) return fail(LH_ERR_DTYPE, "%s: dtype must be 0 (f32) or 1 (bf16)", fn);
+  if (a.n_tok < 0 || a.cols < 0 || a.top_k < 0 || a.n_rows < 0) return fail(LH_ERR_SHAPE, "%s: negative size", fn);
+  if (a.top_k > 0 && a.n_tok > 0x7fffffff / a.top_k)
+    return fail(LH_ERR_SHAPE, "%s: n_tokens * top_k must be below 2^31", fn);
+  if (a.n_rows < a.n_tok * a.top_k) return fail(LH_ERR_SHAPE, "%s: n_rows < n_tokens * top_k", fn);
+  if (ld_tok < a.cols || ld_rows < a.cols) return fail(LH_ERR_SHAPE, "%s: a leading dimension < cols", fn);
+  const bool work = a.n_tok > 0 && a.cols > 0;
+  if (work && (tok == nullptr || (a.top_k > 0 && (rows == nullptr || a.position == nullptr))))
+    return fail(LH_ERR_NULL, "%s: the tokens' and the experts' rows and position are required", fn);
+  const size_t e = elem_size(a.dtype);
+  if (!aligned(tok, e) || !aligned(rows, e) || !aligned(a.position, 4) || !aligned(a.weights, 4))
+    return fail(LH_ERR_ARG, "%s: pointer not aligned to its element size", fn);
+  return LH_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lh_status lh_linear_nvfp4(const void* x, int x_dtype, int64_t n_tokens, int64_t c_in, int64_t ld_x,
+                          int64_t group_stride_x, const uint8_t* packed_e2m1, const uint8_t* scale_e4m3,
+                          const float* global_scale, int64_t c_out, int64_t n_groups, const float* x_scale, void* y,
+                          int y_dtype, int64_t ld_y, int64_t group_stride_y, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  lh::LinearArgs a{false, false, x, x_dtype, n_tokens, ld_x, group_stride_x, nullptr, 0, n_groups, c_out, c_in,
+                   packed_e2m1, scale_e4m3, global_scale, x_scale, y, y_dtype, ld_y, group_stride_y, workspace,
+                   workspace_bytes};
+  return run_linear("lh_linear_nvfp4", a, c_in, c_out, stream);
+}
+
+lh_status lh_linear_nvfp4_grad(const void* dy, int dy_dtype, int64_t n_tokens, int64_t c_out, int64_t ld_dy,
+                               int64_t group_stride_dy, const uint8_t* packed_e2m1, const uint8_t* scale_e4m3,
+                               const float* global_scale, int64_t c_in, int64_t n_groups, void* dx, int dx_dtype,
+                               int64_t ld_dx, int64_t group_stride_dx, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  lh::LinearArgs a{true, false, dy, dy_dtype, n_tokens, ld_dy, group_stride_dy, nullptr, 0, n_groups, c_out, c_in,
+                   packed_e2m1, scale_e4m3, global_scale, nullptr, dx, dx_dtype, ld_dx, group_stride_dx, workspace,
+                   workspace_bytes};
+  return run_linear("lh_linear_nvfp4_grad", a, c_out, c_in, stream);
+}
+
+lh_status lh_linear_nvfp4_ragged(const void* x, int x_dtype, int64_t n_rows, int64_t c_in, int64_t ld_x,
+                                 const int64_t* token_offsets, int64_t n_groups, int64_t max_group_rows,
+                                 const uint8_t* packed_e2m1, const uint8_t* scale_e4m3, const float* global_scale,
+                                 int64_t c_out, const float* x_scale, void* y, int y_dtype, int64_t ld_y,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  lh::LinearArgs a{false, true, x, x_dtype, n_rows, ld_x, 0, token_offsets, max_group_rows, n_groups, c_out, c_in,
+                   packed_e2m1, scale_e4m3, global_scale, x_scale, y, y_dtype, ld_y, 0, workspace, workspace_bytes};
+  return run_linear("lh_linear_nvfp4_ragged", a, c_in, c_out, stream);
+}
+
+lh_status lh_linear_nvfp4_ragged_grad(const void* dy, int dy_dtype, int64_t n_rows, int64_t c_out, int64_t ld_dy,
+                                      const int64_t* token_offsets, int64_t n_groups, int64_t max_group_rows,
+                                      const uint8_t* packed_e2m1, const uint8_t* scale_e4m3,
+                                      const float* global_scale, int64_t c_in, void* dx, int dx_dtype, int64_t ld_dx,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  lh::LinearArgs a{true, true, dy, dy_dtype, n_rows, ld_dy, 0, token_offsets, max_group_rows, n_groups, c_out, c_in,
+                   packed_e2m1, scale_e4m3, global_scale, nullptr, dx, dx_dtype, ld_dx, 0, workspace,
+                   workspace_bytes};
+  return run_linear("lh_linear_nvfp4_ragged_grad", a, c_out, c_in, stream);
+}
+
+size_t lh_moe_sort_workspace_bytes(int64_t n_tokens, int64_t top_k, int64_t n_groups) {
+  if (n_tokens <= 0 || top_k <= 0 || n_groups <= 0 || n_groups > lh::kMoeMaxGroups || n_tokens > 0x7fffffff / top_k)
+    return 0;
+  return lh::moe_sort_ws_bytes(n_tokens * top_k, n_groups);
+}
+
+lh_status lh_moe_sort(const void* expert_ids, int ids_type, int64_t n_tokens, int64_t top_k, int64_t n_groups,
+                      int64_t* offsets, int32_t* position, int32_t* order, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  const char* fn = "lh_moe_sort";
+  g_msg[0] = '\0';
+  if (ids_type != LH_INDEX_I32 && ids_type != LH_INDEX_I64)
+    return fail(LH_ERR_DTYPE, "%s: ids_type must be 0 (int32) or 1 (int64)", fn);
+  if (n_tokens < 0 || top_k < 0 || n_groups < 0) return fail(LH_ERR_SHAPE, "%s: negative size", fn);
+  if (n_groups > lh::kMoeMaxGroups) return fail(LH_ERR_SHAPE, "%s: n_groups must be at most 1024", fn);
+  if (top_k > 0 && n_tokens > 0x7fffffff / top_k)
+    return fail(LH_ERR_SHAPE, "%s: n_tokens * top_k must be below 2^31", fn);
+  const int64_t n = n_tokens * top_k;
+  if (offsets == nullptr) return fail(LH_ERR_NULL, "%s: offsets is NULL", fn);
+  if (n > 0 && (expert_ids == nullptr || position == nullptr))
+    return fail(LH_ERR_NULL, "%s: expert_ids and position are required", fn);
+  if (workspace == nullptr && workspace_bytes > 0) return fail(LH_ERR_NULL, "%s: workspace is NULL but workspace_bytes > 0", fn);
+  if (!aligned(expert_ids, ids_type == LH_INDEX_I64 ? 8 : 4) || !aligned(offsets, 8) || !aligned(position, 4) ||
+      !aligned(order, 4) || !aligned(workspace, 4))
+    return fail(LH_ERR_ARG, "%s: pointer not aligned to its element size", fn);
+  if (n > 0 && workspace_bytes < lh::moe_sort_ws_bytes(n, n_groups))
+    return fail(LH_ERR_WORKSPACE, "%s: workspace smaller than lh_moe_sort_workspace_bytes()", fn);
+  lh::MoeSortArgs a{expert_ids, ids_type == LH_INDEX_I64, n, n_groups, offsets, order, position, workspace};
+  hipError_t e = lh::launch_moe_sort(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+lh_status lh_moe_dispatch(const void* x, int dtype, int64_t n_tokens, int64_t cols, int64_t ld_x,
+                          const int32_t* position, int64_t top_k, void* xs, int64_t n_rows, int64_t ld_xs,
+                          void* stream) {
+  const char* fn = "lh_moe_dispatch";
+  g_msg[0] = '\0';
+  lh::MoeRowsArgs a{dtype, x, ld_x, nullptr, 0, n_rows, n_tokens, cols, top_k, position, nullptr, xs, ld_xs, nullptr};
+  const lh_status st = check_moe_rows(fn, a, x, ld_x, xs, ld_xs);
+  if (st != LH_OK) return st;
+  if (n_tokens == 0 || cols == 0 || top_k == 0) return LH_OK;
+  hipError_t e = lh::launch_moe_dispatch(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+lh_status lh_moe_combine(const void* ys, int dtype, int64_t n_rows, int64_t cols, int64_t ld_ys,
+                         const int32_t* position, const float* weights, int64_t n_tokens, int64_t top_k, void* y,
+                         int64_t ld_y, void* stream) {
+  const char* fn = "lh_moe_combine";
+  g_msg[0] = '\0';
+  lh::MoeRowsArgs a{dtype, nullptr, 0, ys, ld_ys, n_rows, n_tokens, cols, top_k, position, weights, y, ld_y, nullptr};
+  const lh_status st = check_moe_rows(fn, a, y, ld_y, ys, ld_ys);
+  if (st != LH_OK) return st;
+  if (n_tokens == 0 || cols == 0) return LH_OK;
+  hipError_t e = lh::launch_moe_combine(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+lh_status lh_moe_combine_grad(const void* dy, int dtype, int64_t n_tokens, int64_t cols, int64_t ld_dy, const void* ys,
+                              int64_t n_rows, int64_t ld_ys, const int32_t* position, int64_t top_k,
+                              const float* weights, void* dys, int64_t ld_dys, float* dweights, void* stream) {
+  const char* fn = "lh_moe_combine_grad";
+  g_msg[0] = '\0';
+  if (dys == nullptr && dweights == nullptr) return fail(LH_ERR_ARG, "%s: no output requested", fn);
+  lh::MoeRowsArgs a{dtype, dy, ld_dy, ys, ld_ys, n_rows, n_tokens, cols, top_k, position, weights, dys, ld_dys,
+                    dweights};
+  lh_status st = LH_OK;
+  if (dys) st = check_moe_rows(fn, a, dy, ld_dy, dys, ld_dys);
+  if (st == LH_OK && dweights) st = check_moe_rows(fn, a, dy, ld_dy, ys, ld_ys);
+  if (st != LH_OK) return st;
+  if (!aligned(dweights, 4)) return fail(LH_ERR_ARG, "%s: pointer not aligned to its element size", fn);
+  if (n_tokens == 0 || top_k == 0) return LH_OK;
+  hipError_t e = lh::launch_moe_combine_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
 }  // extern "C"
 
 // ---------------------------------------------------------------------------

@@ -199,4 +199,74 @@ struct GptqQuantizeArgs {
 size_t gptq_quantize_ws_bytes(int64_t c_out, int64_t c_in);
 hipError_t launch_gptq_quantize(const GptqQuantizeArgs& a, hipStream_t stream);
 
+struct QuantizeArgs {
+  const void* x;          // [n_groups][rows][ld]
+  int dtype;
+  int64_t rows, c_in, ld, n_groups, gstride;
+  const float* amax;      // [n_groups]
+  void* values;           // nullable: r c, dense, v_dtype
+  int v_dtype;
+  uint8_t* packed;        // nullable
+  uint8_t* codes;         // nullable
+  float* gscale;          // nullable
+};
+hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t stream);
+
+// Products with NVFP4 weights [n_groups][c_out][c_in].  grad false: rows of x
+// [c_in] to rows of y [c_out]; grad true: rows of x = dy [c_out] to rows of
+// y = dx [c_in].
+struct LinearArgs {
+  bool grad;
+  bool ragged;
+  const void* x;
+  int x_dtype;
+  int64_t rows, ld_x, gstride_x;
+  const int64_t* offsets;  // ragged: device [n_groups + 1]
+  int64_t max_group_rows;  // ragged: host bound on any group's rows (0: unknown)
+  int64_t n_groups, c_out, c_in;
+  const uint8_t* packed;
+  const uint8_t* codes;
+  const float* gscale;     // [n_groups]
+  const float* x_scale;    // nullable [n_groups]
+  void* y;
+  int y_dtype;
+  int64_t ld_y, gstride_y;
+  void* ws;                // nullable
+  size_t ws_bytes;
+};
+size_t linear_ws_bytes(const LinearArgs& a);  // of the sizes and types alone
+hipError_t launch_linear(const LinearArgs& a, hipStream_t stream);
+
+constexpr int64_t kMoeMaxGroups = 1024;  // the sort's LDS counters
+struct MoeSortArgs {
+  const void* ids;         // [n]
+  bool ids_i64;
+  int64_t n, n_groups;
+  int64_t* offsets;        // [n_groups + 1]
+  int* order;              // nullable [n]
+  int* position;           // [n]
+  void* ws;                // moe_sort_ws_bytes
+};
+size_t moe_sort_ws_bytes(int64_t n, int64_t n_groups);
+hipError_t launch_moe_sort(const MoeSortArgs& a, hipStream_t stream);
+
+// dispatch: tok -> rows_out; combine: rows -> rows_out; combine gradient:
+// tok (dy) and rows (ys) -> rows_out (dys) and dweights.
+struct MoeRowsArgs {
+  int dtype;
+  const void* tok;         // [n_tok][ld_tok]
+  int64_t ld_tok;
+  const void* rows;        // [n_rows][ld_rows]
+  int64_t ld_rows, n_rows;
+  int64_t n_tok, cols, top_k;
+  const int* position;     // [n_tok][top_k]
+  const float* weights;    // nullable [n_tok][top_k]
+  void* rows_out;
+  int64_t ld_out;
+  float* dweights;         // nullable [n_tok][top_k]
+};
+hipError_t launch_moe_dispatch(const MoeRowsArgs& a, hipStream_t stream);
+hipError_t launch_moe_combine(const MoeRowsArgs& a, hipStream_t stream);
+hipError_t launch_moe_combine_grad(const MoeRowsArgs& a, hipStream_t stream);
+
 }  // namespace lh

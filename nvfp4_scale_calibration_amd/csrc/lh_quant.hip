@@ -7,11 +7,11 @@
 //     into [-6, 6]; max scaling takes the block's largest |w|.
 //   "Algorithm principle": Q(W, s) = Cast(W / s) * s; the kernel receives the
 //     global FP32 amax; candidate scales are bit-consistent with fake-quant.
-// Both kernels are HBM-bound streaming passes.
+// All kernels here are HBM-bound streaming passes.
 #include <math.h>
 
-#include "lh_device.h"
 #include "lh_internal.h"
+#include "lh_rows.h"
 
 namespace lh {
 namespace {
@@ -131,6 +131,104 @@ hipError_t launch_fq_typed(const FakeQuantArgs& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
+// Activations to NVFP4 in one pass: per 16-value block the max rule's scale
+// t = fl32(fl32(a / 6) / S_g) as the nearest positive E4M3 value c, then the
+// cast of fake_quant_kernel with s = fl32(c S_g), bit for bit what
+// lh_select_scales (max) followed by lh_fake_quant_nvfp4 writes.  The values
+// leave as r c, in units of S_g, which bf16 and fp32 both hold exactly.
+// A lane takes 16 bytes (8 bf16 or 4 fp32 values), so two or four
+// neighbouring lanes share a block and find its maximum by xor shuffles;
+// every load and store instruction covers consecutive bytes of the wave.
+// ---------------------------------------------------------------------------
+template <typename T, typename TV>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, int64_t rows, int64_t cols, int64_t ld) {
+  constexpr int kE = 16 / sizeof(T);   // values per lane
+  constexpr int kP = kBlock / kE;      // lanes per block
+  const int64_t vecs = cols / kE;      // lanes' shares per row; a multiple of kP
+  const T* x = static_cast<const T*>(a.x);
+  TV* values = static_cast<TV*>(a.values);
+  for (int64_t g = blockIdx.z; g < a.n_groups; g += gridDim.z) {
+    const float Sg = a.amax[g] / kAmaxDivisor;
+    if (a.gscale && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.gscale[g] = Sg;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+      for (int64_t v = (int64_t)blockIdx.x * kThreads + threadIdx.x; v < vecs; v += (int64_t)gridDim.x * kThreads) {
+        const uint4 raw = load_u128(x + g * a.gstride + r * ld + v * kE);
+        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+        float w[kE];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kE == 8) {
+            w[2 * i] = __uint_as_float(in[i] << 16);
+            w[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
+          } else {
+            w[i] = __uint_as_float(in[i]);
+          }
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(w[i]));
+#pragma unroll
+        for (int off = 1; off < kP; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+        // the nearest positive E4M3 value (ties to even): clamped below the
+        // conversion's overflow, and never the zero code
+        const float t = fminf((m / 6.0f) / Sg, 448.0f);
+        uint32_t code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, t, 0, false) & 0x7fu;
+        code = (Sg > 0.0f && code > 0u) ? code : 1u;
+        const float c = e4m3_to_f32<0>(code);
+        const float s = c * Sg;
+        float q[kE];
+#pragma unroll
+        for (int i = 0; i < kE; ++i) q[i] = (s == 0.0f) ? 0.0f : w[i] / s;  // IEEE division
+        uint32_t pk = 0u;
+        pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[0], q[1], 1.0f, 0);
+        pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[2], q[3], 1.0f, 1);
+        if constexpr (kE == 8) {
+          pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[4], q[5], 1.0f, 2);
+          pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[6], q[7], 1.0f, 3);
+        }
+        const uint32_t nz = (pk | (pk >> 1) | (pk >> 2)) & 0x11111111u;  // -0 is written as +0
+        pk &= 0x77777777u | (nz << 3);
+        const int64_t at = (g * rows + r) * vecs + v;  // dense outputs
+        if (values) {
+          float u[8];
+          units8(pk, c, u);
+          if constexpr (sizeof(TV) == 2 && kE == 8) {
+            const uint32_t b[4] = {pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]),
+                                   pack_bf16(u[6], u[7])};
+            __builtin_memcpy(values + at * kE, b, 16);
+          } else if constexpr (sizeof(TV) == 2) {
+            const uint32_t b[2] = {pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])};
+            __builtin_memcpy(values + at * kE, b, 8);
+          } else {
+            __builtin_memcpy(values + at * kE, u, 4 * kE);
+          }
+        }
+        if (a.packed) {
+          if constexpr (kE == 8) *reinterpret_cast<uint32_t*>(a.packed + 4 * at) = pk;
+          else *reinterpret_cast<uint16_t*>(a.packed + 2 * at) = (uint16_t)pk;
+        }
+        if (a.codes && (v & (kP - 1)) == 0) a.codes[at / kP] = (uint8_t)code;
+      }
+    }
+  }
+}
+
+template <typename T, typename TV>
+hipError_t launch_quantize_typed(const QuantizeArgs& a, hipStream_t stream) {
+  int64_t rows = a.rows, cols = a.c_in;
+  if (a.ld == a.c_in || rows == 1) {  // a group is one flat row
+    cols *= rows;
+    rows = 1;
+  }
+  const int64_t per = kThreads * (16 / (int64_t)sizeof(T));
+  const int64_t gx = (cols + per - 1) / per;
+  const dim3 grid((unsigned)(gx < 1 ? 1 : gx > (1 << 20) ? (1 << 20) : gx), (unsigned)(rows < 1 ? 1 : rows > 65535 ? 65535 : rows),
+                  (unsigned)(a.n_groups > 65535 ? 65535 : a.n_groups));
+  quantize_kernel<T, TV><<<grid, dim3(kThreads), 0, stream>>>(a, rows, cols, a.ld);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
 // Global amax: |w| as fp32 bits is monotone in |w|, so the reduction is an
 // unsigned max; each workgroup folds its rows, then one atomicMax per
 // workgroup into the zero-initialised output (order-independent, exact).
@@ -219,6 +317,14 @@ hipError_t launch_fake_quant(const FakeQuantArgs& a, hipStream_t stream) {
   if (a.dtype == 1)
     return aligned ? launch_fq_typed<uint16_t, true>(a, stream) : launch_fq_typed<uint16_t, false>(a, stream);
   return aligned ? launch_fq_typed<float, true>(a, stream) : launch_fq_typed<float, false>(a, stream);
+}
+
+hipError_t launch_quantize(const QuantizeArgs& a, hipStream_t stream) {
+  if (a.dtype == 1)
+    return a.v_dtype == 1 ? launch_quantize_typed<uint16_t, uint16_t>(a, stream)
+                          : launch_quantize_typed<uint16_t, float>(a, stream);
+  return a.v_dtype == 1 ? launch_quantize_typed<float, uint16_t>(a, stream)
+                        : launch_quantize_typed<float, float>(a, stream);
 }
 
 hipError_t launch_absmax(const AbsmaxArgs& a, hipStream_t stream) {

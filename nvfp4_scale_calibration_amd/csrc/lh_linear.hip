@@ -16,11 +16,43 @@
 // MFMA orientation: operand A = weights (rows = outputs), operand B =
 // activations (columns = tokens), so that a lane's accumulators are
 // consecutive outputs of one token and leave in one store.
+#include <math.h>
+
+#include <utility>
+
 #include "lh_internal.h"
 #include "lh_rows.h"
 
 namespace lh {
 namespace {
+
+// f(integral_constant 0), ..., f(integral_constant N - 1): a loop whose index
+// is a constant for the front end, so that what it indexes is never memory.
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// f(0) && ... && f(N - 1), up to the first false.
+template <typename F, int... I>
+__device__ __forceinline__ bool static_all_impl(F&& f, std::integer_sequence<int, I...>) {
+  return (f(std::integral_constant<int, I>{}) && ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ bool static_all(F&& f) {
+  return static_all_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// A wave-uniform value into scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
 
 // Rows [row0, row1) of group g that tile `t` of the ragged rows covers, with
 // kBT rows per tile and tiles counted group by group; false past the last
@@ -48,9 +80,9 @@ __device__ __forceinline__ bool ragged_tile(const int64_t* __restrict__ offsets,
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
       const int64_t first = before + __shfl(incl - tiles, l);
-      g = g0 + l;
-      row0 = __shfl(a, l) + (t - first) * kBT;
-      row1 = min(row0 + kBT, __shfl(b, l));
+      g = uniform(g0 + l);
+      row0 = uniform(__shfl(a, l) + (t - first) * kBT);
+      row1 = uniform(min(row0 + kBT, (int64_t)__shfl(b, l)));
       return true;
     }
     before += __shfl(incl, 63);
@@ -247,6 +279,509 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
   }
 }
 
+// ---------------------------------------------------------------------------
+// The large product: kNT * 32 tokens x 256 outputs per workgroup of four
+// waves, one wave per SIMD for kNT = 8.
+//
+// Each wave owns 64 outputs alone (2 x kNT tiles of v_mfma_f32_32x32x16_bf16,
+// 32 kNT accumulators per lane), so every weight is decoded once per
+// workgroup, in registers, straight into the MFMA operand: the packed bytes
+// never pass through LDS.  The contraction index may be walked in any order
+// as long as both operands agree: in a chunk of 128 weights of a row, the
+// lanes of half h (l / 32) take weights 64 h .. 64 h + 63, two 16-byte loads,
+// and MFMA step i (of 8) takes weights 64 h + 8 i ..  + 7 of both halves.
+//
+// Activations come through LDS, one chunk of 256 bytes a token in each of two
+// buffers, filled by direct global -> LDS loads (16 bytes a lane, four tokens
+// an instruction, whole lines).  Slot q ^ (token & 15) holds 16-byte piece q,
+// so that the 16 lanes which LDS serves together read one piece of 16 tokens
+// from distinct banks.
+//
+// Per step a wave issues 2 kNT MFMAs, and between them reads the next step's
+// kNT activation operands, decodes its two weight operands (32 vector
+// operations) and issues its share of the next chunk's loads: with one wave
+// per SIMD the matrix pipe is covered only by what is interleaved by hand
+// (sched_barrier keeps each group where it is written).  The barrier of a
+// chunk stands before its last step, whose operands are in registers by then,
+// so that step's MFMAs cover the first reads of the next chunk.
+// ---------------------------------------------------------------------------
+constexpr int kChunk = 128;   // contraction elements per chunk
+
+struct BigArgs {
+  LinearArgs a;
+  const uint16_t* x;       // bf16 rows, 16-byte aligned, a multiple of kChunk elements each
+  int64_t ld, gstride;
+  int chunks, w_chunks;    // chunks of x per row (1 or 3 planes) and of a weight row
+  int64_t m_tiles, t_tiles;  // output tiles, token tiles (all groups)
+  int splits;              // > 1: workgroups per tile, each over its share of the chunks, into part
+  float* part;             // [splits][n_groups * rows][c_out]
+};
+
+// Workgroups go to the 8 XCDs in turn, and each XCD has its own L2.  Dense
+// rows: the tiles are dealt so that an XCD works through a run of neighbours,
+// walked in columns of 8 output tiles.  Ragged rows: how many token tiles
+// there are is known on the device alone, so an XCD takes every eighth token
+// tile with all its outputs (the tiles past the last one then spread evenly;
+// t_tiles is a multiple of 8).
+__device__ __forceinline__ void big_tile(int64_t b, const BigArgs& a, int64_t& tile, int64_t& mt) {
+  if (a.a.ragged) {
+    const int64_t q = b / 8;
+    tile = q / a.m_tiles * 8 + b % 8;
+    mt = q % a.m_tiles;
+    return;
+  }
+  const int64_t tiles = a.t_tiles * a.m_tiles;
+  const int64_t per = tiles / 8, rest = tiles % 8, xcd = b % 8;
+  const int64_t t = xcd * per + min(xcd, rest) + b / 8;
+  const int64_t col = t / (8 * a.t_tiles), in = t - col * 8 * a.t_tiles;
+  const int64_t width = min((int64_t)8, a.m_tiles - 8 * col);
+  tile = in / width;
+  mt = 8 * col + in - tile * width;
+}
+
+// 16 bytes per lane from base + off straight into LDS (lane l at lds + 16 l);
+// the kernel waits with s_waitcnt vmcnt before the barrier that publishes the
+// data.  No register is written; M0 carries the LDS address.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+// A barrier that waits for this wave's LDS reads but for none of its loads
+// from global memory (which __syncthreads would drain).
+__device__ __forceinline__ void block_sync() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Weights 2 i, 2 i + 1 of the eight nibbles pk times c, as packed bf16.
+template <int i>
+__device__ __forceinline__ uint32_t units2(uint32_t pk, float c) {
+  const f32x2_t r = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(pk, 1.0f, i);
+  return pack_bf16(r.x * c, r.y * c);
+}
+
+// A lane's share of one weight row's chunk: 64 weights and their 4 codes.
+// kPart: the row may end inside the chunk; the share then goes on with other
+// weights of the row, finite values that meet the zeros behind the
+// activations' row.
+typedef uint32_t u32x8_t __attribute__((ext_vector_type(8)));
+struct RawW {
+  u32x8_t w;
+  uint32_t c;   // the four codes, or
+  uint4 c4;     // (kPart) one each
+  template <bool kPart, int i>
+  __device__ __forceinline__ float scale() const {
+    if constexpr (!kPart) return e4m3_to_f32<i>(c);
+    else return e4m3_to_f32<0>(i == 0 ? c4.x : i == 1 ? c4.y : i == 2 ? c4.z : c4.w);
+  }
+};
+template <bool kPart>
+__device__ __forceinline__ RawW load_raw(const uint8_t* row_q, const uint8_t* row_c, int64_t k, int64_t c_in) {
+  RawW r;
+  if constexpr (!kPart) {
+    const uint4 u = load_u128(row_q + k / 2), v = load_u128(row_q + k / 2 + 16);
+    r.w = u32x8_t{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    r.c = load_u32(row_c + k / 16);
+  } else {
+    uint32_t code[4];
+    static_for<4>([&](auto e) {
+      const int64_t at = k + 16 * e < c_in ? k + 16 * e : 0;
+      const uint2 v = load_u64(row_q + at / 2);
+      r.w[2 * e] = v.x;
+      r.w[2 * e + 1] = v.y;
+      code[e] = row_c[at / 16];
+    });
+    r.c4 = make_uint4(code[0], code[1], code[2], code[3]);
+  }
+  return r;
+}
+
+template <int kNT, int kRF, int kDepth, int kWaves, bool kPart>
+__global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b) {
+  constexpr int kBT = 32 * kNT;              // tokens
+  constexpr int kWM = 32 * kRF;              // outputs per wave
+  constexpr int kBuf = kBT * 256;            // bytes of an LDS buffer
+  constexpr int kBufs = kDepth + 1;
+  constexpr int kLoads = 2 * kNT;            // direct loads per wave and chunk
+  constexpr int kAhead = (kDepth - 1) * (kLoads + (kPart ? 8 : 3) * kRF);  // loads issued behind the next chunk's at its barrier
+  __shared__ __attribute__((aligned(1024))) uint8_t xs[kBufs * kBuf];
+  int64_t tile, mt;
+  big_tile(blockIdx.x, b, tile, mt);
+  Place p;
+  if (!place_of<kBT>(b.a, tile, p)) return;  // the whole workgroup
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t c_in = b.a.c_in, c_out = b.a.c_out;
+  const int64_t m0 = mt * 4 * kWM + kWM * wave;  // the wave's first output
+  // this workgroup's share of the chunks
+  const int c_first = (int)((int64_t)b.chunks * blockIdx.y / b.splits);
+  const int end = (int)((int64_t)b.chunks * (blockIdx.y + 1) / b.splits) - 1;  // its last one
+
+  // direct loads: instruction i of a wave fills tokens 4 (wave + 4 i) .. + 3
+  const int trow = 4 * wave + (lane >> 4);                 // token & 15
+  const uint32_t piece = (lane & 15) ^ trow;               // the piece that slot lane & 15 holds
+  const uint16_t* xg = b.x + uniform((b.a.ragged ? 0 : p.g * b.gstride) + p.row0 * b.ld);
+  const int last = (int)(p.row1 - p.row0) - 1;
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)min(trow + 16 * i, last) * (uint32_t)(b.ld * 2) + piece * 16;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)xs) + 1024 * wave;
+  auto dload = [&](int chunk, int buf, int i) {
+    dma16(xg + uniform((int64_t)chunk * kChunk), off[i], lds0 + buf * kBuf + i * 4096);
+  };
+
+  // weights: row 32 f + l32 of the wave's outputs (past the last one: the last)
+  const uint8_t* wq[kRF];
+  const uint8_t* wc[kRF];
+#pragma unroll
+  for (int f = 0; f < kRF; ++f) {
+    const int64_t o = p.g * c_out + min(m0 + 32 * f + l32, c_out - 1);
+    wq[f] = b.a.packed + o * (c_in / 2);
+    wc[f] = b.a.codes + o * (c_in / 16);
+  }
+  RawW ring[kBufs][kRF];  // this chunk's weights, the next ones'
+  auto wload = [&](auto d, int chunk) {
+    const int w = chunk % b.w_chunks;
+    static_for<kRF>([&](auto f) { ring[d][f] = load_raw<kPart>(wq[f], wc[f], (int64_t)w * kChunk + 64 * h, c_in); });
+  };
+
+  uint4 fa[2][kRF];
+  uint4 fb[2][kNT];
+  f32x16_t acc[kRF][kNT];
+#pragma unroll
+  for (int f = 0; f < kRF; ++f)
+#pragma unroll
+    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[f][t][e] = 0.0f;
+
+  // operand of step i, tokens 32 t + l32: piece 8 h + i of the token's buffer row
+  const uint32_t rd0 = l32 * 256 + (((8 * h) ^ (l32 & 15)) * 16);
+  auto bread = [&](auto set, uint32_t rd, auto i, auto t) {
+    fb[set][t] = *reinterpret_cast<const uint4*>(xs + (rd ^ (16 * i)) + 8192 * t);
+  };
+  // pair e (of 4) of weight operand f for step s of the chunk in ring slot u (8: the next chunk's first step)
+  auto decode = [&](auto set, auto u, auto s, auto f, auto e) {
+    constexpr int i = s & 7;
+    const RawW& r = ring[(u + (s >> 3)) % kBufs][f];
+    const uint32_t v = units2<e>(r.w[i], r.template scale<kPart, (i >> 1)>());
+    if constexpr (e == 0) fa[set][f].x = v;
+    else if constexpr (e == 1) fa[set][f].y = v;
+    else if constexpr (e == 2) fa[set][f].z = v;
+    else fa[set][f].w = v;
+  };
+  // Step s of the chunk in slot u: the MFMAs of operand set s & 1; between
+  // them the operands of step s + 1 (LDS row address rd) and the direct loads
+  // d0 .. d1 - 1 of chunk dst into buffer dbuf.
+  auto step = [&](auto u, auto s, uint32_t rd, int dst, int dbuf, auto d0, auto d1) {
+    constexpr int set = s & 1;
+    static_for<kRF * kNT>([&](auto N) {
+      constexpr int n = N;
+      if constexpr (n % 4 == 0 && d0 + n / 4 < d1) dload(dst, dbuf, d0 + n / 4);
+      if constexpr (kRF * kNT < 4 && n == 1 && d0 + 1 < d1) dload(dst, dbuf, d0 + 1);
+      if constexpr (n < kNT)
+        bread(std::integral_constant<int, set ^ 1>{}, rd, std::integral_constant<int, (s + 1) & 7>{}, N);
+      constexpr int per = 4 / kNT > 0 ? 4 / kNT : 1;  // pairs per MFMA (kNT = 8: every other one)
+      if constexpr (kNT < 8 || n % 2 == 0)
+        static_for<per>([&](auto E) {
+          constexpr int k = kNT < 8 ? n * per + E : n / 2;  // of 4 kRF pairs
+          decode(std::integral_constant<int, set ^ 1>{}, u, std::integral_constant<int, s + 1>{},
+                 std::integral_constant<int, (k >> 2)>{}, std::integral_constant<int, (k & 3)>{});
+        });
+      constexpr int f = n / kNT, t = n % kNT;
+      acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[set][f]),
+                                                          __builtin_bit_cast(bf16x8_t, fb[set][t]), acc[f][t], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  // Chunk c sits in buffer (c - c_first) % kBufs and is loaded kDepth chunks
+  // ahead, in four steps: the last step of chunk c - kBufs (whose buffer it
+  // takes: that chunk's last reads precede the barrier before its last step)
+  // and the first three of the chunk after that.  Past the end the final
+  // chunk is loaded again, into buffers that are read no more, so that no
+  // branch breaks the schedule and the counted waits hold.
+  static_for<kDepth>([&](auto d) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) dload(min(c_first + d, end), d, i);
+    wload(d, min(c_first + d, end));
+  });
+#pragma unroll
+  for (int i = 0; i < kLoads / 4; ++i) dload(min(c_first + kDepth, end), kDepth, i);
+  wait_loads<0>();
+  __syncthreads();
+  static_for<kNT>([&](auto t) {
+    bread(std::integral_constant<int, 0>{}, rd0, std::integral_constant<int, 0>{}, t);
+  });
+  static_for<4 * kRF>([&](auto K) {
+    decode(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{},
+           std::integral_constant<int, (K >> 2)>{}, std::integral_constant<int, (K & 3)>{});
+  });
+  // chunk c, its weights in ring slot u and its activations in LDS buffer
+  // buf; returns whether another one follows
+  auto chunk = [&](auto u, int c, int buf) {
+    const int dst1 = min(c + kDepth, end), dst2 = min(c + kDepth + 1, end);
+    const int nbuf = buf + 1 == kBufs ? 0 : buf + 1, pbuf = buf == 0 ? kBufs - 1 : buf - 1;
+    const uint32_t rd = rd0 + buf * kBuf, rd_next = rd0 + nbuf * kBuf;
+    wload(std::integral_constant<int, (u + kDepth) % kBufs>{}, dst1);
+    static_for<7>([&](auto s) {
+      constexpr int q0 = s < 3 ? (s + 1) * kLoads / 4 : 0, q1 = s < 3 ? (s + 2) * kLoads / 4 : 0;
+      step(u, s, rd, dst1, pbuf, std::integral_constant<int, q0>{}, std::integral_constant<int, q1>{});
+    });
+    wait_loads<kAhead>();  // the next chunk has landed; this one's last operands are in registers
+    block_sync();
+    step(u, std::integral_constant<int, 7>{}, rd_next, dst2, buf, std::integral_constant<int, 0>{},
+         std::integral_constant<int, kLoads / 4>{});
+    return c < end;
+  };
+  if constexpr (kDepth == 1) {
+    int buf = 0;
+    for (int c = c_first; c <= end; ++c) {
+      chunk(std::integral_constant<int, 0>{}, c, buf);
+      static_for<kRF>([&](auto f) { ring[0][f] = ring[1][f]; });  // loaded a chunk ago
+      buf ^= 1;
+    }
+  } else {
+    // the ring turns by unrolling: to copy a register that a load has yet to
+    // fill would wait for that load
+    for (int c = c_first; static_all<kBufs>([&](auto u) { return chunk(u, c + u, u); }); c += kBufs) {
+    }
+  }
+  wait_loads<0>();  // the repeated loads: nothing lands after the workgroup has ended
+
+  const float sc = out_scale(b.a, p.g);
+  float* part = b.splits > 1 ? b.part + (blockIdx.y * b.a.n_groups + p.g) * b.a.rows * c_out : nullptr;
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+    const int64_t tok = p.row0 + 32 * t + l32;
+    if (tok >= p.row1) continue;
+#pragma unroll
+    for (int f = 0; f < kRF; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t o = m0 + 32 * f + 8 * q + 4 * h;
+        if (o >= c_out) continue;
+        const float v[4] = {sc * acc[f][t][4 * q], sc * acc[f][t][4 * q + 1], sc * acc[f][t][4 * q + 2],
+                            sc * acc[f][t][4 * q + 3]};
+        if (part) store4(part + tok * c_out + o, c_out - o, v);
+        else if (b.a.y_dtype == 1) store4(reinterpret_cast<uint16_t*>(p.y) + tok * b.a.ld_y + o, c_out - o, v);
+        else store4(reinterpret_cast<float*>(p.y) + tok * b.a.ld_y + o, c_out - o, v);
+      }
+  }
+}
+
+// y = the splits' sums, added in split order.
+template <typename TY>
+__global__ __launch_bounds__(kThreads) void split_sum_kernel(const float* __restrict__ part, int splits, int64_t rows,
+                                                             int64_t n_groups, int64_t cols, TY* __restrict__ y,
+                                                             int64_t ld_y, int64_t gstride_y) {
+  const int64_t vecs = (cols + 3) / 4;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t r = i / vecs, c = 4 * (i - r * vecs);
+  if (r >= rows * n_groups) return;
+  const int64_t n = cols - c, step = n_groups * rows * cols;
+  const float* p = part + r * cols + c;
+  float v[4] = {};
+  for (int s = 0; s < splits; ++s, p += step) {
+    float u[4] = {};
+    if (n >= 4) {
+      __builtin_memcpy(u, p, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) u[e] = p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = s == 0 ? u[e] : v[e] + u[e];
+  }
+  const int64_t g = r / rows;
+  store4(y + g * gstride_y + (r - g * rows) * ld_y + c, n, v);
+}
+
+// Rows of any alignment and length to bf16 rows of kp elements (zeros past
+// k), fp32 as three planes of kp elements behind each other: the sum over
+// all 3 kp of them, with the weights walked three times, is the product.
+template <typename TX>
+__global__ __launch_bounds__(kThreads) void pack_rows_kernel(const TX* __restrict__ x, int64_t rows, int64_t k,
+                                                             int64_t ld, int64_t n_groups, int64_t gstride, int64_t kp,
+                                                             uint16_t* __restrict__ out) {
+  constexpr int kPlanes = sizeof(TX) == 4 ? 3 : 1;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t vecs = kp / 8, r = i / vecs, c = 8 * (i - r * vecs);
+  if (r >= rows * n_groups) return;
+  const int64_t g = r / rows;
+  const TX* p = x + g * gstride + (r - g * rows) * ld + c;
+  TX v[8] = {};
+  if (c + 8 <= k) {
+    __builtin_memcpy(v, p, 8 * sizeof(TX));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < k) v[e] = p[e];
+  }
+  uint4* d = reinterpret_cast<uint4*>(out + r * kPlanes * kp + c);
+  if constexpr (kPlanes == 1) {
+    uint4 o;
+    __builtin_memcpy(&o, v, 16);
+    *d = o;
+  } else {
+    uint32_t b[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split3(v[2 * e], v[2 * e + 1], b[e]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) d[q * (kp / 8)] = make_uint4(b[0][q], b[1][q], b[2][q], b[3][q]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// A few tokens (decoding): kTok tokens x kRows outputs per wave, no matrix
+// cores.  The packed weights are read once and everything else is made small
+// against them: lane l takes weights 32 l .. 32 l + 31 of a 2048-weight span
+// of each row (one 16-byte load, consecutive over the wave), keeps the same
+// span of the activations in registers for all its rows, and multiplies in
+// pairs: E2M1 values are exact in bf16, so v_dot2_f32_bf16 adds two exact
+// products to an fp32 sum, and the E4M3 scale multiplies the 16-weight sums,
+// not the weights (1.1 vector operations per weight and token, against 2 to
+// build an MFMA operand).  fp32 activations take fused multiply-adds instead.
+// The lanes' sums are added by xor shuffles at the end, in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int kSpan = 2048;
+
+// Sums over the wave of kN values (a power of two): lane l gets the sum of
+// value l / (64 / kN).  Each of the first steps exchanges half of the values
+// with the other half of the lanes, so 2 kN shuffles do instead of 6 kN.
+template <int kN>
+__device__ __forceinline__ float wave_sums(float (&v)[kN]) {
+  const int lane = threadIdx.x & 63;
+  static_for<6>([&](auto S) {
+    constexpr int off = 32 >> S, live = kN >> S;  // values a lane still carries
+    if constexpr (live > 1) {
+      const bool upper = (lane & off) != 0;
+#pragma unroll
+      for (int i = 0; i < live / 2; ++i) {
+        const float give = upper ? v[i] : v[i + live / 2], keep = upper ? v[i + live / 2] : v[i];
+        v[i] = keep + __shfl_xor(give, off);
+      }
+    } else {
+      v[0] += __shfl_xor(v[0], off);
+    }
+  });
+  return v[0];
+}
+
+template <int i>
+__device__ __forceinline__ bf16x2_t nibbles2(uint32_t pk) {
+  return __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(pk, 1.0f, i);
+}
+
+template <int kTok, int kRows, typename TX, typename TY>
+__global__ __launch_bounds__(kThreads) void linear_few_kernel(LinearArgs a, int64_t row_groups) {
+  constexpr bool kBf16 = sizeof(TX) == 2;
+  constexpr int kXw = kBf16 ? 16 : 32;  // 32-bit words of a lane's 32 activations
+  const int64_t tile = blockIdx.x / row_groups;
+  const int lane = threadIdx.x & 63;
+  Place p;
+  if (!place_of<kTok>(a, tile, p)) return;  // the whole workgroup
+  const int64_t o0 = ((blockIdx.x - tile * row_groups) * (kThreads / 64) + (threadIdx.x >> 6)) * kRows;
+  if (o0 >= a.c_out) return;                // the whole wave (no barrier follows)
+  const uint8_t* wq = a.packed + p.g * a.c_out * (a.c_in / 2) + 16 * lane;
+  const uint8_t* wc = a.codes + p.g * a.c_out * (a.c_in / 16) + 2 * lane;
+  const TX* x = reinterpret_cast<const TX*>(p.x) + 32 * lane;
+
+  struct Span {
+    uint4 w[kRows];
+    uint32_t c[kRows];
+  };
+  const int64_t spans = (a.c_in + kSpan - 1) / kSpan;
+  auto wload = [&](int64_t s) {
+    Span v;
+    const int64_t n = a.c_in - s * kSpan - 32 * lane;  // a multiple of 16
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int64_t o = min(o0 + r, a.c_out - 1);
+      const uint8_t* q = wq + o * (a.c_in / 2) + s * (kSpan / 2);
+      const uint8_t* c = wc + o * (a.c_in / 16) + s * (kSpan / 16);
+      v.w[r] = make_uint4(0u, 0u, 0u, 0u);
+      v.c[r] = 0;
+      if (n >= 32) {
+        v.w[r] = load_u128(q);
+        uint16_t h;
+        __builtin_memcpy(&h, c, 2);
+        v.c[r] = h;
+      } else if (n >= 16) {
+        const uint2 u = load_u64(q);
+        v.w[r].x = u.x;
+        v.w[r].y = u.y;
+        v.c[r] = c[0];
+      }
+    }
+    return v;
+  };
+
+  float acc[kRows * kTok] = {};
+  Span cur = wload(0);
+  for (int64_t s = 0; s < spans; ++s) {
+    uint32_t xv[kTok][kXw];
+    const int64_t n = a.c_in - s * kSpan - 32 * lane;
+#pragma unroll
+    for (int t = 0; t < kTok; ++t) {
+      const TX* xp = x + min(p.row0 + t, p.row1 - 1) * a.ld_x + s * kSpan;
+#pragma unroll
+      for (int q = 0; q < kXw / 4; ++q) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (n >= (q + 1) * (kBf16 ? 8 : 4)) u = load_u128(xp + q * (kBf16 ? 8 : 4));
+        xv[t][4 * q] = u.x; xv[t][4 * q + 1] = u.y; xv[t][4 * q + 2] = u.z; xv[t][4 * q + 3] = u.w;
+      }
+    }
+    const Span next = wload(min(s + 1, spans - 1));
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t w[4] = {cur.w[r].x, cur.w[r].y, cur.w[r].z, cur.w[r].w};
+      const float c[2] = {e4m3_to_f32<0>(cur.c[r]), e4m3_to_f32<1>(cur.c[r])};
+      static_for<2>([&](auto B) {  // the lane's two blocks
+        float sum[kTok] = {};
+        static_for<2>([&](auto D) {
+          constexpr int d = 2 * B + D;  // word of eight weights
+          static_for<4>([&](auto P) {
+            if constexpr (kBf16) {
+              const bf16x2_t u = nibbles2<P>(w[d]);
+#pragma unroll
+              for (int t = 0; t < kTok; ++t)
+                sum[t] = __builtin_amdgcn_fdot2_f32_bf16(u, __builtin_bit_cast(bf16x2_t, xv[t][4 * d + P]), sum[t],
+                                                         false);
+            } else {
+              const f32x2_t u = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[d], 1.0f, P);
+#pragma unroll
+              for (int t = 0; t < kTok; ++t) {
+                sum[t] = __builtin_fmaf(u.x, __uint_as_float(xv[t][8 * d + 2 * P]), sum[t]);
+                sum[t] = __builtin_fmaf(u.y, __uint_as_float(xv[t][8 * d + 2 * P + 1]), sum[t]);
+              }
+            }
+          });
+        });
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) acc[r * kTok + t] = __builtin_fmaf(c[B], sum[t], acc[r * kTok + t]);
+      });
+    }
+    cur = next;
+  }
+  const float v = wave_sums(acc) * out_scale(a, p.g);
+  constexpr int kShare = 64 / (kRows * kTok);  // lanes that hold the same sum
+  const int r = lane / kShare / kTok, t = lane / kShare % kTok;
+  if (lane % kShare == 0 && o0 + r < a.c_out && p.row0 + t < p.row1) {
+    TY* y = reinterpret_cast<TY*>(p.y) + (p.row0 + t) * a.ld_y + o0 + r;
+    if constexpr (sizeof(TY) == 2) *y = f32_to_bf16_bits(v);
+    else *y = v;
+  }
+}
+
 // Tiles of kBT tokens the grid needs: exact for dense rows, an upper bound
 // for ragged ones (a group of n rows has n / kBT full tiles and at most one more).
 int64_t token_tiles(const LinearArgs& a, int64_t bt) {
@@ -268,14 +803,191 @@ hipError_t launch_x(const LinearArgs& a, hipStream_t stream) {
   return a.y_dtype == 1 ? launch_tile<kGrad, TX, uint16_t>(a, stream) : launch_tile<kGrad, TX, float>(a, stream);
 }
 
+// ---------------------------------------------------------------------------
+// Which kernel, from sizes and types alone.
+// ---------------------------------------------------------------------------
+struct Plan {
+  int few = 0;             // > 0: linear_few_kernel with that many tokens per wave
+  int nt = 0;              // > 0: linear_big_kernel<nt>
+  int splits = 1;
+  int64_t kp = 0;          // packed row length (one plane), chunks * kChunk / planes
+  bool pack = false;       // x goes through pack_rows_kernel
+  size_t pack_bytes = 0, part_bytes = 0;
+};
+
+// Outputs of a workgroup of linear_big_kernel<nt>.
+int64_t big_m(int nt) { return nt >= 4 ? 256 : 128; }
+
+// Time of a launch of linear_big_kernel<nt> in microseconds, from what its
+// parts measured on MI355X: a chunk takes `one` with one workgroup on a CU
+// and `all` with as many as fit (`fit`), each workgroup starts and ends for
+// 3.5, and a split adds a launch and its partial sums' way to memory and back.
+// (4096 x 4096 weights, 512 tokens: nt 2 unsplit 27.9, in 2 parts 34.7, nt 4
+// in 4 parts 37.5; 128 tokens: nt 1 in 2 parts 18.6, nt 2 in 4 parts 19.9;
+// 8192 tokens on 12288 x 4096: nt 4 740, nt 8 757.)
+struct BigCost {
+  int nt, fit;
+  double one, all;
+};
+constexpr BigCost kBigCosts[] = {{8, 1, 3.9, 3.9}, {4, 2, 2.3, 3.85}, {2, 2, 0.85, 1.35}, {1, 4, 0.65, 1.6}};
+constexpr int kCUs = 256;
+
+double big_cost(const BigCost& k, double tiles, int64_t chunks, int splits, double part_values) {
+  const double groups = tiles * splits, slots = (double)kCUs * k.fit;
+  const double rounds = groups > slots ? groups / slots : 1.0;
+  const double load = groups >= slots ? 1.0 : groups > kCUs ? (groups - kCUs) / (slots - kCUs) : 0.0;
+  const double chunk = k.one + (k.all - k.one) * load;
+  // the last round is rarely full: half a workgroup's time more on average past the first round
+  const double turns = rounds > 1.0 ? (rounds < 4.0 ? ceil(rounds) : rounds + 0.5) : 1.0;
+  double t = turns * (3.5 + chunk * (double)((chunks + splits - 1) / splits));
+  if (splits > 1) t += 2.5 + splits * part_values * 8e-6 / 4.0;
+  return t;
+}
+
+Plan plan_of(const LinearArgs& a) {
+  Plan p;
+  if (a.rows <= 0 || a.c_in <= 0 || a.c_out <= 0) return p;
+  if (a.grad) return p;
+  // Up to four tokens: linear_few_kernel (5120 x 17408 weights, one token:
+  // 12.9 us against 30 for nt 1 in 8 parts; 12288 x 4096, four tokens: 13.1
+  // against 24).  Ragged rows of several experts: nt 1 from 64 rows on 64
+  // experts on (14.1 us against 17.2).
+  if (a.ragged ? a.rows <= 16 : a.rows <= 4) {
+    p.few = a.ragged || a.rows <= 1 ? 1 : a.rows <= 2 ? 2 : 4;
+    return p;
+  }
+  const int planes = a.x_dtype == 1 ? 1 : 3;
+  p.kp = (a.c_in + kChunk - 1) / kChunk * kChunk;
+  p.pack = planes == 3 || a.c_in % kChunk != 0;
+  const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups;
+  const int64_t chunks = planes * (p.kp / kChunk);
+  double best = 0.0;
+  for (const BigCost& k : kBigCosts) {
+    const int64_t bt = 32 * k.nt, m_tiles = (a.c_out + big_m(k.nt) - 1) / big_m(k.nt);
+    // ragged: about half of a tile more per group that has rows
+    const double used = (double)(a.n_groups < a.rows ? a.n_groups : a.rows);
+    const double t_tiles = a.ragged ? (double)a.rows / bt + 0.5 * used : (double)((a.rows + bt - 1) / bt * a.n_groups);
+    for (int splits = 1; splits <= (a.ragged ? 1 : 16) && splits <= chunks; splits *= 2) {
+      const double t = big_cost(k, t_tiles * m_tiles, chunks, splits, (double)all * a.c_out);
+      if (p.nt == 0 || t < best) {
+        best = t;
+        p.nt = k.nt;
+        p.splits = splits;
+      }
+    }
+  }
+  if (p.pack) p.pack_bytes = ((size_t)all * planes * p.kp * 2 + 255) / 256 * 256;
+  if (p.splits > 1) p.part_bytes = (size_t)p.splits * all * a.c_out * 4;
+  return p;
+}
+
+template <int kTok, int kRows, typename TX, typename TY>
+hipError_t launch_few_typed(const LinearArgs& a, hipStream_t stream) {
+  const int64_t per = kRows * (kThreads / 64);
+  const int64_t row_groups = (a.c_out + per - 1) / per;
+  linear_few_kernel<kTok, kRows, TX, TY><<<dim3((unsigned)(row_groups * token_tiles(a, kTok))), dim3(kThreads), 0,
+                                           stream>>>(a, row_groups);
+  return hipGetLastError();
+}
+// Rows per wave: two for one bf16 token (5120 x 17408: 12.9 us, four rows
+// 14.6), four where the activations in registers weigh more (two tokens,
+// 12288 x 4096: 9.6, two rows 10.5; one fp32 token: 11.8 and 15.2).
+template <int kTok, typename TX>
+hipError_t launch_few_y(const LinearArgs& a, hipStream_t stream) {
+  constexpr int kRows = kTok == 1 && sizeof(TX) == 2 ? 2 : 4;
+  return a.y_dtype == 1 ? launch_few_typed<kTok, kRows, TX, uint16_t>(a, stream)
+                        : launch_few_typed<kTok, kRows, TX, float>(a, stream);
+}
+template <int kTok>
+hipError_t launch_few_x(const LinearArgs& a, hipStream_t stream) {
+  return a.x_dtype == 1 ? launch_few_y<kTok, uint16_t>(a, stream) : launch_few_y<kTok, float>(a, stream);
+}
+hipError_t launch_few(const LinearArgs& a, int tok, hipStream_t stream) {
+  switch (tok) {
+    case 1: return launch_few_x<1>(a, stream);
+    case 2: return launch_few_x<2>(a, stream);
+    default: return launch_few_x<4>(a, stream);
+  }
+}
+
+template <int kNT, int kRF, int kDepth, int kWaves>
+hipError_t launch_big_nt(const BigArgs& b, hipStream_t stream) {
+  const dim3 grid((unsigned)(b.m_tiles * b.t_tiles), (unsigned)b.splits);
+  if (b.a.c_in % kChunk == 0)
+    linear_big_kernel<kNT, kRF, kDepth, kWaves, false><<<grid, dim3(kThreads), 0, stream>>>(b);
+  else
+    linear_big_kernel<kNT, kRF, kDepth, kWaves, true><<<grid, dim3(kThreads), 0, stream>>>(b);
+  return hipGetLastError();
+}
+
+
+hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
+  const int planes = a.x_dtype == 1 ? 1 : 3;
+  BigArgs b{};
+  b.a = a;
+  b.w_chunks = (int)(p.kp / kChunk);
+  b.chunks = planes * b.w_chunks;
+  b.splits = p.splits;
+  b.m_tiles = (a.c_out + big_m(p.nt) - 1) / big_m(p.nt);
+  b.t_tiles = token_tiles(a, 32 * p.nt);
+  if (a.ragged) b.t_tiles = (b.t_tiles + 7) / 8 * 8;
+  const int64_t groups = a.ragged ? 1 : a.n_groups;
+  if (p.pack) {
+    b.x = static_cast<const uint16_t*>(a.ws);
+    b.ld = planes * p.kp;
+    b.gstride = a.rows * b.ld;
+    const unsigned grid = (unsigned)((a.rows * groups * (p.kp / 8) + kThreads - 1) / kThreads);
+    if (planes == 3)
+      pack_rows_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(
+          static_cast<const float*>(a.x), a.rows, a.c_in, a.ld_x, groups, a.gstride_x, p.kp, static_cast<uint16_t*>(a.ws));
+    else
+      pack_rows_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(
+          static_cast<const uint16_t*>(a.x), a.rows, a.c_in, a.ld_x, groups, a.gstride_x, p.kp,
+          static_cast<uint16_t*>(a.ws));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  } else {
+    b.x = static_cast<const uint16_t*>(a.x);
+    b.ld = a.ld_x;
+    b.gstride = a.gstride_x;
+  }
+  b.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.pack_bytes);
+  hipError_t e;
+  switch (p.nt) {
+    case 8: e = launch_big_nt<8, 2, 1, 1>(b, stream); break;
+    case 4: e = launch_big_nt<4, 2, 1, 2>(b, stream); break;
+    case 2: e = launch_big_nt<2, 1, 4, 2>(b, stream); break;
+    default: e = launch_big_nt<1, 1, 4, 3>(b, stream); break;
+  }
+  if (e != hipSuccess || p.splits == 1) return e;
+  const unsigned grid = (unsigned)((a.rows * groups * ((a.c_out + 3) / 4) + kThreads - 1) / kThreads);
+  if (a.y_dtype == 1)
+    split_sum_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(b.part, p.splits, a.rows, groups, a.c_out,
+                                                                         static_cast<uint16_t*>(a.y), a.ld_y, a.gstride_y);
+  else
+    split_sum_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(b.part, p.splits, a.rows, groups, a.c_out,
+                                                                      static_cast<float*>(a.y), a.ld_y, a.gstride_y);
+  return hipGetLastError();
+}
+
+// Whether the rows of x can be loaded to LDS directly (else the general kernel takes them).
+bool direct_rows(const LinearArgs& a, const Plan& p) {
+  if (p.pack) return true;
+  return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld_x % 8 == 0 || a.rows == 1) && a.gstride_x % 8 == 0 &&
+         a.ld_x < (1 << 22);
+}
+
 }  // namespace
 
 size_t linear_ws_bytes(const LinearArgs& a) {
-  (void)a;
-  return 0;
+  const Plan p = plan_of(a);
+  return p.pack_bytes + p.part_bytes;
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
+  const Plan p = plan_of(a);
+  if (p.few > 0) return launch_few(a, p.few, stream);
+  if (p.nt > 0 && direct_rows(a, p) && (p.pack_bytes + p.part_bytes == 0 || a.ws)) return launch_big(a, p, stream);
   if (a.grad) return a.x_dtype == 1 ? launch_x<true, uint16_t>(a, stream) : launch_x<true, float>(a, stream);
   return a.x_dtype == 1 ? launch_x<false, uint16_t>(a, stream) : launch_x<false, float>(a, stream);
 }

@@ -323,18 +323,19 @@ struct BigArgs {
 // there are is known on the device alone, so an XCD takes every eighth token
 // tile with all its outputs (the tiles past the last one then spread evenly;
 // t_tiles is a multiple of 8).
-__device__ __forceinline__ void big_tile(int64_t b, const BigArgs& a, int64_t& tile, int64_t& mt) {
-  if (a.a.ragged) {
+__device__ __forceinline__ void big_tile(int64_t b, bool ragged, int64_t m_tiles, int64_t t_tiles, int64_t& tile,
+                                         int64_t& mt) {
+  if (ragged) {
     const int64_t q = b / 8;
-    tile = q / a.m_tiles * 8 + b % 8;
-    mt = q % a.m_tiles;
+    tile = q / m_tiles * 8 + b % 8;
+    mt = q % m_tiles;
     return;
   }
-  const int64_t tiles = a.t_tiles * a.m_tiles;
+  const int64_t tiles = t_tiles * m_tiles;
   const int64_t per = tiles / 8, rest = tiles % 8, xcd = b % 8;
   const int64_t t = xcd * per + min(xcd, rest) + b / 8;
-  const int64_t col = t / (8 * a.t_tiles), in = t - col * 8 * a.t_tiles;
-  const int64_t width = min((int64_t)8, a.m_tiles - 8 * col);
+  const int64_t col = t / (8 * t_tiles), in = t - col * 8 * t_tiles;
+  const int64_t width = min((int64_t)8, m_tiles - 8 * col);
   tile = in / width;
   mt = 8 * col + in - tile * width;
 }
@@ -371,6 +372,7 @@ __device__ __forceinline__ uint32_t units2(uint32_t pk, float c) {
 // kPart: the row may end inside the chunk; the share then goes on with other
 // weights of the row, finite values that meet the zeros behind the
 // activations' row.
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x8_t __attribute__((ext_vector_type(8)));
 struct RawW {
   u32x8_t w;
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   constexpr int kAhead = (kDepth - 1) * (kLoads + (kPart ? 8 : 3) * kRF);  // loads issued behind the next chunk's at its barrier
   __shared__ __attribute__((aligned(1024))) uint8_t xs[kBufs * kBuf];
   int64_t tile, mt;
-  big_tile(blockIdx.x, b, tile, mt);
+  big_tile(blockIdx.x, b.a.ragged, b.m_tiles, b.t_tiles, tile, mt);
   Place p;
   if (!place_of<kBT>(b.a, tile, p)) return;  // the whole workgroup
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
@@ -574,6 +576,272 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
         else if (b.a.y_dtype == 1) store4(reinterpret_cast<uint16_t*>(p.y) + tok * b.a.ld_y + o, c_out - o, v);
         else store4(reinterpret_cast<float*>(p.y) + tok * b.a.ld_y + o, c_out - o, v);
       }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The large gradient: 64 kNT tokens x 256 columns per workgroup, four waves
+// of 32 kNT tokens x 128 columns.
+//
+// The contraction runs down the weights' rows, so an MFMA operand needs the
+// same column of eight rows.  Nothing is transposed for that: operand f (of
+// four) of a wave stands for columns 4 m + f (m its row 0..31), so lane m
+// needs the same two bytes of eight rows, four neighbouring columns, and the
+// rounding to bf16, which packs two values a register, pairs the rows.  The
+// accumulators of a lane are then 16 consecutive columns of its token.
+//
+// A stage is 64 rows of W (o) for all tokens and columns of the workgroup.
+// Everything comes by direct global -> LDS loads: dy 128 bytes a token (slot
+// q ^ (token / 2 % 8) holds 16-byte piece q, so 16 tokens' reads of one piece
+// meet no bank twice), the packed rows 128 bytes each, and the codes, one
+// 32-bit word each, four rows of a block side by side, so that a lane reads
+// its eight rows' codes in two 16-byte reads.  With no load into registers in
+// the loop every wait is counted by hand, kDepth stages ahead.
+//
+// Per step (16 rows) a wave issues 4 kNT MFMAs and between them reads the next
+// step's operands in the first slots and decodes them in the later ones (72
+// vector operations; a weight is decoded by the two waves that share its
+// columns).
+// ---------------------------------------------------------------------------
+constexpr int kGradK = 64;      // rows of W per stage
+constexpr int kGradM = 256;     // columns per workgroup
+
+struct GradArgs {
+  LinearArgs a;
+  const uint16_t* x;       // dy: bf16 rows, 16-byte aligned, a multiple of kGradK elements each
+  int64_t ld, gstride;
+  int stages, w_stages;    // stages of an x row (1 or 3 planes) and of W
+  int64_t m_tiles, t_tiles;
+  int splits;
+  float* part;
+};
+
+// 4 bytes (1 byte, zero-extended to 4) per lane from base + off straight into LDS (lane l at lds + 4 l).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma1(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// kW4: the packed rows are not 16-byte aligned and come in 4-byte pieces.
+template <int kNT, int kDepth, int kWaves, bool kW4>
+__global__ __launch_bounds__(kThreads, kWaves) void grad_big_kernel(GradArgs b) {
+  constexpr int kBT = 64 * kNT;
+  constexpr int kXBytes = kBT * 2 * kGradK, kWBytes = kGradK * kGradM / 2, kCBytes = kGradK * kGradM / 16 * 4;
+  constexpr int kBuf = kXBytes + kWBytes + kCBytes;
+  constexpr int kBufs = kDepth + 1;
+  constexpr int kXLoads = kXBytes / 4096, kWLoads = kW4 ? 8 : 2, kCLoads = 4;  // per wave and stage
+  constexpr int kLoads = kXLoads + kWLoads + kCLoads;
+  constexpr int kAhead = (kDepth - 1) * kLoads;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kBufs * kBuf];
+  int64_t tile, mt;
+  big_tile(blockIdx.x, b.a.ragged, b.m_tiles, b.t_tiles, tile, mt);
+  Place p;
+  if (!place_of<kBT>(b.a, tile, p)) return;  // the whole workgroup
+  const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t c_in = b.a.c_in, c_out = b.a.c_out, m0 = mt * kGradM;
+  const int s_first = (int)((int64_t)b.stages * blockIdx.y / b.splits);
+  const int end = (int)((int64_t)b.stages * (blockIdx.y + 1) / b.splits) - 1;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+
+  // dy: instruction i of a wave fills tokens 8 (wave + 4 i) .. + 7
+  const uint16_t* xg = b.x + uniform((b.a.ragged ? 0 : p.g * b.gstride) + p.row0 * b.ld);
+  const int last = (int)(p.row1 - p.row0) - 1;
+  const int xrow = 8 * wave + (lane >> 3);
+  uint32_t xoff[kXLoads];
+#pragma unroll
+  for (int i = 0; i < kXLoads; ++i) {
+    const int t = xrow + 32 * i;
+    xoff[i] = (uint32_t)min(t, last) * (uint32_t)(b.ld * 2) + (uint32_t)(((lane & 7) ^ ((t >> 1) & 7)) * 16);
+  }
+  // packed rows: 16-byte pieces, 8 rows an instruction, or 4-byte pieces, 2
+  // rows; a piece past the row's end is the row's first one (columns that are
+  // not stored)
+  const int64_t w_row = c_in / 2, c_row = c_in / 16;
+  constexpr int kWRows = kW4 ? 2 : 8;  // rows an instruction
+  const int wrow = kW4 ? lane >> 5 : lane >> 3;
+  int64_t wcol = m0 / 2 + (kW4 ? 4 * (lane & 31) : 16 * (lane & 7));
+  if (wcol >= w_row) wcol = 0;
+  // codes: block lane / 4, rows lane % 4 of an instruction's four
+  const int crow = lane & 3;
+  int64_t ccol = m0 / 16 + (lane >> 2);
+  if (ccol >= c_row) ccol = 0;
+  const uint8_t* wg = b.a.packed + uniform(p.g * c_out * w_row);
+  const uint8_t* cg = b.a.codes + uniform(p.g * c_out * c_row);
+  // load n of a stage's kLoads of this wave into buffer buf
+  auto dload = [&](int st, int buf, auto N) {
+    constexpr int n = N;
+    const uint32_t at = lds0 + buf * kBuf;
+    if constexpr (n < kXLoads) {
+      dma16(xg + uniform((int64_t)st * kGradK), xoff[n], at + 1024 * (wave + 4 * n));
+    } else {
+      // row o0 of the stage; rows past the last one are the last one (their dy is zero)
+      const int64_t o0 = (int64_t)(st % b.w_stages) * kGradK;
+      if constexpr (n < kXLoads + kWLoads) {
+        constexpr int i = n - kXLoads;
+        const int base = kWRows * (wave + 4 * i);
+        const int64_t o = min(o0 + base + wrow, c_out - 1);
+        const int64_t first = min(o0 + base, c_out - 1);  // wave-uniform
+        const uint32_t off = (uint32_t)((o - first) * w_row + wcol);
+        const uint32_t dst = at + kXBytes + base * (kGradM / 2);
+        if constexpr (kW4) dma4(wg + uniform(first * w_row), off, dst);
+        else dma16(wg + uniform(first * w_row), off, dst);
+      } else {
+        constexpr int i = n - kXLoads - kWLoads;
+        const int base = 4 * (wave + 4 * i);
+        const int64_t o = min(o0 + base + crow, c_out - 1);
+        const int64_t first = min(o0 + base, c_out - 1);
+        dma1(cg + uniform(first * c_row), (uint32_t)((o - first) * c_row + ccol),
+             at + kXBytes + kWBytes + base * (kGradM / 16) * 4);
+      }
+    }
+  };
+
+  // operand addresses within a buffer
+  const uint32_t xrd = (32 * kNT * wn + l32) * 128;            // + 4096 t, piece 2 i + h
+  const uint32_t xsw = (l32 >> 1) & 7;
+  const uint32_t wrd = kXBytes + 8 * h * (kGradM / 2) + 64 * wm + 2 * l32;                // + 128 (16 i + e)
+  const uint32_t crd = kXBytes + kWBytes + ((2 * h) * (kGradM / 16) + 8 * wm + (l32 >> 2)) * 16;  // + 1024 i
+
+  f32x16_t acc[4][kNT];
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[f][t][e] = 0.0f;
+  u32x4_t fa[2][4];
+  uint4 fb[2][kNT];
+  uint32_t raw[4];   // rows 2 e, 2 e + 1 of the step: two bytes each
+  uint4 code[2];
+
+  auto bread = [&](auto set, int base, auto i, auto t) {
+    fb[set][t] = *reinterpret_cast<const uint4*>(lds + base + xrd + 4096 * t + (((2 * i + h) ^ xsw) * 16));
+  };
+  auto wread = [&](int base, auto i, auto e) {
+    const uint8_t* r = lds + base + wrd + (16 * i + 2 * e) * (kGradM / 2);
+    const uint32_t lo = *reinterpret_cast<const uint16_t*>(r);
+    const uint32_t hi = *reinterpret_cast<const uint16_t*>(r + kGradM / 2);
+    raw[e] = lo | (hi << 16);
+  };
+  auto cread = [&](int base, auto i, auto j) {
+    code[j] = *reinterpret_cast<const uint4*>(lds + base + crd + (16 * i + 4 * j) / 4 * (kGradM / 16) * 16);
+  };
+  // rows 2 e, 2 e + 1, columns 2 q, 2 q + 1 of the four
+  auto decode = [&](auto set, auto U) {
+    constexpr int e = U >> 1, q = U & 1;
+    const uint4 cc = code[e >> 1];
+    const float s0 = e4m3_to_f32<0>(e & 1 ? cc.z : cc.x), s1 = e4m3_to_f32<0>(e & 1 ? cc.w : cc.y);
+    const f32x2_t r0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(raw[e], 1.0f, q);
+    const f32x2_t r1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(raw[e], 1.0f, 2 + q);
+    fa[set][2 * q][e] = pack_bf16(r0.x * s0, r1.x * s1);
+    fa[set][2 * q + 1][e] = pack_bf16(r0.y * s0, r1.y * s1);
+  };
+  // Step s (of 4): the MFMAs of operand set s & 1; the operands of the next
+  // step from LDS buffer `base`; direct loads d0 .. d1 - 1 of stage dst.
+  auto step = [&](auto s, int base, int dst, int dbuf, auto d0, auto d1) {
+    constexpr int set = s & 1, slots = 4 * kNT;
+    static_for<slots>([&](auto N) {
+      constexpr int n = N;
+      std::integral_constant<int, set ^ 1> nset;
+      std::integral_constant<int, (s + 1) & 3> ni;
+      // reads first: codes and packed rows in slots 0, 1 (kNT = 2) or 0 .. 3, activations over the step
+      constexpr int rs = slots / 4;
+      if constexpr (n < rs) {
+        static_for<4 / rs>([&](auto K) { wread(base, ni, std::integral_constant<int, n * (4 / rs) + K>{}); });
+        if constexpr (n < 2) cread(base, ni, N);
+        if constexpr (rs == 1) cread(base, ni, std::integral_constant<int, 1>{});
+      } else if constexpr (n - rs < kNT) {
+        bread(nset, base, ni, std::integral_constant<int, n - rs>{});
+      }
+      // direct loads, dealt over the slots
+      static_for<(d1 - d0 + slots - 1) / slots>([&](auto K) {
+        constexpr int per = (d1 - d0 + slots - 1) / slots, i = d0 + n * per + K;
+        if constexpr (i < d1) dload(dst, dbuf, std::integral_constant<int, i>{});
+      });
+      // decoding from slot slots / 2 on
+      constexpr int u0 = n < slots / 2 ? 0 : (n - slots / 2) * 8 / (slots / 2),
+                    u1 = n < slots / 2 ? 0 : (n + 1 - slots / 2) * 8 / (slots / 2);
+      static_for<u1 - u0>([&](auto K) { decode(nset, std::integral_constant<int, u0 + K>{}); });
+      constexpr int f = n / kNT, t = n % kNT;
+      acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[set][f]),
+                                                          __builtin_bit_cast(bf16x8_t, fb[set][t]), acc[f][t], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  // Stage S sits in buffer (S - s_first) % kBufs.  Its loads go out in three
+  // steps: the last step of stage S - kBufs (after the barrier that ends that
+  // stage's reads) and the first two of the next stage; past the end the
+  // final stage is loaded again into buffers that are read no more.
+  constexpr int kQ0 = kLoads / 3, kQ1 = 2 * kLoads / 3;
+  static_for<kDepth>([&](auto d) {
+    static_for<kLoads>([&](auto n) { dload(min(s_first + d, end), d, n); });
+  });
+  static_for<kQ0>([&](auto n) { dload(min(s_first + kDepth, end), kDepth, n); });
+  wait_loads<0>();
+  __syncthreads();
+  {
+    std::integral_constant<int, 0> zero;
+    static_for<4>([&](auto e) { wread(0, zero, e); });
+    static_for<2>([&](auto j) { cread(0, zero, j); });
+    static_for<kNT>([&](auto t) { bread(zero, 0, zero, t); });
+    static_for<8>([&](auto u) { decode(zero, u); });
+  }
+  int buf = 0;
+  for (int st = s_first; st <= end; ++st) {
+    const int dst1 = min(st + kDepth, end), dst2 = min(st + kDepth + 1, end);
+    const int nbuf = buf + 1 == kBufs ? 0 : buf + 1, pbuf = buf == 0 ? kBufs - 1 : buf - 1;
+    const int base = buf * kBuf, nbase = nbuf * kBuf;
+    std::integral_constant<int, 0> i0;
+    std::integral_constant<int, 1> i1;
+    std::integral_constant<int, 2> i2;
+    std::integral_constant<int, 3> i3;
+    std::integral_constant<int, kQ0> q0;
+    std::integral_constant<int, kQ1> q1;
+    std::integral_constant<int, kLoads> q2;
+    step(i0, base, dst1, pbuf, q0, q1);
+    step(i1, base, dst1, pbuf, q1, q2);
+    step(i2, base, dst1, pbuf, i0, i0);
+    wait_loads<kAhead>();  // the next stage has landed; this one's last operands are in registers
+    block_sync();
+    step(i3, nbase, dst2, buf, i0, q0);
+    buf = nbuf;
+  }
+  wait_loads<0>();  // the repeated loads: nothing lands after the workgroup has ended
+
+  // lane: token 32 kNT wn + 32 t + l32, columns m0 + 128 wm + 32 q + 16 h + 4 r + f
+  const float sc = out_scale(b.a, p.g);
+  float* part = b.splits > 1 ? b.part + (blockIdx.y * b.a.n_groups + p.g) * b.a.rows * c_in : nullptr;
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+    const int64_t tok = p.row0 + 32 * kNT * wn + 32 * t + l32;
+    if (tok >= p.row1) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t c = m0 + 128 * wm + 32 * q + 16 * h;
+      if (c >= c_in) continue;  // c_in is a multiple of 16: all sixteen or none
+      float v[16];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) v[4 * r + f] = sc * acc[f][t][4 * q + r];
+      if (part || b.a.y_dtype == 0) {
+        float* d = part ? part + tok * c_in + c : reinterpret_cast<float*>(p.y) + tok * b.a.ld_y + c;
+        __builtin_memcpy(d, v, 64);
+      } else {
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        __builtin_memcpy(reinterpret_cast<uint16_t*>(p.y) + tok * b.a.ld_y + c, o, 32);
+      }
+    }
   }
 }
 
@@ -818,18 +1086,22 @@ struct Plan {
 // Outputs of a workgroup of linear_big_kernel<nt>.
 int64_t big_m(int nt) { return nt >= 4 ? 256 : 128; }
 
-// Time of a launch of linear_big_kernel<nt> in microseconds, from what its
-// parts measured on MI355X: a chunk takes `one` with one workgroup on a CU
-// and `all` with as many as fit (`fit`), each workgroup starts and ends for
+// Time of a launch of a large kernel in microseconds, from what its parts
+// measured on MI355X: a chunk (or stage) takes `one` with one workgroup on a
+// CU and `all` with as many as fit (`fit`), each workgroup starts and ends for
 // 3.5, and a split adds a launch and its partial sums' way to memory and back.
-// (4096 x 4096 weights, 512 tokens: nt 2 unsplit 27.9, in 2 parts 34.7, nt 4
-// in 4 parts 37.5; 128 tokens: nt 1 in 2 parts 18.6, nt 2 in 4 parts 19.9;
-// 8192 tokens on 12288 x 4096: nt 4 740, nt 8 757.)
+// Product, 4096 x 4096 weights, 512 tokens: nt 2 unsplit 27.9, in 2 parts
+// 34.7, nt 4 in 4 parts 37.5; 128 tokens: nt 1 in 2 parts 18.6, nt 2 in 4
+// parts 19.9; 8192 tokens on 12288 x 4096: nt 4 740, nt 8 757.
+// Gradient, 4096 x 4096 weights, 4096 tokens: nt 4 132, nt 2 155, nt 1 237;
+// 1024 tokens: nt 4 in 4 parts 67, unsplit 118; 256 tokens: nt 2 in 8 parts
+// 33, nt 4 in 4 parts 48; 64 tokens: nt 1 in 8 parts 25, nt 2 26.
 struct BigCost {
   int nt, fit;
   double one, all;
 };
 constexpr BigCost kBigCosts[] = {{8, 1, 3.9, 3.9}, {4, 2, 2.3, 3.85}, {2, 2, 0.85, 1.35}, {1, 4, 0.65, 1.6}};
+constexpr BigCost kGradCosts[] = {{4, 1, 2.0, 2.0}, {2, 2, 1.45, 2.35}, {1, 2, 1.27, 1.8}};
 constexpr int kCUs = 256;
 
 double big_cost(const BigCost& k, double tiles, int64_t chunks, int splits, double part_values) {
@@ -837,38 +1109,25 @@ double big_cost(const BigCost& k, double tiles, int64_t chunks, int splits, doub
   const double rounds = groups > slots ? groups / slots : 1.0;
   const double load = groups >= slots ? 1.0 : groups > kCUs ? (groups - kCUs) / (slots - kCUs) : 0.0;
   const double chunk = k.one + (k.all - k.one) * load;
-  // the last round is rarely full: half a workgroup's time more on average past the first round
+  // the last round is rarely full: half a workgroup's time more on average past the first rounds
   const double turns = rounds > 1.0 ? (rounds < 4.0 ? ceil(rounds) : rounds + 0.5) : 1.0;
   double t = turns * (3.5 + chunk * (double)((chunks + splits - 1) / splits));
   if (splits > 1) t += 2.5 + splits * part_values * 8e-6 / 4.0;
   return t;
 }
 
-Plan plan_of(const LinearArgs& a) {
-  Plan p;
-  if (a.rows <= 0 || a.c_in <= 0 || a.c_out <= 0) return p;
-  if (a.grad) return p;
-  // Up to four tokens: linear_few_kernel (5120 x 17408 weights, one token:
-  // 12.9 us against 30 for nt 1 in 8 parts; 12288 x 4096, four tokens: 13.1
-  // against 24).  Ragged rows of several experts: nt 1 from 64 rows on 64
-  // experts on (14.1 us against 17.2).
-  if (a.ragged ? a.rows <= 16 : a.rows <= 4) {
-    p.few = a.ragged || a.rows <= 1 ? 1 : a.rows <= 2 ? 2 : 4;
-    return p;
-  }
-  const int planes = a.x_dtype == 1 ? 1 : 3;
-  p.kp = (a.c_in + kChunk - 1) / kChunk * kChunk;
-  p.pack = planes == 3 || a.c_in % kChunk != 0;
-  const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups;
-  const int64_t chunks = planes * (p.kp / kChunk);
+// The cheapest of kCosts' kernels and of up to 16 parts for a.
+template <int kN>
+void cheapest(Plan& p, const LinearArgs& a, const BigCost (&costs)[kN], int64_t chunks) {
+  const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups, m = a.grad ? a.c_in : a.c_out;
   double best = 0.0;
-  for (const BigCost& k : kBigCosts) {
-    const int64_t bt = 32 * k.nt, m_tiles = (a.c_out + big_m(k.nt) - 1) / big_m(k.nt);
+  for (const BigCost& k : costs) {
+    const int64_t bt = (a.grad ? 64 : 32) * k.nt, bm = a.grad ? kGradM : big_m(k.nt), m_tiles = (m + bm - 1) / bm;
     // ragged: about half of a tile more per group that has rows
     const double used = (double)(a.n_groups < a.rows ? a.n_groups : a.rows);
     const double t_tiles = a.ragged ? (double)a.rows / bt + 0.5 * used : (double)((a.rows + bt - 1) / bt * a.n_groups);
     for (int splits = 1; splits <= (a.ragged ? 1 : 16) && splits <= chunks; splits *= 2) {
-      const double t = big_cost(k, t_tiles * m_tiles, chunks, splits, (double)all * a.c_out);
+      const double t = big_cost(k, t_tiles * m_tiles, chunks, splits, (double)all * m);
       if (p.nt == 0 || t < best) {
         best = t;
         p.nt = k.nt;
@@ -876,8 +1135,28 @@ Plan plan_of(const LinearArgs& a) {
       }
     }
   }
+}
+
+Plan plan_of(const LinearArgs& a) {
+  Plan p;
+  if (a.rows <= 0 || a.c_in <= 0 || a.c_out <= 0) return p;
+  // Up to four tokens: linear_few_kernel (5120 x 17408 weights, one token:
+  // 12.9 us against 30 for nt 1 in 8 parts; 12288 x 4096, four tokens: 13.1
+  // against 24).  Ragged rows of several experts: nt 1 from 64 rows on 64
+  // experts on (14.1 us against 17.2).
+  if (!a.grad && (a.ragged ? a.rows <= 16 : a.rows <= 4)) {
+    p.few = a.ragged || a.rows <= 1 ? 1 : a.rows <= 2 ? 2 : 4;
+    return p;
+  }
+  const int planes = a.x_dtype == 1 ? 1 : 3;
+  const int64_t k = a.grad ? a.c_out : a.c_in, step = a.grad ? kGradK : kChunk;
+  const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups;
+  p.kp = (k + step - 1) / step * step;
+  p.pack = planes == 3 || k % step != 0;
+  if (a.grad) cheapest(p, a, kGradCosts, planes * p.kp / step);
+  else cheapest(p, a, kBigCosts, planes * p.kp / step);
   if (p.pack) p.pack_bytes = ((size_t)all * planes * p.kp * 2 + 255) / 256 * 256;
-  if (p.splits > 1) p.part_bytes = (size_t)p.splits * all * a.c_out * 4;
+  if (p.splits > 1) p.part_bytes = (size_t)p.splits * all * (a.grad ? a.c_in : a.c_out) * 4;
   return p;
 }
 
@@ -921,53 +1200,82 @@ hipError_t launch_big_nt(const BigArgs& b, hipStream_t stream) {
 }
 
 
-hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
+template <int kNT, int kDepth, int kWaves>
+hipError_t launch_grad_nt(const GradArgs& b, hipStream_t stream) {
+  const dim3 grid((unsigned)(b.m_tiles * b.t_tiles), (unsigned)b.splits);
+  if (b.a.c_in % 32 == 0 && reinterpret_cast<uintptr_t>(b.a.packed) % 16 == 0)
+    grad_big_kernel<kNT, kDepth, kWaves, false><<<grid, dim3(kThreads), 0, stream>>>(b);
+  else
+    grad_big_kernel<kNT, kDepth, kWaves, true><<<grid, dim3(kThreads), 0, stream>>>(b);
+  return hipGetLastError();
+}
+
+// The rows of x as the large kernels take them: themselves, or packed into the workspace.
+struct Rows {
+  const uint16_t* x;
+  int64_t ld, gstride;
+};
+hipError_t pack_rows(const LinearArgs& a, const Plan& p, Rows& r, hipStream_t stream) {
+  if (!p.pack) {
+    r = Rows{static_cast<const uint16_t*>(a.x), a.ld_x, a.gstride_x};
+    return hipSuccess;
+  }
   const int planes = a.x_dtype == 1 ? 1 : 3;
-  BigArgs b{};
-  b.a = a;
-  b.w_chunks = (int)(p.kp / kChunk);
-  b.chunks = planes * b.w_chunks;
-  b.splits = p.splits;
-  b.m_tiles = (a.c_out + big_m(p.nt) - 1) / big_m(p.nt);
-  b.t_tiles = token_tiles(a, 32 * p.nt);
-  if (a.ragged) b.t_tiles = (b.t_tiles + 7) / 8 * 8;
-  const int64_t groups = a.ragged ? 1 : a.n_groups;
-  if (p.pack) {
-    b.x = static_cast<const uint16_t*>(a.ws);
-    b.ld = planes * p.kp;
-    b.gstride = a.rows * b.ld;
-    const unsigned grid = (unsigned)((a.rows * groups * (p.kp / 8) + kThreads - 1) / kThreads);
-    if (planes == 3)
-      pack_rows_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(
-          static_cast<const float*>(a.x), a.rows, a.c_in, a.ld_x, groups, a.gstride_x, p.kp, static_cast<uint16_t*>(a.ws));
-    else
-      pack_rows_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(
-          static_cast<const uint16_t*>(a.x), a.rows, a.c_in, a.ld_x, groups, a.gstride_x, p.kp,
-          static_cast<uint16_t*>(a.ws));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  } else {
-    b.x = static_cast<const uint16_t*>(a.x);
-    b.ld = a.ld_x;
-    b.gstride = a.gstride_x;
-  }
-  b.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.pack_bytes);
-  hipError_t e;
-  switch (p.nt) {
-    case 8: e = launch_big_nt<8, 2, 1, 1>(b, stream); break;
-    case 4: e = launch_big_nt<4, 2, 1, 2>(b, stream); break;
-    case 2: e = launch_big_nt<2, 1, 4, 2>(b, stream); break;
-    default: e = launch_big_nt<1, 1, 4, 3>(b, stream); break;
-  }
-  if (e != hipSuccess || p.splits == 1) return e;
-  const unsigned grid = (unsigned)((a.rows * groups * ((a.c_out + 3) / 4) + kThreads - 1) / kThreads);
+  const int64_t groups = a.ragged ? 1 : a.n_groups, k = a.grad ? a.c_out : a.c_in;
+  uint16_t* out = static_cast<uint16_t*>(a.ws);
+  r = Rows{out, planes * p.kp, a.rows * planes * p.kp};
+  const unsigned grid = (unsigned)((a.rows * groups * (p.kp / 8) + kThreads - 1) / kThreads);
+  if (planes == 3)
+    pack_rows_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(static_cast<const float*>(a.x), a.rows, k,
+                                                                      a.ld_x, groups, a.gstride_x, p.kp, out);
+  else
+    pack_rows_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(static_cast<const uint16_t*>(a.x), a.rows, k,
+                                                                         a.ld_x, groups, a.gstride_x, p.kp, out);
+  return hipGetLastError();
+}
+
+hipError_t sum_splits(const LinearArgs& a, const Plan& p, const float* part, hipStream_t stream) {
+  const int64_t groups = a.ragged ? 1 : a.n_groups, cols = a.grad ? a.c_in : a.c_out;
+  const unsigned grid = (unsigned)((a.rows * groups * ((cols + 3) / 4) + kThreads - 1) / kThreads);
   if (a.y_dtype == 1)
-    split_sum_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(b.part, p.splits, a.rows, groups, a.c_out,
+    split_sum_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(part, p.splits, a.rows, groups, cols,
                                                                          static_cast<uint16_t*>(a.y), a.ld_y, a.gstride_y);
   else
-    split_sum_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(b.part, p.splits, a.rows, groups, a.c_out,
+    split_sum_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(part, p.splits, a.rows, groups, cols,
                                                                       static_cast<float*>(a.y), a.ld_y, a.gstride_y);
   return hipGetLastError();
+}
+
+hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
+  const int planes = a.x_dtype == 1 ? 1 : 3;
+  Rows r;
+  hipError_t e = pack_rows(a, p, r, stream);
+  if (e != hipSuccess) return e;
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.pack_bytes);
+  int64_t t_tiles = token_tiles(a, a.grad ? 64 * p.nt : 32 * p.nt);
+  if (a.ragged) t_tiles = (t_tiles + 7) / 8 * 8;
+  if (a.grad) {
+    const int w_stages = (int)(p.kp / kGradK);
+    const GradArgs b{a, r.x, r.ld, r.gstride, planes * w_stages, w_stages, (a.c_in + kGradM - 1) / kGradM, t_tiles,
+                     p.splits, part};
+    switch (p.nt) {
+      case 4: e = launch_grad_nt<4, 2, 1>(b, stream); break;
+      case 2: e = launch_grad_nt<2, 1, 2>(b, stream); break;
+      default: e = launch_grad_nt<1, 2, 2>(b, stream); break;
+    }
+  } else {
+    const int w_chunks = (int)(p.kp / kChunk);
+    const BigArgs b{a, r.x, r.ld, r.gstride, planes * w_chunks, w_chunks, (a.c_out + big_m(p.nt) - 1) / big_m(p.nt),
+                    t_tiles, p.splits, part};
+    switch (p.nt) {
+      case 8: e = launch_big_nt<8, 2, 1, 1>(b, stream); break;
+      case 4: e = launch_big_nt<4, 2, 1, 2>(b, stream); break;
+      case 2: e = launch_big_nt<2, 1, 4, 2>(b, stream); break;
+      default: e = launch_big_nt<1, 1, 4, 3>(b, stream); break;
+    }
+  }
+  if (e != hipSuccess || p.splits == 1) return e;
+  return sum_splits(a, p, part, stream);
 }
 
 // Whether the rows of x can be loaded to LDS directly (else the general kernel takes them).

@@ -140,11 +140,13 @@ def _check(status: int) -> None:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """The current stream of t's device as an integer (the raw call takes a
+    tenth of a microsecond, building a Stream object two)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -651,13 +653,19 @@ def _dense(t: torch.Tensor | None, name: str, dtype, shape=None) -> None:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _same_device(first: torch.Tensor, *others) -> None:
+def _on_device(first: torch.Tensor, *others) -> None:
+    """All given tensors on one ROCm device."""
+    d = first.get_device()
+    if d < 0:
+        raise ValueError("liblh works on device tensors only (got a %s tensor)" % first.device)
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
+            if not t.is_cuda:
+                raise ValueError("liblh works on device tensors only (got a %s tensor)" % t.device)
             raise ValueError("tensors on different devices (%s and %s)" % (first.device, t.device))
 
 
@@ -670,19 +678,17 @@ def lh_quantize_nvfp4(x: torch.Tensor, amax: torch.Tensor, values: bool | torch.
     outputs: values [g, rows, c_in] = r * c in units of S_g (exact; x's dtype
     unless values_dtype says otherwise), packed, scale_e4m3, global_scale as
     lh_fake_quant_nvfp4."""
-    _require_device(x, amax)
+    _on_device(x, amax)
     x3 = _as3(x)
     if x3.shape[-1] > 0 and x3.stride(-1) != 1:
         raise ValueError("last dim of x must be contiguous")
     g, rows, c_in = x3.shape
-    _same_device(x, amax)
     _dense(amax, "amax", torch.float32, (g,))
     dev = x.device
 
     def out(req, shape, dtype, name):
         if isinstance(req, torch.Tensor):
-            _require_device(req)
-            _same_device(x, req)
+            _on_device(x, req)
             _dense(req, name, dtype, shape)
             return req
         return torch.empty(shape, dtype=dtype, device=dev) if req else None
@@ -709,8 +715,7 @@ def lh_linear_nvfp4_workspace_bytes(n_rows: int, c_in: int, c_out: int, n_groups
 
 def _linear(x, offsets, packed, scale_e4m3, global_scale, x_scale, y, out_dtype, max_group_rows, workspace, grad):
     """The four product calls: x [rows, .] or [g, rows, .]; offsets None or int64 [g + 1]."""
-    _require_device(x, offsets, packed, scale_e4m3, global_scale, x_scale, y)
-    _same_device(x, offsets, packed, scale_e4m3, global_scale, x_scale, y)
+    _on_device(x, offsets, packed, scale_e4m3, global_scale, x_scale, y)
     x3, p3, s3 = _as3(x), _as3(packed), _as3(scale_e4m3)
     g, c_out, half = p3.shape
     c_in = 2 * half
@@ -813,7 +818,7 @@ def lh_moe_sort(expert_ids: torch.Tensor, n_groups: int, order: bool = True,
     [n_groups + 1], position int32 [n_tokens, top_k] (the row, or -1 - row of
     a dropped one) and, with order=True, order int32 [n_tokens * top_k] (the
     assignment of each row, or -1 - it)."""
-    _require_device(expert_ids, workspace)
+    _on_device(expert_ids, workspace)
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be [n_tokens, top_k]")
     if expert_ids.dtype not in (torch.int32, torch.int64):
@@ -847,8 +852,7 @@ def _rows2(t: torch.Tensor, name: str, cols: int | None = None, like: torch.Tens
 def lh_moe_dispatch(x: torch.Tensor, position: torch.Tensor, xs: torch.Tensor | None = None) -> torch.Tensor:
     """Tokens' rows to their experts: xs[position[t, k]] = x[t], zero rows for
     dropped assignments; xs [n_tokens * top_k, cols] unless given."""
-    _require_device(x, position, xs)
-    _same_device(x, position, xs)
+    _on_device(x, position, xs)
     _rows2(x, "x")
     t, cols = x.shape
     _dense(position, "position", torch.int32)
@@ -867,8 +871,7 @@ def lh_moe_combine(ys: torch.Tensor, position: torch.Tensor, weights: torch.Tens
                    y: torch.Tensor | None = None) -> torch.Tensor:
     """Rows back to their tokens: y[t] = sum_k weights[t, k] ys[position[t, k]]
     over the assignments that have an expert (weights fp32, None: 1)."""
-    _require_device(ys, position, weights, y)
-    _same_device(ys, position, weights, y)
+    _on_device(ys, position, weights, y)
     _rows2(ys, "ys")
     _dense(position, "position", torch.int32)
     if position.dim() != 2:
@@ -892,8 +895,7 @@ def lh_moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, position: torch.Tens
     """Gradients of lh_moe_combine: (dys, dweights) with dys[position[t, k]] =
     weights[t, k] dy[t] (zero rows for dropped assignments) and dweights[t, k]
     = <dy[t], ys[position[t, k]]>; None where not requested (False)."""
-    _require_device(dy, ys, position, weights)
-    _same_device(dy, ys, position, weights)
+    _on_device(dy, ys, position, weights)
     _rows2(dy, "dy")
     t, cols = dy.shape
     _rows2(ys, "ys", cols, dy)
@@ -907,8 +909,7 @@ def lh_moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, position: torch.Tens
     elif dys is False:
         dys = None
     if dys is not None:
-        _require_device(dys)
-        _same_device(dy, dys)
+        _on_device(dy, dys)
         _rows2(dys, "dys", cols, dy)
         if dys.shape[0] != ys.shape[0]:
             raise ValueError("dys must have ys's rows")
@@ -917,8 +918,7 @@ def lh_moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, position: torch.Tens
     elif dweights is False:
         dweights = None
     if dweights is not None:
-        _require_device(dweights)
-        _same_device(dy, dweights)
+        _on_device(dy, dweights)
         _dense(dweights, "dweights", torch.float32, (t, k))
     _check(lib.lh_moe_combine_grad(_ptr(dy), _dtype(dy), t, cols, _row_stride(dy), _ptr(ys), ys.shape[0],
                                    _row_stride(ys), _ptr(position), k, _ptr(weights), _ptr(dys),

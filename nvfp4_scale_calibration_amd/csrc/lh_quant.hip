@@ -138,8 +138,46 @@ hipError_t launch_fq_typed(const FakeQuantArgs& a, hipStream_t stream) {
 // leave as r c, in units of S_g, which bf16 and fp32 both hold exactly.
 // A lane takes 16 bytes (8 bf16 or 4 fp32 values), so two or four
 // neighbouring lanes share a block and find its maximum by xor shuffles;
-// every load and store instruction covers consecutive bytes of the wave.
+// every load and store instruction covers consecutive bytes of the wave, and
+// a thread has kQVecs of them in flight.
+//
+// IEEE divisions (some ten operations each) would take most of the vector
+// unit's time, so quotients are formed with the reciprocal first, within
+// 2^-21 of the exact one, and rounded to the grid a little above and a little
+// below (2^-20): where both land on the same point, so does the exact
+// quotient, and only where they differ is the division done.
 // ---------------------------------------------------------------------------
+constexpr int kQVecs = 4;
+constexpr float kAbove = 1.0f + 0x1p-20f, kBelow = 1.0f - 0x1p-20f;
+
+// E2M1 nibbles of the kE quotients q, low nibble first.
+template <int kE>
+__device__ __forceinline__ uint32_t nibbles_of(const float (&q)[kE]) {
+  uint32_t pk = 0u;
+  pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[0], q[1], 1.0f, 0);
+  pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[2], q[3], 1.0f, 1);
+  if constexpr (kE == 8) {
+    pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[4], q[5], 1.0f, 2);
+    pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[6], q[7], 1.0f, 3);
+  }
+  return pk;
+}
+
+// The code of t = fl32(fl32(m / 6) / Sg): the nearest positive E4M3 value
+// (ties to even), clamped below the conversion's overflow, never the zero
+// code.  inv: about 1 / (6 Sg), or 0 where that is not a normal number.
+__device__ __forceinline__ uint32_t max_rule_code(float m, float Sg, float inv) {
+  if (!(Sg > 0.0f)) return 1u;
+  const float y = fminf(m * inv, 448.0f);
+  uint32_t two = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(y * kAbove, 448.0f), y * kBelow, 0, false);
+  if (inv == 0.0f || ((two ^ (two >> 8)) & 0xffu)) {
+    const float t = fminf((m / 6.0f) / Sg, 448.0f);
+    two = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, t, 0, false);
+  }
+  const uint32_t code = two & 0x7fu;
+  return code > 0u ? code : 1u;
+}
+
 template <typename T, typename TV>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, int64_t rows, int64_t cols, int64_t ld) {
   constexpr int kE = 16 / sizeof(T);   // values per lane
@@ -149,65 +187,79 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantizeArgs a, int6
   TV* values = static_cast<TV*>(a.values);
   for (int64_t g = blockIdx.z; g < a.n_groups; g += gridDim.z) {
     const float Sg = a.amax[g] / kAmaxDivisor;
+    const float six = 6.0f * Sg;
+    const float inv6 = six > 0x1p-100f && six < 0x1p100f ? __builtin_amdgcn_rcpf(six) : 0.0f;
     if (a.gscale && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.gscale[g] = Sg;
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-      for (int64_t v = (int64_t)blockIdx.x * kThreads + threadIdx.x; v < vecs; v += (int64_t)gridDim.x * kThreads) {
-        const uint4 raw = load_u128(x + g * a.gstride + r * ld + v * kE);
-        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-        float w[kE];
+      const T* row = x + g * a.gstride + r * ld;
+      for (int64_t v0 = (int64_t)blockIdx.x * (kThreads * kQVecs) + threadIdx.x; v0 < vecs;
+           v0 += (int64_t)gridDim.x * (kThreads * kQVecs)) {
+        uint4 raw[kQVecs];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (kE == 8) {
-            w[2 * i] = __uint_as_float(in[i] << 16);
-            w[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
-          } else {
-            w[i] = __uint_as_float(in[i]);
+        for (int j = 0; j < kQVecs; ++j)
+          if (v0 + j * kThreads < vecs) raw[j] = load_u128(row + (v0 + j * kThreads) * kE);
+#pragma unroll
+        for (int j = 0; j < kQVecs; ++j) {
+          const int64_t v = v0 + j * kThreads;
+          if (v >= vecs) break;  // the lanes of a block leave together
+          const uint32_t in[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+          float w[kE];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (kE == 8) {
+              w[2 * i] = __uint_as_float(in[i] << 16);
+              w[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
+            } else {
+              w[i] = __uint_as_float(in[i]);
+            }
           }
-        }
-        float m = 0.0f;
+          float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(w[i]));
+          for (int i = 0; i < kE; ++i) m = fmaxf(m, fabsf(w[i]));
 #pragma unroll
-        for (int off = 1; off < kP; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
-        // the nearest positive E4M3 value (ties to even): clamped below the
-        // conversion's overflow, and never the zero code
-        const float t = fminf((m / 6.0f) / Sg, 448.0f);
-        uint32_t code = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t, t, 0, false) & 0x7fu;
-        code = (Sg > 0.0f && code > 0u) ? code : 1u;
-        const float c = e4m3_to_f32<0>(code);
-        const float s = c * Sg;
-        float q[kE];
+          for (int off = 1; off < kP; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+          const uint32_t code = max_rule_code(m, Sg, inv6);
+          const float c = e4m3_to_f32<0>(code);
+          const float s = c * Sg;
+          const bool near = s > 0x1p-100f && s < 0x1p100f;
+          const float inv = __builtin_amdgcn_rcpf(s);
+          float above[kE], below[kE];
 #pragma unroll
-        for (int i = 0; i < kE; ++i) q[i] = (s == 0.0f) ? 0.0f : w[i] / s;  // IEEE division
-        uint32_t pk = 0u;
-        pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[0], q[1], 1.0f, 0);
-        pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[2], q[3], 1.0f, 1);
-        if constexpr (kE == 8) {
-          pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[4], q[5], 1.0f, 2);
-          pk = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(pk, q[6], q[7], 1.0f, 3);
-        }
-        const uint32_t nz = (pk | (pk >> 1) | (pk >> 2)) & 0x11111111u;  // -0 is written as +0
-        pk &= 0x77777777u | (nz << 3);
-        const int64_t at = (g * rows + r) * vecs + v;  // dense outputs
-        if (values) {
-          float u[8];
-          units8(pk, c, u);
-          if constexpr (sizeof(TV) == 2 && kE == 8) {
-            const uint32_t b[4] = {pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]),
-                                   pack_bf16(u[6], u[7])};
-            __builtin_memcpy(values + at * kE, b, 16);
-          } else if constexpr (sizeof(TV) == 2) {
-            const uint32_t b[2] = {pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])};
-            __builtin_memcpy(values + at * kE, b, 8);
-          } else {
-            __builtin_memcpy(values + at * kE, u, 4 * kE);
+          for (int i = 0; i < kE; ++i) {
+            const float y = w[i] * inv;
+            above[i] = y * kAbove;
+            below[i] = y * kBelow;
           }
+          uint32_t pk = nibbles_of(above);
+          if (!near || pk != nibbles_of(below)) {
+            float q[kE];
+#pragma unroll
+            for (int i = 0; i < kE; ++i) q[i] = (s == 0.0f) ? 0.0f : w[i] / s;  // IEEE division
+            pk = nibbles_of(q);
+          }
+          const uint32_t nz = (pk | (pk >> 1) | (pk >> 2)) & 0x11111111u;  // -0 is written as +0
+          pk &= 0x77777777u | (nz << 3);
+          const int64_t at = (g * rows + r) * vecs + v;  // dense outputs
+          if (values) {
+            float u[8];
+            units8(pk, c, u);
+            if constexpr (sizeof(TV) == 2 && kE == 8) {
+              const uint32_t b[4] = {pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]), pack_bf16(u[4], u[5]),
+                                     pack_bf16(u[6], u[7])};
+              __builtin_memcpy(values + at * kE, b, 16);
+            } else if constexpr (sizeof(TV) == 2) {
+              const uint32_t b[2] = {pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3])};
+              __builtin_memcpy(values + at * kE, b, 8);
+            } else {
+              __builtin_memcpy(values + at * kE, u, 4 * kE);
+            }
+          }
+          if (a.packed) {
+            if constexpr (kE == 8) *reinterpret_cast<uint32_t*>(a.packed + 4 * at) = pk;
+            else *reinterpret_cast<uint16_t*>(a.packed + 2 * at) = (uint16_t)pk;
+          }
+          if (a.codes && (v & (kP - 1)) == 0) a.codes[at / kP] = (uint8_t)code;
         }
-        if (a.packed) {
-          if constexpr (kE == 8) *reinterpret_cast<uint32_t*>(a.packed + 4 * at) = pk;
-          else *reinterpret_cast<uint16_t*>(a.packed + 2 * at) = (uint16_t)pk;
-        }
-        if (a.codes && (v & (kP - 1)) == 0) a.codes[at / kP] = (uint8_t)code;
       }
     }
   }
@@ -220,7 +272,7 @@ hipError_t launch_quantize_typed(const QuantizeArgs& a, hipStream_t stream) {
     cols *= rows;
     rows = 1;
   }
-  const int64_t per = kThreads * (16 / (int64_t)sizeof(T));
+  const int64_t per = kThreads * kQVecs * (16 / (int64_t)sizeof(T));
   const int64_t gx = (cols + per - 1) / per;
   const dim3 grid((unsigned)(gx < 1 ? 1 : gx > (1 << 20) ? (1 << 20) : gx), (unsigned)(rows < 1 ? 1 : rows > 65535 ? 65535 : rows),
                   (unsigned)(a.n_groups > 65535 ? 65535 : a.n_groups));

@@ -405,6 +405,60 @@ __device__ __forceinline__ RawW load_raw(const uint8_t* row_q, const uint8_t* ro
   return r;
 }
 
+// A wave's corner of LDS for 32 rows of kRow bytes (padded by 16).
+template <int kRow>
+__device__ __forceinline__ uint8_t* lds_corner(uint8_t* lds, int wave) {
+  return lds + wave * 32 * (kRow + 16);
+}
+
+// Rows row0 + 32 t + (0..31) < row1, outputs m0 .. m0 + 32 kRF - 1 < m_len of
+// y = s * acc, acc as v_mfma_f32_32x32x16 leaves it (lane: token l % 32,
+// outputs 32 f + 8 q + 4 (l / 32) + r).  All LDS traffic is the wave's own.
+template <int kNT, int kRF, typename TY>
+__device__ __forceinline__ void store_rows(const f32x16_t (&acc)[kRF][kNT], float s, uint8_t* corner,
+                                           TY* __restrict__ y, int64_t ld, int64_t row0, int64_t row1, int64_t m0,
+                                           int64_t m_len) {
+  constexpr int kRow = 32 * kRF * (int)sizeof(TY), kPitch = kRow + 16, kE = 16 / (int)sizeof(TY);
+  constexpr int kLanes = kRow / 16, kTok = 64 / kLanes;  // lanes per row, rows per instruction
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int64_t m = m0 + (lane % kLanes) * kE;
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+    for (int f = 0; f < kRF; ++f)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v[4] = {s * acc[f][t][4 * q], s * acc[f][t][4 * q + 1], s * acc[f][t][4 * q + 2],
+                            s * acc[f][t][4 * q + 3]};
+        uint8_t* d = corner + l32 * kPitch + (32 * f + 8 * q + 4 * h) * sizeof(TY);
+        if constexpr (sizeof(TY) == 2)
+          *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else
+          *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 0; i < 32 / kTok; ++i) {
+      const int r = i * kTok + lane / kLanes;
+      const int64_t tok = row0 + 32 * t + r;
+      const uint4 u = *reinterpret_cast<const uint4*>(corner + r * kPitch + (lane % kLanes) * 16);
+      if (tok < row1 && m < m_len) {
+        TY* d = y + tok * ld + m;
+        TY w[kE];
+        __builtin_memcpy(w, &u, 16);
+        if (m + kE <= m_len) {
+          __builtin_memcpy(d, w, 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kE; ++e)
+            if (m + e < m_len) d[e] = w[e];
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
 template <int kNT, int kRF, int kDepth, int kWaves, bool kPart>
 __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b) {
   constexpr int kBT = 32 * kNT;              // tokens
@@ -412,6 +466,9 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   constexpr int kBuf = kBT * 256;            // bytes of an LDS buffer
   constexpr int kBufs = kDepth + 1;
   constexpr int kLoads = 2 * kNT;            // direct loads per wave and chunk
+  // steps by which activation operands are read ahead: one step of 8 or 16
+  // MFMAs covers the way through LDS, one of 1 or 2 does not
+  constexpr int kR = kNT >= 4 ? 1 : 3;
   constexpr int kAhead = (kDepth - 1) * (kLoads + (kPart ? 8 : 3) * kRF);  // loads issued behind the next chunk's at its barrier
   __shared__ __attribute__((aligned(1024))) uint8_t xs[kBufs * kBuf];
   int64_t tile, mt;
@@ -455,7 +512,7 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   };
 
   uint4 fa[2][kRF];
-  uint4 fb[2][kNT];
+  uint4 fb[kR + 1][kNT];
   f32x16_t acc[kRF][kNT];
 #pragma unroll
   for (int f = 0; f < kRF; ++f)
@@ -479,17 +536,17 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
     else if constexpr (e == 2) fa[set][f].z = v;
     else fa[set][f].w = v;
   };
-  // Step s of the chunk in slot u: the MFMAs of operand set s & 1; between
-  // them the operands of step s + 1 (LDS row address rd) and the direct loads
-  // d0 .. d1 - 1 of chunk dst into buffer dbuf.
+  // Step s of the chunk in slot u: its MFMAs; between them the weight operand
+  // of step s + 1, the activation operands of step s + kR (LDS row address rd)
+  // and the direct loads d0 .. d1 - 1 of chunk dst into buffer dbuf.
   auto step = [&](auto u, auto s, uint32_t rd, int dst, int dbuf, auto d0, auto d1) {
-    constexpr int set = s & 1;
+    constexpr int set = s & 1, bset = s % (kR + 1), rset = (s + kR) % (kR + 1);
     static_for<kRF * kNT>([&](auto N) {
       constexpr int n = N;
       if constexpr (n % 4 == 0 && d0 + n / 4 < d1) dload(dst, dbuf, d0 + n / 4);
       if constexpr (kRF * kNT < 4 && n == 1 && d0 + 1 < d1) dload(dst, dbuf, d0 + 1);
       if constexpr (n < kNT)
-        bread(std::integral_constant<int, set ^ 1>{}, rd, std::integral_constant<int, (s + 1) & 7>{}, N);
+        bread(std::integral_constant<int, rset>{}, rd, std::integral_constant<int, (s + kR) & 7>{}, N);
       constexpr int per = 4 / kNT > 0 ? 4 / kNT : 1;  // pairs per MFMA (kNT = 8: every other one)
       if constexpr (kNT < 8 || n % 2 == 0)
         static_for<per>([&](auto E) {
@@ -499,15 +556,15 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
         });
       constexpr int f = n / kNT, t = n % kNT;
       acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[set][f]),
-                                                          __builtin_bit_cast(bf16x8_t, fb[set][t]), acc[f][t], 0, 0, 0);
+                                                          __builtin_bit_cast(bf16x8_t, fb[bset][t]), acc[f][t], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
 
   // Chunk c sits in buffer (c - c_first) % kBufs and is loaded kDepth chunks
   // ahead, in four steps: the last step of chunk c - kBufs (whose buffer it
-  // takes: that chunk's last reads precede the barrier before its last step)
-  // and the first three of the chunk after that.  Past the end the final
+  // takes: that chunk's last reads precede its barrier) and the first three of
+  // the chunk after that.  Past the end the final
   // chunk is loaded again, into buffers that are read no more, so that no
   // branch breaks the schedule and the counted waits hold.
   static_for<kDepth>([&](auto d) {
@@ -519,8 +576,8 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   for (int i = 0; i < kLoads / 4; ++i) dload(min(c_first + kDepth, end), kDepth, i);
   wait_loads<0>();
   __syncthreads();
-  static_for<kNT>([&](auto t) {
-    bread(std::integral_constant<int, 0>{}, rd0, std::integral_constant<int, 0>{}, t);
+  static_for<kR>([&](auto i) {
+    static_for<kNT>([&](auto t) { bread(i, rd0, i, t); });
   });
   static_for<4 * kRF>([&](auto K) {
     decode(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{},
@@ -533,14 +590,16 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
     const int nbuf = buf + 1 == kBufs ? 0 : buf + 1, pbuf = buf == 0 ? kBufs - 1 : buf - 1;
     const uint32_t rd = rd0 + buf * kBuf, rd_next = rd0 + nbuf * kBuf;
     wload(std::integral_constant<int, (u + kDepth) % kBufs>{}, dst1);
-    static_for<7>([&](auto s) {
-      constexpr int q0 = s < 3 ? (s + 1) * kLoads / 4 : 0, q1 = s < 3 ? (s + 2) * kLoads / 4 : 0;
-      step(u, s, rd, dst1, pbuf, std::integral_constant<int, q0>{}, std::integral_constant<int, q1>{});
+    static_for<8>([&](auto s) {
+      if constexpr (s == 8 - kR) {
+        wait_loads<kAhead>();  // the next chunk has landed; this one's last operands are in registers
+        block_sync();
+      }
+      // loads: quarters, from the last step on
+      constexpr int q0 = s < 3 ? (s + 1) * kLoads / 4 : 0, q1 = s < 3 ? (s + 2) * kLoads / 4 : s == 7 ? kLoads / 4 : 0;
+      step(u, s, s < 8 - kR ? rd : rd_next, s == 7 ? dst2 : dst1, s == 7 ? buf : pbuf,
+           std::integral_constant<int, q0>{}, std::integral_constant<int, q1>{});
     });
-    wait_loads<kAhead>();  // the next chunk has landed; this one's last operands are in registers
-    block_sync();
-    step(u, std::integral_constant<int, 7>{}, rd_next, dst2, buf, std::integral_constant<int, 0>{},
-         std::integral_constant<int, kLoads / 4>{});
     return c < end;
   };
   if constexpr (kDepth == 1) {
@@ -556,27 +615,21 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
     for (int c = c_first; static_all<kBufs>([&](auto u) { return chunk(u, c + u, u); }); c += kBufs) {
     }
   }
-  wait_loads<0>();  // the repeated loads: nothing lands after the workgroup has ended
+  wait_loads<0>();  // the repeated loads have landed
+  __syncthreads();  // in every wave: LDS is free
 
+  // The wave's outputs leave through its own corner of LDS, 32 tokens at a
+  // time, as whole rows of kWM outputs: a lane's four neighbouring outputs
+  // alone would put 8 bytes on each of 32 lines per store instruction.
   const float sc = out_scale(b.a, p.g);
-  float* part = b.splits > 1 ? b.part + (blockIdx.y * b.a.n_groups + p.g) * b.a.rows * c_out : nullptr;
-#pragma unroll
-  for (int t = 0; t < kNT; ++t) {
-    const int64_t tok = p.row0 + 32 * t + l32;
-    if (tok >= p.row1) continue;
-#pragma unroll
-    for (int f = 0; f < kRF; ++f)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t o = m0 + 32 * f + 8 * q + 4 * h;
-        if (o >= c_out) continue;
-        const float v[4] = {sc * acc[f][t][4 * q], sc * acc[f][t][4 * q + 1], sc * acc[f][t][4 * q + 2],
-                            sc * acc[f][t][4 * q + 3]};
-        if (part) store4(part + tok * c_out + o, c_out - o, v);
-        else if (b.a.y_dtype == 1) store4(reinterpret_cast<uint16_t*>(p.y) + tok * b.a.ld_y + o, c_out - o, v);
-        else store4(reinterpret_cast<float*>(p.y) + tok * b.a.ld_y + o, c_out - o, v);
-      }
-  }
+  float* const part = b.splits > 1 ? b.part + (blockIdx.y * b.a.n_groups + p.g) * b.a.rows * c_out : nullptr;
+  if (part) store_rows<kNT, kRF>(acc, sc, lds_corner<kWM * 4>(xs, wave), part, c_out, p.row0, p.row1, m0, c_out);
+  else if (b.a.y_dtype == 1)
+    store_rows<kNT, kRF>(acc, sc, lds_corner<kWM * 4>(xs, wave), reinterpret_cast<uint16_t*>(p.y), b.a.ld_y, p.row0,
+                         p.row1, m0, c_out);
+  else
+    store_rows<kNT, kRF>(acc, sc, lds_corner<kWM * 4>(xs, wave), reinterpret_cast<float*>(p.y), b.a.ld_y, p.row0,
+                         p.row1, m0, c_out);
 }
 
 // ---------------------------------------------------------------------------

@@ -18,24 +18,11 @@
 // consecutive outputs of one token and leave in one store.
 #include <math.h>
 
-#include <utility>
-
 #include "lh_internal.h"
 #include "lh_rows.h"
 
 namespace lh {
 namespace {
-
-// f(integral_constant 0), ..., f(integral_constant N - 1): a loop whose index
-// is a constant for the front end, so that what it indexes is never memory.
-template <typename F, int... I>
-__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  static_for_impl(f, std::make_integer_sequence<int, N>{});
-}
 
 // f(0) && ... && f(N - 1), up to the first false.
 template <typename F, int... I>
@@ -45,13 +32,6 @@ __device__ __forceinline__ bool static_all_impl(F&& f, std::integer_sequence<int
 template <int N, typename F>
 __device__ __forceinline__ bool static_all(F&& f) {
   return static_all_impl(f, std::make_integer_sequence<int, N>{});
-}
-
-// A wave-uniform value into scalar registers.
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
 // Rows [row0, row1) of group g that tile `t` of the ragged rows covers, with
@@ -469,7 +449,8 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   // steps by which activation operands are read ahead: one step of 8 or 16
   // MFMAs covers the way through LDS, one of 1 or 2 does not
   constexpr int kR = kNT >= 4 ? 1 : 3;
-  constexpr int kAhead = (kDepth - 1) * (kLoads + (kPart ? 8 : 3) * kRF);  // loads issued behind the next chunk's at its barrier
+  // loads issued behind the next chunk's by its barrier (the counter holds 63)
+  constexpr int kAheadAll = (kDepth - 1) * (kLoads + (kPart ? 8 : 3) * kRF), kAhead = kAheadAll < 63 ? kAheadAll : 63;
   __shared__ __attribute__((aligned(1024))) uint8_t xs[kBufs * kBuf];
   int64_t tile, mt;
   big_tile(blockIdx.x, b.a.ragged, b.m_tiles, b.t_tiles, tile, mt);
@@ -974,28 +955,6 @@ __global__ __launch_bounds__(kThreads) void pack_rows_kernel(const TX* __restric
 // The lanes' sums are added by xor shuffles at the end, in a fixed order.
 // ---------------------------------------------------------------------------
 constexpr int kSpan = 2048;
-
-// Sums over the wave of kN values (a power of two): lane l gets the sum of
-// value l / (64 / kN).  Each of the first steps exchanges half of the values
-// with the other half of the lanes, so 2 kN shuffles do instead of 6 kN.
-template <int kN>
-__device__ __forceinline__ float wave_sums(float (&v)[kN]) {
-  const int lane = threadIdx.x & 63;
-  static_for<6>([&](auto S) {
-    constexpr int off = 32 >> S, live = kN >> S;  // values a lane still carries
-    if constexpr (live > 1) {
-      const bool upper = (lane & off) != 0;
-#pragma unroll
-      for (int i = 0; i < live / 2; ++i) {
-        const float give = upper ? v[i] : v[i + live / 2], keep = upper ? v[i + live / 2] : v[i];
-        v[i] = keep + __shfl_xor(give, off);
-      }
-    } else {
-      v[0] += __shfl_xor(v[0], off);
-    }
-  });
-  return v[0];
-}
 
 template <int i>
 __device__ __forceinline__ bf16x2_t nibbles2(uint32_t pk) {

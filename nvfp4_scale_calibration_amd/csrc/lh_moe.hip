@@ -37,11 +37,28 @@ __device__ __forceinline__ int expert_of(const TI* __restrict__ ids, int64_t a, 
   return (v >= 0 && v < (TI)n_groups) ? (int)v : n_groups;  // n_groups: no expert
 }
 
+// The first kHold * 64 assignments of a wave's share, looked up once: all of
+// them in a chunk of the usual size.
+constexpr int kHold = 4;
+template <typename TI>
+__device__ __forceinline__ void hold_share(const TI* __restrict__ ids, int64_t a0, int64_t a1, int n_groups,
+                                           int (&held)[kHold]) {
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) {
+    const int64_t a = a0 + 64 * i + (threadIdx.x & 63);
+    held[i] = a < a1 ? expert_of(ids, a, n_groups) : -1;
+  }
+}
+
 // counts[wave][bin] += this wave's share of the chunk; bins 0..n_groups.
 template <typename TI>
 __device__ __forceinline__ void count_share(const TI* __restrict__ ids, int64_t a0, int64_t a1, int n_groups,
-                                            unsigned int* mine) {
-  for (int64_t a = a0 + (threadIdx.x & 63); a < a1; a += 64) atomicAdd(&mine[expert_of(ids, a, n_groups)], 1u);
+                                            const int (&held)[kHold], unsigned int* mine) {
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (held[i] >= 0) atomicAdd(&mine[held[i]], 1u);
+  for (int64_t a = a0 + 64 * kHold + (threadIdx.x & 63); a < a1; a += 64)
+    atomicAdd(&mine[expert_of(ids, a, n_groups)], 1u);
 }
 
 // The wave's share [a0, a1) of chunk `c`.
@@ -57,12 +74,14 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(const TI* __res
                                                                  int n_groups, int* __restrict__ hist) {
   extern __shared__ unsigned int counts[];  // [kSortWaves][n_groups + 1]
   const int bins = n_groups + 1;
-  for (int i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) counts[i] = 0u;
-  __syncthreads();
   int64_t a0, a1;
   const int wave = threadIdx.x >> 6;
   wave_share(n, chunk, blockIdx.x, wave, a0, a1);
-  count_share(ids, a0, a1, n_groups, counts + wave * bins);
+  int held[kHold];
+  hold_share(ids, a0, a1, n_groups, held);
+  for (int i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) counts[i] = 0u;
+  __syncthreads();
+  count_share(ids, a0, a1, n_groups, held, counts + wave * bins);
   __syncthreads();
   for (int e = threadIdx.x; e < bins; e += kSortThreads) {
     unsigned int s = 0;
@@ -82,17 +101,20 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const TI* __rest
   unsigned int* const total = counts + kSortWaves * bins;
   __shared__ unsigned int wave_sum[kSortWaves];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  for (int i = tid; i < kSortWaves * bins; i += kSortThreads) counts[i] = 0u;
-  __syncthreads();
   int64_t a0, a1;
   wave_share(n, chunk, blockIdx.x, wave, a0, a1);
-  count_share(ids, a0, a1, n_groups, counts + wave * bins);
+  int held[kHold];
+  hold_share(ids, a0, a1, n_groups, held);
+  for (int i = tid; i < kSortWaves * bins; i += kSortThreads) counts[i] = 0u;
+  __syncthreads();
+  count_share(ids, a0, a1, n_groups, held, counts + wave * bins);
   __syncthreads();
   // per expert: its rows in all chunks (total) and in earlier ones, and its
   // waves' first rows within them
   for (int e = tid; e < bins; e += kSortThreads) {
     unsigned int before = 0, all = 0;
     if (n_chunks > 1) {
+#pragma unroll 16
       for (int64_t c = 0; c < n_chunks; ++c) {
         const unsigned int h = (unsigned int)hist[c * bins + e];
         before += c < (int64_t)blockIdx.x ? h : 0u;
@@ -134,9 +156,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const TI* __rest
   int bits = 0;
   while ((1 << bits) < bins) ++bits;
   unsigned int* const mine = counts + wave * bins;
-  for (int64_t a = a0; a < a1; a += 64) {  // the same trip count for every lane of the wave
-    const bool have = a + lane < a1;
-    const int e = have ? expert_of(ids, a + lane, n_groups) : n_groups;
+  // 64 assignments from `a` on, e the expert of this lane's (-1: past the share)
+  auto place = [&](int64_t a, int e) {
+    const bool have = e >= 0;
     unsigned long long same = __ballot(have);
     for (int b = 0; b < bits; ++b) {
       const unsigned long long set = __ballot((e >> b) & 1);
@@ -157,7 +179,12 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const TI* __rest
       position[at] = live ? (int)row : -1 - (int)row;
       if (order) order[row] = live ? (int)at : -1 - (int)at;
     }
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (a0 + 64 * i < a1) place(a0 + 64 * i, held[i]);  // a wave-uniform branch
+  for (int64_t a = a0 + 64 * kHold; a < a1; a += 64)  // the same trip count for every lane of the wave
+    place(a, a + lane < a1 ? expert_of(ids, a + lane, n_groups) : -1);
 }
 
 // ---------------------------------------------------------------------------
@@ -171,33 +198,49 @@ struct Vec {
 };
 
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, int n, float (&v)[Vec<T>::kN]) {
+__device__ __forceinline__ uint4 load_raw16(const T* p, int n) {
+  if (n >= Vec<T>::kN) return load_u128(p);
   T raw[Vec<T>::kN];
-  if (n >= Vec<T>::kN) {
-    __builtin_memcpy(raw, p, 16);
-  } else {
 #pragma unroll
-    for (int i = 0; i < Vec<T>::kN; ++i) raw[i] = i < n ? p[i] : T(0);
-  }
-#pragma unroll
-  for (int i = 0; i < Vec<T>::kN; ++i) v[i] = load_as_f32<T>(raw, i);
+  for (int i = 0; i < Vec<T>::kN; ++i) raw[i] = i < n ? p[i] : T(0);
+  return __builtin_bit_cast(uint4, raw);
 }
-
-__device__ __forceinline__ void to_bits(float v, float& o) { o = v; }
-__device__ __forceinline__ void to_bits(float v, uint16_t& o) { o = f32_to_bf16_bits(v); }
-
 template <typename T>
-__device__ __forceinline__ void store_vec(T* p, int n, const float (&v)[Vec<T>::kN]) {
-  T raw[Vec<T>::kN];
+__device__ __forceinline__ void values_of(const uint4 u, float (&v)[Vec<T>::kN]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < Vec<T>::kN; ++i) to_bits(v[i], raw[i]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+// The first n values of 16 bytes.
+template <typename T>
+__device__ __forceinline__ void store_raw16(T* p, int n, const uint4 u) {
   if (n >= Vec<T>::kN) {
-    __builtin_memcpy(p, raw, 16);
+    __builtin_memcpy(p, &u, 16);
   } else {
+    T raw[Vec<T>::kN];
+    __builtin_memcpy(raw, &u, 16);
 #pragma unroll
     for (int i = 0; i < Vec<T>::kN; ++i)
       if (i < n) p[i] = raw[i];
   }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 raw_of(const float (&v)[Vec<T>::kN]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    else w[i] = __float_as_uint(v[i]);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The row an entry of `position` names, or -1 - row for an assignment without
@@ -208,6 +251,17 @@ __device__ __forceinline__ int64_t row_of(int entry, int64_t n_rows) {
   return entry;
 }
 
+// The wave's unit of work, as scalars: what depends on it (positions,
+// weights, row addresses) then comes through the scalar cache.
+__device__ __forceinline__ int64_t wave_unit() {
+  const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  return (int64_t)blockIdx.x * (kThreads / 64) + w;
+}
+
+// Assignments of a token that are looked up and moved together: their loads
+// are all in flight before the first is used.
+constexpr int kAtOnce = 8;
+
 // One wave per (token, 64-lane span of columns): the token's span is read
 // once and written top_k times.
 template <typename T>
@@ -216,18 +270,24 @@ __global__ __launch_bounds__(kThreads) void moe_dispatch_kernel(const T* __restr
                                                                 const int* __restrict__ position, T* __restrict__ xs,
                                                                 int64_t ld_xs, int64_t n_rows) {
   constexpr int kN = Vec<T>::kN;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  const int64_t unit = wave_unit();
   const int64_t t = unit / spans;
+  if (t >= n_tok) return;
   const int64_t c = (unit - t * spans) * (64 * kN) + (threadIdx.x & 63) * kN;
-  if (t >= n_tok || c >= cols) return;
+  if (c >= cols) return;
   const int n = (int)min((int64_t)kN, cols - c);
-  float v[kN];
-  const float zero[kN] = {};
-  load_vec<T>(x + t * ld_x + c, n, v);
-  for (int k = 0; k < top_k; ++k) {
-    const int64_t r = row_of(position[t * top_k + k], n_rows);
-    if (r >= 0) store_vec<T>(xs + r * ld_xs + c, n, v);
-    else if (r != INT64_MIN) store_vec<T>(xs + (-1 - r) * ld_xs + c, n, zero);
+  const uint4 v = load_raw16<T>(x + t * ld_x + c, n), zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int k0 = 0; k0 < top_k; k0 += kAtOnce) {
+    int at[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) at[k] = position[t * top_k + min(k0 + k, top_k - 1)];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int64_t r = row_of(at[k], n_rows);
+      if (k0 + k >= top_k || r == INT64_MIN) continue;
+      if (r >= 0) store_raw16<T>(xs + r * ld_xs + c, n, v);
+      else store_raw16<T>(xs + (-1 - r) * ld_xs + c, n, zero);
+    }
   }
 }
 
@@ -238,73 +298,99 @@ __global__ __launch_bounds__(kThreads) void moe_combine_kernel(const T* __restri
                                                                const float* __restrict__ weights, T* __restrict__ y,
                                                                int64_t ld_y) {
   constexpr int kN = Vec<T>::kN;
-  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  const int64_t unit = wave_unit();
   const int64_t t = unit / spans;
+  if (t >= n_tok) return;
   const int64_t c = (unit - t * spans) * (64 * kN) + (threadIdx.x & 63) * kN;
-  if (t >= n_tok || c >= cols) return;
+  if (c >= cols) return;
   const int n = (int)min((int64_t)kN, cols - c);
   float sum[kN] = {};
-  for (int k = 0; k < top_k; ++k) {
-    const int64_t r = row_of(position[t * top_k + k], n_rows);
-    if (r < 0) continue;
-    const float w = weights ? weights[t * top_k + k] : 1.0f;
-    float v[kN];
-    load_vec<T>(ys + r * ld_ys + c, n, v);
+  for (int k0 = 0; k0 < top_k; k0 += kAtOnce) {
+    uint4 raw[kAtOnce];
+    float w[kAtOnce];
+    bool live[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) sum[i] = __builtin_fmaf(w, v[i], sum[i]);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int64_t a = t * top_k + min(k0 + k, top_k - 1);
+      const int64_t r = row_of(position[a], n_rows);
+      live[k] = k0 + k < top_k && r >= 0;
+      w[k] = weights ? weights[a] : 1.0f;
+      if (live[k]) raw[k] = load_raw16<T>(ys + r * ld_ys + c, n);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (live[k]) {
+        float v[kN];
+        values_of<T>(raw[k], v);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) sum[i] = __builtin_fmaf(w[k], v[i], sum[i]);
+      }
   }
-  store_vec<T>(y + t * ld_y + c, n, sum);
+  store_raw16<T>(y + t * ld_y + c, n, raw_of<T>(sum));
 }
 
-// One workgroup per token: dys rows written, the dots reduced over lanes
-// (xor shuffles), then the waves' sums in wave order.
+// One workgroup per token, kAtOnce assignments at a time: dy's columns are
+// read once for all of them, each thread's dots are reduced over the wave
+// (the lanes exchange halves of the values), then over the waves in order.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void moe_combine_grad_kernel(
     const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ ys, int64_t ld_ys, int64_t n_rows, int64_t cols,
     int top_k, const int* __restrict__ position, const float* __restrict__ weights, T* __restrict__ dys,
     int64_t ld_dys, float* __restrict__ dw) {
   constexpr int kN = Vec<T>::kN;
-  __shared__ float part[kThreads / 64];
+  __shared__ float part[kThreads / 64][kAtOnce];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  for (int k = 0; k < top_k; ++k) {  // position is the same for the whole workgroup: so are the branches
-    const int64_t a = t * top_k + k;
-    const int64_t r = row_of(position[a], n_rows);
-    if (r < 0) {
-      if (r != INT64_MIN && dys) {
-        const float zero[kN] = {};
-        for (int64_t c = (int64_t)tid * kN; c < cols; c += (int64_t)kThreads * kN)
-          store_vec<T>(dys + (-1 - r) * ld_dys + c, (int)min((int64_t)kN, cols - c), zero);
-      }
-      if (tid == 0 && dw) dw[a] = 0.0f;
-      continue;
+  for (int k0 = 0; k0 < top_k; k0 += kAtOnce) {
+    int64_t row[kAtOnce];  // the same for the whole workgroup
+    float w[kAtOnce], dot[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int64_t a = t * top_k + min(k0 + k, top_k - 1);
+      row[k] = k0 + k < top_k ? row_of(position[a], n_rows) : INT64_MIN;
+      w[k] = weights ? weights[a] : 1.0f;
+      dot[k] = 0.0f;
     }
-    const float w = weights ? weights[a] : 1.0f;
-    float dot = 0.0f;
     for (int64_t c = (int64_t)tid * kN; c < cols; c += (int64_t)kThreads * kN) {
       const int n = (int)min((int64_t)kN, cols - c);
-      float d[kN], v[kN];
-      load_vec<T>(dy + t * ld_dy + c, n, d);
+      uint4 raw[kAtOnce];
+      const uint4 rawd = load_raw16<T>(dy + t * ld_dy + c, n);
       if (dw) {
-        load_vec<T>(ys + r * ld_ys + c, n, v);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) dot = __builtin_fmaf(d[i], v[i], dot);
+        for (int k = 0; k < kAtOnce; ++k)
+          if (row[k] >= 0) raw[k] = load_raw16<T>(ys + row[k] * ld_ys + c, n);
       }
-      if (dys) {
+      float d[kN];
+      values_of<T>(rawd, d);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) d[i] *= w;
-        store_vec<T>(dys + r * ld_dys + c, n, d);
+      for (int k = 0; k < kAtOnce; ++k) {
+        if (row[k] == INT64_MIN) continue;
+        if (row[k] < 0) {
+          if (dys) store_raw16<T>(dys + (-1 - row[k]) * ld_dys + c, n, make_uint4(0u, 0u, 0u, 0u));
+          continue;
+        }
+        if (dw) {
+          float v[kN];
+          values_of<T>(raw[k], v);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) dot[k] = __builtin_fmaf(d[i], v[i], dot[k]);
+        }
+        if (dys) {
+          float g[kN];
+#pragma unroll
+          for (int i = 0; i < kN; ++i) g[i] = d[i] * w[k];
+          store_raw16<T>(dys + row[k] * ld_dys + c, n, raw_of<T>(g));
+        }
       }
     }
     if (dw) {
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) dot += __shfl_xor(dot, off);
-      if (lane == 0) part[wave] = dot;
+      const float s = wave_sums(dot);  // lane l: assignment l / (64 / kAtOnce)
+      if (lane % (64 / kAtOnce) == 0) part[wave][lane / (64 / kAtOnce)] = s;
       __syncthreads();
-      if (tid == 0) {
-        float s = part[0];
-        for (int i = 1; i < kThreads / 64; ++i) s += part[i];
-        dw[a] = s;
+      if (tid < kAtOnce && k0 + tid < top_k) {
+        float sum = part[0][tid];
+        for (int i = 1; i < kThreads / 64; ++i) sum += part[i][tid];
+        dw[t * top_k + k0 + tid] = sum;
       }
       __syncthreads();
     }

@@ -3,6 +3,8 @@
 // lh_moe.hip, lh_quant.hip).
 #pragma once
 
+#include <utility>
+
 #include "lh_device.h"
 
 namespace lh {
@@ -11,6 +13,46 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// f(integral_constant 0), ..., f(integral_constant N - 1): a loop whose index
+// is a constant for the front end, so that what it indexes is never memory.
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// A wave-uniform value into scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Sums over the wave of kN values (a power of two): lane l gets the sum of
+// value l / (64 / kN).  Each of the first steps exchanges half of the values
+// with the other half of the lanes, so 2 kN shuffles do instead of 6 kN.
+template <int kN>
+__device__ __forceinline__ float wave_sums(float (&v)[kN]) {
+  const int lane = threadIdx.x & 63;
+  static_for<6>([&](auto S) {
+    constexpr int off = 32 >> S, live = kN >> S;  // values a lane still carries
+    if constexpr (live > 1) {
+      const bool upper = (lane & off) != 0;
+#pragma unroll
+      for (int i = 0; i < live / 2; ++i) {
+        const float give = upper ? v[i] : v[i + live / 2], keep = upper ? v[i + live / 2] : v[i];
+        v[i] = keep + __shfl_xor(give, off);
+      }
+    } else {
+      v[0] += __shfl_xor(v[0], off);
+    }
+  });
+  return v[0];
+}
 
 // 16 and 8 bytes from any address (global memory takes unaligned accesses;
 // memcpy says so to the compiler, which emits one wide load).

@@ -328,6 +328,16 @@ __device__ __forceinline__ void big_tile(int64_t b, bool ragged, int64_t m_tiles
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
+// The same for 4 bytes, 2 bytes and 1 byte (zero-extended to 4) per lane: lane l at lds + 4 l.
+__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma2(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ushort %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma1(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
 #pragma clang diagnostic pop
 // A barrier that waits for this wave's LDS reads but for none of its loads
 // from global memory (which __syncthreads would drain).
@@ -555,8 +565,9 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   });
 #pragma unroll
   for (int i = 0; i < kLoads / 4; ++i) dload(min(c_first + kDepth, end), kDepth, i);
-  wait_loads<0>();
-  __syncthreads();
+  constexpr int kStart = kAheadAll + kLoads / 4;
+  wait_loads<kStart < 63 ? kStart : 63>();  // the first chunk has landed
+  block_sync();
   static_for<kR>([&](auto i) {
     static_for<kNT>([&](auto t) { bread(i, rd0, i, t); });
   });
@@ -614,6 +625,345 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
 }
 
 // ---------------------------------------------------------------------------
+// 32 tokens a tile (2 x 16): 128 outputs per workgroup of eight waves, 16
+// outputs each, v_mfma_f32_16x16x32_bf16.
+//
+// Here the time is the latency of the packed weights, and what counts is how
+// many bytes are under way.  So nothing is loaded into registers (the
+// compiler's waits for such loads know nothing of the direct ones beside them
+// and drain those too): activations, packed weights and codes all go to LDS
+// directly, kBufs pairs of chunks, with every wait counted.  A wave's weights
+// are its own, so the barrier of a chunk is for the activations alone.
+//
+// Per chunk of 128 weights lane group g (l / 16) takes weights 32 g .. 32 g + 31
+// of its row and MFMA step i (of 4) weights 32 g + 8 i .. + 7.  Activations as
+// in linear_big_kernel; weights 64 bytes a row, the wave's 1 KiB in one
+// instruction; codes one 32-bit word per lane, its two codes (kW4: one word
+// each).  kW4: rows that are not 16-byte aligned, in 4-byte pieces.
+// ---------------------------------------------------------------------------
+constexpr int kSmallM = 128;
+
+template <int kBufs, bool kW4>
+__global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
+  constexpr int kNT = 2, kBT = 16 * kNT;
+  constexpr int kXBytes = kBT * 256, kWBytes = 8192, kCBytes = kW4 ? 4096 : 2048;
+  constexpr int kBuf = kXBytes + kWBytes + kCBytes;   // of one chunk
+  constexpr int kWLoads = kW4 ? 4 : 1, kCLoads = kW4 ? 2 : 1;
+  constexpr int kLoads = 1 + kWLoads + kCLoads;         // per wave and chunk
+  constexpr int kAheadAll = (kBufs - 2) * 2 * kLoads, kAhead = kAheadAll < 63 ? kAheadAll : 63;
+  constexpr int kR = 3;                                 // steps by which activation operands are read ahead
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kBufs * 2 * kBuf];
+  int64_t tile, mt;
+  big_tile(blockIdx.x, b.a.ragged, b.m_tiles, b.t_tiles, tile, mt);
+  Place p;
+  if (!place_of<kBT>(b.a, tile, p)) return;  // the whole workgroup
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c_in = b.a.c_in, c_out = b.a.c_out;
+  const int64_t m0 = mt * kSmallM + 16 * wave;
+  const int c_first = (int)((int64_t)b.chunks * blockIdx.y / b.splits);
+  const int end = (int)((int64_t)b.chunks * (blockIdx.y + 1) / b.splits) - 1;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+
+  const uint16_t* const xg = b.x + uniform((b.a.ragged ? 0 : p.g * b.gstride) + p.row0 * b.ld);
+  const int last = (int)(p.row1 - p.row0) - 1;
+  const int xt = 4 * wave + (lane >> 4);  // the token this lane loads from
+  const uint32_t xoff = (uint32_t)min(xt, last) * (uint32_t)(b.ld * 2) + (uint32_t)(((lane & 15) ^ (xt & 15)) * 16);
+  // the wave's rows from its first one on (rows past the last one are the last one)
+  const int64_t w_row = c_in / 2, c_row = c_in / 16, o0 = min(m0, c_out - 1);
+  const uint8_t* const wg = b.a.packed + uniform((p.g * c_out + o0) * w_row);
+  const uint8_t* const cg = b.a.codes + uniform((p.g * c_out + o0) * c_row);
+  auto row_of = [&](int r) { return (uint32_t)(min(m0 + r, c_out - 1) - o0); };
+  // weights: row lane / 4, 16-byte piece lane % 4; or (kW4) rows 4 i + lane / 16, 4-byte piece lane % 16
+  uint32_t woff[kWLoads];
+#pragma unroll
+  for (int i = 0; i < kWLoads; ++i) woff[i] = row_of(kW4 ? 4 * i + (lane >> 4) : lane >> 2) * (uint32_t)w_row;
+  const uint32_t coff = row_of(l16) * (uint32_t)c_row;
+  const int w_last = b.w_chunks - 1;
+  const uint32_t left = (uint32_t)(c_in - (int64_t)w_last * kChunk);  // weights of a row's last chunk
+  // the loads of a chunk into buffer `at`; a piece past the row's end is the
+  // chunk's first one (finite weights that meet the zeros behind the
+  // activations' row)
+  int ld_c = c_first, ld_w = c_first % b.w_chunks;  // the next chunk to load, and that chunk of W (which repeats)
+  auto dload = [&](uint32_t at) {
+    dma16(xg + ld_c * kChunk, xoff, lds0 + at + 1024 * wave);
+    const uint32_t n = ld_w == w_last ? left : (uint32_t)kChunk;
+    const uint8_t* const wb = wg + ld_w * (kChunk / 2);
+    const uint8_t* const cb = cg + ld_w * (kChunk / 16);
+    if (ld_c < end) {
+      ++ld_c;
+      ld_w = ld_w == w_last ? 0 : ld_w + 1;
+    }
+    const uint32_t wd = lds0 + at + kXBytes + 1024 * wave, cd = lds0 + at + kXBytes + kWBytes + (kCBytes / 8) * wave;
+    if constexpr (!kW4) {
+      const uint32_t q = (lane & 3) * 32u < n ? (lane & 3) * 16u : 0u;
+      dma16(wb, woff[0] + q, wd);
+      dma2(cb, coff + (g * 32u < n ? g * 2u : 0u), cd);
+    } else {
+      const uint32_t q = l16 * 8u < n ? l16 * 4u : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dma4(wb, woff[i] + q, wd + 256 * i);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) dma1(cb, coff + (g * 32u + i * 16u < n ? g * 2u + i : 0u), cd + 256 * i);
+    }
+  };
+
+  uint4 fa[2], fb[kR + 1][kNT], raw, raw_next;
+  uint32_t code[2], code_next[2];
+  f32x4_t acc[kNT];
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  // activations: token 16 t + l16, piece 4 g + i; weights: row l16, piece g
+  const uint32_t rd0 = l16 * 256 + (((4 * g) ^ l16) * 16);
+  const uint32_t wrd = kXBytes + 1024 * wave + l16 * 64 + g * 16;
+  const uint32_t crd = kXBytes + kWBytes + (kCBytes / 8) * wave + lane * 4;
+  auto bread = [&](auto set, uint32_t at, auto i) {
+#pragma unroll
+    for (int t = 0; t < kNT; ++t)
+      fb[set][t] = *reinterpret_cast<const uint4*>(lds + at + (rd0 ^ (16 * i)) + 4096 * t);
+  };
+  // live: all ones, or zero past the last chunk (an odd one out is walked with zero scales)
+  auto wread = [&](uint32_t at, uint32_t live) {
+    raw_next = *reinterpret_cast<const uint4*>(lds + at + wrd);
+    code_next[0] = *reinterpret_cast<const uint32_t*>(lds + at + crd) & live;
+    if constexpr (kW4) code_next[1] = *reinterpret_cast<const uint32_t*>(lds + at + crd + 256) & live;
+  };
+  auto decode = [&](auto set, const uint4& r, const uint32_t (&cc)[2], auto i) {
+    const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
+    const float c = kW4 ? e4m3_to_f32<0>(i < 2 ? cc[0] : cc[1]) : e4m3_to_f32<(i >> 1)>(cc[0]);
+    fa[set] = units8_bf16(w, c);
+  };
+
+  for (int d = 0; d < 2 * kBufs; ++d) dload(d * kBuf);
+  constexpr int kStart = (kBufs - 1) * 2 * kLoads;
+  wait_loads<kStart < 63 ? kStart : 63>();  // the first two chunks have landed
+  block_sync();
+  std::integral_constant<int, 0> i0;
+  static_for<kR>([&](auto i) { bread(i, 0u, i); });
+  wread(0u, ~0u);
+  auto take = [&]() {
+    raw = raw_next;
+    code[0] = code_next[0];
+    if constexpr (kW4) code[1] = code_next[1];
+  };
+  take();
+  decode(i0, raw, code, i0);
+  uint32_t at = 0;
+  for (int c = c_first; c <= end; c += 2) {  // two chunks, eight steps
+    const uint32_t second = at + kBuf, next = at + 2 * kBuf == kBufs * 2 * kBuf ? 0u : at + 2 * kBuf;
+    static_for<8>([&](auto s) {
+      if constexpr (s == 1) wread(second, c < end ? ~0u : 0u);
+      constexpr int rs = s + kR, ns = s + 1;
+      bread(std::integral_constant<int, rs & 3>{}, rs >= 8 ? next : rs >= 4 ? second : at,
+            std::integral_constant<int, rs & 3>{});
+      if constexpr (s == 4) {
+        // the last operands of these two chunks are on their way to registers
+        // and the next two chunks have landed: past the barrier, in every
+        // wave, and these two's buffers can be loaded again
+        wait_loads<kAhead>();
+        wread(next, ~0u);
+        block_sync();
+        dload(at);
+        dload(second);
+      }
+      std::integral_constant<int, ns & 1> nset;
+      std::integral_constant<int, ns & 3> ni;
+      if constexpr ((ns & 3) == 0) take();
+      decode(nset, raw, code, ni);
+#pragma unroll
+      for (int t = 0; t < kNT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fa[s & 1]),
+                                                         __builtin_bit_cast(bf16x8_t, fb[s & 3][t]), acc[t], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    at = next;
+  }
+  wait_loads<0>();  // the repeated loads: nothing lands after the workgroup has ended
+
+  const float sc = out_scale(b.a, p.g);
+  float* const part = b.splits > 1 ? b.part + (blockIdx.y * b.a.n_groups + p.g) * b.a.rows * c_out : nullptr;
+  const int64_t m = m0 + 4 * g;
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+    const int64_t tok = p.row0 + 16 * t + l16;
+    if (tok >= p.row1 || m >= c_out) continue;
+    const float v[4] = {sc * acc[t][0], sc * acc[t][1], sc * acc[t][2], sc * acc[t][3]};
+    if (part) store4(part + tok * c_out + m, c_out - m, v);
+    else if (b.a.y_dtype == 1) store4(reinterpret_cast<uint16_t*>(p.y) + tok * b.a.ld_y + m, c_out - m, v);
+    else store4(reinterpret_cast<float*>(p.y) + tok * b.a.ld_y + m, c_out - m, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 tokens a tile: 32 outputs per workgroup, the contraction split over
+// its kW waves, v_mfma_f32_16x16x32_bf16.
+//
+// What counts is how many bytes of weights are under way and that nothing
+// stands still for anything else: every wave streams its own chunks of
+// activations (4 KiB), packed weights (2 KiB) and codes to its own part of LDS
+// by direct loads, kBufs chunks ahead, with counted waits, and no barrier is
+// met before the end, where the waves' sums are added in order.  (The
+// activations' repeated way to LDS is twice the weights' bytes, from L2.)
+//
+// Per chunk of 128 weights lane group g (l / 16) takes weights 32 g .. 32 g + 31
+// of its row and MFMA step i (of 4) weights 32 g + 8 i .. + 7.  LDS: 256 bytes a
+// token, slot q ^ (token & 15) holding 16-byte piece q; 64 bytes a row of
+// weights; one 32-bit word per lane and operand for its two codes (kW4: one
+// word each).  kW4: rows that are not 16-byte aligned, in 4-byte pieces.
+// ---------------------------------------------------------------------------
+constexpr int kSkinnyM = 32;
+
+template <int kW, int kBufs, bool kW4>
+__global__ __launch_bounds__(64 * kW, 2) void linear_skinny_kernel(BigArgs b) {
+  constexpr int kXBytes = 4096, kWBytes = 2048, kCBytes = kW4 ? 1024 : 512;
+  constexpr int kBuf = kXBytes + kWBytes + kCBytes;
+  constexpr int kWLoads = kW4 ? 8 : 2, kCLoads = kW4 ? 4 : 2, kLoads = 4 + kWLoads + kCLoads;
+  static_assert((kBufs - 1) * kLoads < 64, "the load counter");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kW * kBufs * kBuf];
+  int64_t tile, mt;
+  big_tile(blockIdx.x, b.a.ragged, b.m_tiles, b.t_tiles, tile, mt);
+  Place p;
+  if (!place_of<16>(b.a, tile, p)) return;  // the whole workgroup
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c_in = b.a.c_in, c_out = b.a.c_out, m0 = mt * kSkinnyM;
+  const int64_t share = (int64_t)blockIdx.y * kW + wave, shares = (int64_t)b.splits * kW;
+  const int c_first = (int)(b.chunks * share / shares);
+  const int end = (int)(b.chunks * (share + 1) / shares) - 1;  // < c_first: nothing to do
+
+  const uint16_t* const xg = b.x + uniform((b.a.ragged ? 0 : p.g * b.gstride) + p.row0 * b.ld);
+  const int last = (int)(p.row1 - p.row0) - 1;
+  uint32_t xoff[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 4 * i + (lane >> 4);
+    xoff[i] = (uint32_t)min(t, last) * (uint32_t)(b.ld * 2) + (uint32_t)(((lane & 15) ^ t) * 16);
+  }
+  const int64_t w_row = c_in / 2, c_row = c_in / 16;
+  const uint8_t* const wg = b.a.packed + uniform((p.g * c_out + m0) * w_row);
+  const uint8_t* const cg = b.a.codes + uniform((p.g * c_out + m0) * c_row);
+  auto row_of = [&](int r) { return (uint32_t)(min(m0 + r, c_out - 1) - m0); };
+  // weights: rows 16 i + lane / 4, piece lane % 4; or (kW4) rows 4 i + lane / 16, 4-byte piece lane % 16
+  uint32_t woff[kWLoads], coff[2];
+#pragma unroll
+  for (int i = 0; i < kWLoads; ++i)
+    woff[i] = row_of(kW4 ? 4 * i + (lane >> 4) : 16 * i + (lane >> 2)) * (uint32_t)w_row;
+#pragma unroll
+  for (int f = 0; f < 2; ++f) coff[f] = row_of(16 * f + l16) * (uint32_t)c_row;
+  const int w_last = b.w_chunks - 1;
+  const uint32_t left = (uint32_t)(c_in - (int64_t)w_last * kChunk);  // weights of a row's last chunk
+  uint8_t* const mine = lds + wave * (kBufs * kBuf);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)mine);
+  int ld_c = c_first, ld_w = c_first % b.w_chunks;  // the next chunk to load, and that chunk of W (which repeats)
+  // that chunk into buffer `at`; a piece past the row's end is the chunk's
+  // first one (finite weights that meet the zeros behind the activations' row)
+  auto dload = [&](uint32_t at) {
+    const uint16_t* const xb = xg + ld_c * kChunk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dma16(xb, xoff[i], lds0 + at + 1024 * i);
+    const uint32_t n = ld_w == w_last ? left : (uint32_t)kChunk;
+    const uint8_t* const wb = wg + ld_w * (kChunk / 2);
+    const uint8_t* const cb = cg + ld_w * (kChunk / 16);
+    const uint32_t wd = lds0 + at + kXBytes, cd = wd + kWBytes;
+    const uint32_t q = kW4 ? (l16 * 8u < n ? l16 * 4u : 0u) : ((lane & 3) * 32u < n ? (lane & 3) * 16u : 0u);
+#pragma unroll
+    for (int i = 0; i < kWLoads; ++i) {
+      if constexpr (kW4) dma4(wb, woff[i] + q, wd + 256 * i);
+      else dma16(wb, woff[i] + q, wd + 1024 * i);
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      if constexpr (!kW4) {
+        dma2(cb, coff[f] + (g * 32u < n ? g * 2u : 0u), cd + 256 * f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          dma1(cb, coff[f] + (g * 32u + i * 16u < n ? g * 2u + i : 0u), cd + 512 * f + 256 * i);
+      }
+    }
+    if (ld_c < end) {  // past the end the last chunk again, into buffers that are read no more
+      ++ld_c;
+      ld_w = ld_w == w_last ? 0 : ld_w + 1;
+    }
+  };
+
+  // a chunk's operands in registers
+  struct Regs {
+    uint4 x[4], w[2];
+    uint32_t c[2], c1[2];
+  };
+  auto lread = [&](uint32_t at) {
+    Regs r;
+    const uint8_t* const q = mine + at;
+    static_for<4>([&](auto i) {
+      r.x[i] = *reinterpret_cast<const uint4*>(q + l16 * 256 + (((4 * g + i) ^ l16) * 16));
+    });
+    static_for<2>([&](auto f) {
+      r.w[f] = *reinterpret_cast<const uint4*>(q + kXBytes + 1024 * f + l16 * 64 + g * 16);
+      const uint8_t* const c = q + kXBytes + kWBytes + (kW4 ? 512 : 256) * f + lane * 4;
+      r.c[f] = *reinterpret_cast<const uint32_t*>(c);
+      if constexpr (kW4) r.c1[f] = *reinterpret_cast<const uint32_t*>(c + 256);
+    });
+    return r;
+  };
+  f32x4_t acc[2] = {f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}};
+  if (c_first <= end) {
+    for (int d = 0; d < kBufs; ++d) dload(d * kBuf);
+    wait_loads<(kBufs - 1) * kLoads>();
+    Regs r = lread(0);
+    uint32_t at = 0;
+    for (int c = c_first; c <= end; ++c) {
+      const uint32_t next = at + kBuf == kBufs * kBuf ? 0u : at + kBuf;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this chunk's operands are in registers:
+      dload(at);                                          // its buffer is free
+      wait_loads<(kBufs - 1) * kLoads>();                 // the next chunk has landed
+      const Regs n = lread(next);
+      static_for<4>([&](auto i) {
+        static_for<2>([&](auto f) {
+          const uint32_t w = i == 0 ? r.w[f].x : i == 1 ? r.w[f].y : i == 2 ? r.w[f].z : r.w[f].w;
+          const float s = kW4 ? e4m3_to_f32<0>(i < 2 ? r.c[f] : r.c1[f]) : e4m3_to_f32<(i >> 1)>(r.c[f]);
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, units8_bf16(w, s)),
+                                                           __builtin_bit_cast(bf16x8_t, r.x[i]), acc[f], 0, 0, 0);
+        });
+      });
+      r = n;
+      at = next;
+    }
+    wait_loads<0>();  // the repeated loads have landed
+  }
+
+  // the waves' sums, added in their order: output row 16 f + 4 g + e of token l16 at [f][lane]
+  __syncthreads();
+  float4* const sums = reinterpret_cast<float4*>(lds);
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+    sums[(wave * 2 + f) * 64 + lane] = make_float4(acc[f][0], acc[f][1], acc[f][2], acc[f][3]);
+  __syncthreads();
+  if (wave >= 2) return;
+  const int f = wave;
+  float v[4] = {};
+#pragma unroll
+  for (int q = 0; q < kW; ++q) {
+    const float4 u = sums[(q * 2 + f) * 64 + lane];
+    v[0] = q == 0 ? u.x : v[0] + u.x;
+    v[1] = q == 0 ? u.y : v[1] + u.y;
+    v[2] = q == 0 ? u.z : v[2] + u.z;
+    v[3] = q == 0 ? u.w : v[3] + u.w;
+  }
+  const float sc = out_scale(b.a, p.g);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] *= sc;
+  const int64_t tok = p.row0 + l16, m = m0 + 16 * f + 4 * g;
+  if (tok >= p.row1 || m >= c_out) return;
+  if (b.splits > 1)
+    store4(b.part + (blockIdx.y * b.a.n_groups + p.g) * b.a.rows * c_out + tok * c_out + m, c_out - m, v);
+  else if (b.a.y_dtype == 1)
+    store4(reinterpret_cast<uint16_t*>(p.y) + tok * b.a.ld_y + m, c_out - m, v);
+  else
+    store4(reinterpret_cast<float*>(p.y) + tok * b.a.ld_y + m, c_out - m, v);
+}
+
+// ---------------------------------------------------------------------------
 // The large gradient: 64 kNT tokens x 256 columns per workgroup, four waves
 // of 32 kNT tokens x 128 columns.
 //
@@ -649,17 +999,6 @@ struct GradArgs {
   int splits;
   float* part;
 };
-
-// 4 bytes (1 byte, zero-extended to 4) per lane from base + off straight into LDS (lane l at lds + 4 l).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ void dma1(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 // kW4: the packed rows are not 16-byte aligned and come in 4-byte pieces.
 template <int kNT, int kDepth, int kWaves, bool kW4>
@@ -819,8 +1158,8 @@ __global__ __launch_bounds__(kThreads, kWaves) void grad_big_kernel(GradArgs b) 
     static_for<kLoads>([&](auto n) { dload(min(s_first + d, end), d, n); });
   });
   static_for<kQ0>([&](auto n) { dload(min(s_first + kDepth, end), kDepth, n); });
-  wait_loads<0>();
-  __syncthreads();
+  wait_loads<kAhead + kQ0>();  // the first stage has landed
+  block_sync();
   {
     std::integral_constant<int, 0> zero;
     static_for<4>([&](auto e) { wread(0, zero, e); });
@@ -1088,32 +1427,39 @@ hipError_t launch_x(const LinearArgs& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 struct Plan {
   int few = 0;             // > 0: linear_few_kernel with that many tokens per wave
-  int nt = 0;              // > 0: linear_big_kernel<nt>
+  int tok = 0;             // > 0: the kernel with tiles of that many tokens (big_tokens)
   int splits = 1;
   int64_t kp = 0;          // packed row length (one plane), chunks * kChunk / planes
   bool pack = false;       // x goes through pack_rows_kernel
   size_t pack_bytes = 0, part_bytes = 0;
 };
 
-// Outputs of a workgroup of linear_big_kernel<nt>.
-int64_t big_m(int nt) { return nt >= 4 ? 256 : 128; }
+// Outputs of a workgroup of the product's kernel for tiles of tok tokens.
+int64_t big_m(int tok) { return tok >= 128 ? 256 : tok >= 32 ? kSmallM : kSkinnyM; }
 
-// Time of a launch of a large kernel in microseconds, from what its parts
-// measured on MI355X: a chunk (or stage) takes `one` with one workgroup on a
-// CU and `all` with as many as fit (`fit`), each workgroup starts and ends for
-// 3.5, and a split adds a launch and its partial sums' way to memory and back.
-// Product, 4096 x 4096 weights, 512 tokens: nt 2 unsplit 27.9, in 2 parts
-// 34.7, nt 4 in 4 parts 37.5; 128 tokens: nt 1 in 2 parts 18.6, nt 2 in 4
-// parts 19.9; 8192 tokens on 12288 x 4096: nt 4 740, nt 8 757.
-// Gradient, 4096 x 4096 weights, 4096 tokens: nt 4 132, nt 2 155, nt 1 237;
-// 1024 tokens: nt 4 in 4 parts 67, unsplit 118; 256 tokens: nt 2 in 8 parts
-// 33, nt 4 in 4 parts 48; 64 tokens: nt 1 in 8 parts 25, nt 2 26.
+// Time of a launch in microseconds, from what its parts measured on MI355X: a
+// workgroup starts and ends for `ends`, a chunk (or stage) takes it `one` where
+// it is alone on its CU and `all` where as many as fit are there (`fit`), and a
+// split adds a launch and its partial sums' way to memory and back.  The
+// constants reproduce these (medians, weights of 4096 x 4096 unless named):
+//   product, 16 tokens: tile 16 8.0, tile 32 in 4 parts 13.3, tile 64 in 4
+//     parts 12; 16 tokens on 12288 x 4096: 13.6 and 16.6; 48 tokens on 12288 x
+//     4096: tile 64 in 2 parts 18.5, tile 32 22.4; 512 tokens: tile 64 25.7,
+//     tile 128 in 4 parts 35.9; 4096 tokens: tile 256 112, tile 128 120
+//   64 experts of 1024 x 2048, 128 rows: tile 32 14.6, tile 64 15.1, tile 16
+//     19.2; 2048 rows: 33.4, 36.7, 71; 32768 rows: tile 128 174, tile 256 189
+//   gradient, 4096 tokens: tile 256 132, tile 128 155, tile 64 237; 1024 tokens:
+//     tile 256 in 4 parts 67, unsplit 118; 256 tokens: tile 128 in 8 parts 33,
+//     tile 256 in 4 parts 48; 64 tokens: tile 64 in 8 parts 25, tile 128 26;
+//     experts, 32768 rows: tile 128 199, tile 256 232
 struct BigCost {
-  int nt, fit;
-  double one, all;
+  int tok, fit;
+  double ends, one, all;
 };
-constexpr BigCost kBigCosts[] = {{8, 1, 3.9, 3.9}, {4, 2, 2.3, 3.85}, {2, 2, 0.85, 1.35}, {1, 4, 0.65, 1.6}};
-constexpr BigCost kGradCosts[] = {{4, 1, 2.0, 2.0}, {2, 2, 1.45, 2.35}, {1, 2, 1.27, 1.8}};
+constexpr BigCost kBigCosts[] = {
+    {256, 1, 10.0, 2.6, 3.25}, {128, 2, 5.0, 1.8, 3.46}, {64, 2, 4.0, 0.67, 2.0}, {32, 2, 4.0, 0.55, 1.4},
+    {16, 2, 3.5, 0.14, 0.35}};
+constexpr BigCost kGradCosts[] = {{256, 1, 9.0, 1.92, 1.92}, {128, 2, 5.0, 1.43, 2.33}, {64, 2, 4.0, 1.27, 2.6}};
 constexpr int kCUs = 256;
 
 double big_cost(const BigCost& k, double tiles, int64_t chunks, int splits, double part_values) {
@@ -1121,28 +1467,28 @@ double big_cost(const BigCost& k, double tiles, int64_t chunks, int splits, doub
   const double rounds = groups > slots ? groups / slots : 1.0;
   const double load = groups >= slots ? 1.0 : groups > kCUs ? (groups - kCUs) / (slots - kCUs) : 0.0;
   const double chunk = k.one + (k.all - k.one) * load;
-  // the last round is rarely full: half a workgroup's time more on average past the first rounds
-  const double turns = rounds > 1.0 ? (rounds < 4.0 ? ceil(rounds) : rounds + 0.5) : 1.0;
-  double t = turns * (3.5 + chunk * (double)((chunks + splits - 1) / splits));
-  if (splits > 1) t += 2.5 + splits * part_values * 8e-6 / 4.0;
+  // long workgroups: the last round takes as long as a full one, and half of one more on average past the first few
+  const double turns = k.tok <= 32 || rounds <= 1.0 ? rounds : rounds < 4.0 ? ceil(rounds) : rounds + 0.5;
+  double t = turns * (k.ends + chunk * (double)((chunks + splits - 1) / splits));
+  if (splits > 1) t += 3.0 + splits * part_values * 8e-6 / 4.0;
   return t;
 }
 
-// The cheapest of kCosts' kernels and of up to 16 parts for a.
+// The cheapest kernel and number of parts (up to 16) for a.
 template <int kN>
 void cheapest(Plan& p, const LinearArgs& a, const BigCost (&costs)[kN], int64_t chunks) {
   const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups, m = a.grad ? a.c_in : a.c_out;
   double best = 0.0;
   for (const BigCost& k : costs) {
-    const int64_t bt = (a.grad ? 64 : 32) * k.nt, bm = a.grad ? kGradM : big_m(k.nt), m_tiles = (m + bm - 1) / bm;
+    const int64_t bt = k.tok, bm = a.grad ? kGradM : big_m(k.tok), m_tiles = (m + bm - 1) / bm;
     // ragged: about half of a tile more per group that has rows
     const double used = (double)(a.n_groups < a.rows ? a.n_groups : a.rows);
     const double t_tiles = a.ragged ? (double)a.rows / bt + 0.5 * used : (double)((a.rows + bt - 1) / bt * a.n_groups);
     for (int splits = 1; splits <= (a.ragged ? 1 : 16) && splits <= chunks; splits *= 2) {
       const double t = big_cost(k, t_tiles * m_tiles, chunks, splits, (double)all * m);
-      if (p.nt == 0 || t < best) {
+      if (p.tok == 0 || t < best) {
         best = t;
-        p.nt = k.nt;
+        p.tok = k.tok;
         p.splits = splits;
       }
     }
@@ -1152,12 +1498,12 @@ void cheapest(Plan& p, const LinearArgs& a, const BigCost (&costs)[kN], int64_t 
 Plan plan_of(const LinearArgs& a) {
   Plan p;
   if (a.rows <= 0 || a.c_in <= 0 || a.c_out <= 0) return p;
-  // Up to four tokens: linear_few_kernel (5120 x 17408 weights, one token:
-  // 12.9 us against 30 for nt 1 in 8 parts; 12288 x 4096, four tokens: 13.1
-  // against 24).  Ragged rows of several experts: nt 1 from 64 rows on 64
-  // experts on (14.1 us against 17.2).
-  if (!a.grad && (a.ragged ? a.rows <= 16 : a.rows <= 4)) {
-    p.few = a.ragged || a.rows <= 1 ? 1 : a.rows <= 2 ? 2 : 4;
+  // Up to two tokens, or eight ragged rows: linear_few_kernel (5120 x 17408
+  // weights, one token: 12.9 us against 21.5; 12288 x 4096, two tokens: 9.6
+  // against 13.0, four tokens 13.1 against 13.0; eight rows on 64 experts of
+  // 1024 x 2048: 4.7 against 6.0).
+  if (!a.grad && a.rows <= (a.ragged ? 8 : 2)) {
+    p.few = a.ragged ? 1 : (int)a.rows;
     return p;
   }
   const int planes = a.x_dtype == 1 ? 1 : 3;
@@ -1196,8 +1542,7 @@ hipError_t launch_few_x(const LinearArgs& a, hipStream_t stream) {
 hipError_t launch_few(const LinearArgs& a, int tok, hipStream_t stream) {
   switch (tok) {
     case 1: return launch_few_x<1>(a, stream);
-    case 2: return launch_few_x<2>(a, stream);
-    default: return launch_few_x<4>(a, stream);
+    default: return launch_few_x<2>(a, stream);
   }
 }
 
@@ -1211,6 +1556,28 @@ hipError_t launch_big_nt(const BigArgs& b, hipStream_t stream) {
   return hipGetLastError();
 }
 
+
+// Whether rows of packed weights are whole 16-byte pieces and the codes whole pairs.
+bool whole_pieces(const LinearArgs& a) {
+  return a.c_in % 32 == 0 && reinterpret_cast<uintptr_t>(a.packed) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(a.codes) % 2 == 0;
+}
+
+template <int kW, int kBufs>
+hipError_t launch_skinny(const BigArgs& b, hipStream_t stream) {
+  const dim3 grid((unsigned)(b.m_tiles * b.t_tiles), (unsigned)b.splits);
+  if (whole_pieces(b.a)) linear_skinny_kernel<kW, kBufs, false><<<grid, dim3(64 * kW), 0, stream>>>(b);
+  else linear_skinny_kernel<kW, 2, true><<<grid, dim3(64 * kW), 0, stream>>>(b);
+  return hipGetLastError();
+}
+
+template <int kBufs>
+hipError_t launch_small(const BigArgs& b, hipStream_t stream) {
+  const dim3 grid((unsigned)(b.m_tiles * b.t_tiles), (unsigned)b.splits);
+  if (whole_pieces(b.a)) linear_small_kernel<kBufs, false><<<grid, dim3(512), 0, stream>>>(b);
+  else linear_small_kernel<kBufs, true><<<grid, dim3(512), 0, stream>>>(b);
+  return hipGetLastError();
+}
 
 template <int kNT, int kDepth, int kWaves>
 hipError_t launch_grad_nt(const GradArgs& b, hipStream_t stream) {
@@ -1264,26 +1631,27 @@ hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
   hipError_t e = pack_rows(a, p, r, stream);
   if (e != hipSuccess) return e;
   float* const part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.pack_bytes);
-  int64_t t_tiles = token_tiles(a, a.grad ? 64 * p.nt : 32 * p.nt);
+  int64_t t_tiles = token_tiles(a, p.tok);
   if (a.ragged) t_tiles = (t_tiles + 7) / 8 * 8;
   if (a.grad) {
     const int w_stages = (int)(p.kp / kGradK);
     const GradArgs b{a, r.x, r.ld, r.gstride, planes * w_stages, w_stages, (a.c_in + kGradM - 1) / kGradM, t_tiles,
                      p.splits, part};
-    switch (p.nt) {
-      case 4: e = launch_grad_nt<4, 2, 1>(b, stream); break;
-      case 2: e = launch_grad_nt<2, 1, 2>(b, stream); break;
+    switch (p.tok) {
+      case 256: e = launch_grad_nt<4, 2, 1>(b, stream); break;
+      case 128: e = launch_grad_nt<2, 1, 2>(b, stream); break;
       default: e = launch_grad_nt<1, 2, 2>(b, stream); break;
     }
   } else {
     const int w_chunks = (int)(p.kp / kChunk);
-    const BigArgs b{a, r.x, r.ld, r.gstride, planes * w_chunks, w_chunks, (a.c_out + big_m(p.nt) - 1) / big_m(p.nt),
+    const BigArgs b{a, r.x, r.ld, r.gstride, planes * w_chunks, w_chunks, (a.c_out + big_m(p.tok) - 1) / big_m(p.tok),
                     t_tiles, p.splits, part};
-    switch (p.nt) {
-      case 8: e = launch_big_nt<8, 2, 1, 1>(b, stream); break;
-      case 4: e = launch_big_nt<4, 2, 1, 2>(b, stream); break;
-      case 2: e = launch_big_nt<2, 1, 4, 2>(b, stream); break;
-      default: e = launch_big_nt<1, 1, 4, 3>(b, stream); break;
+    switch (p.tok) {
+      case 256: e = launch_big_nt<8, 2, 1, 1>(b, stream); break;
+      case 128: e = launch_big_nt<4, 2, 1, 2>(b, stream); break;
+      case 64: e = launch_big_nt<2, 1, 4, 2>(b, stream); break;
+      case 32: e = launch_small<2>(b, stream); break;
+      default: e = launch_skinny<4, 3>(b, stream); break;
     }
   }
   if (e != hipSuccess || p.splits == 1) return e;
@@ -1307,7 +1675,7 @@ size_t linear_ws_bytes(const LinearArgs& a) {
 hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
   const Plan p = plan_of(a);
   if (p.few > 0) return launch_few(a, p.few, stream);
-  if (p.nt > 0 && direct_rows(a, p) && (p.pack_bytes + p.part_bytes == 0 || a.ws)) return launch_big(a, p, stream);
+  if (p.tok > 0 && direct_rows(a, p) && (p.pack_bytes + p.part_bytes == 0 || a.ws)) return launch_big(a, p, stream);
   if (a.grad) return a.x_dtype == 1 ? launch_x<true, uint16_t>(a, stream) : launch_x<true, float>(a, stream);
   return a.x_dtype == 1 ? launch_x<false, uint16_t>(a, stream) : launch_x<false, float>(a, stream);
 }

@@ -1658,11 +1658,14 @@ hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
   return sum_splits(a, p, part, stream);
 }
 
-// Whether the rows of x can be loaded to LDS directly (else the general kernel takes them).
+// Whether the kernels with direct loads take a: rows that they can load
+// themselves (or packed ones), and offsets within a tile in 32 bits.  The
+// general kernel takes the rest.
 bool direct_rows(const LinearArgs& a, const Plan& p) {
-  if (p.pack) return true;
-  return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld_x % 8 == 0 || a.rows == 1) && a.gstride_x % 8 == 0 &&
-         a.ld_x < (1 << 22);
+  const int planes = a.x_dtype == 1 ? 1 : 3;
+  if ((p.pack ? planes * p.kp : a.ld_x) >= (1 << 22) || a.c_in >= (1 << 28)) return false;
+  if (p.pack) return a.ws != nullptr;
+  return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld_x % 8 == 0 || a.rows == 1) && a.gstride_x % 8 == 0;
 }
 
 }  // namespace
@@ -1673,9 +1676,10 @@ size_t linear_ws_bytes(const LinearArgs& a) {
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
-  const Plan p = plan_of(a);
+  Plan p = plan_of(a);
   if (p.few > 0) return launch_few(a, p.few, stream);
-  if (p.tok > 0 && direct_rows(a, p) && (p.pack_bytes + p.part_bytes == 0 || a.ws)) return launch_big(a, p, stream);
+  if (a.ws == nullptr) p.splits = 1;  // no place for partial sums
+  if (p.tok > 0 && direct_rows(a, p)) return launch_big(a, p, stream);
   if (a.grad) return a.x_dtype == 1 ? launch_x<true, uint16_t>(a, stream) : launch_x<true, float>(a, stream);
   return a.x_dtype == 1 ? launch_x<false, uint16_t>(a, stream) : launch_x<false, float>(a, stream);
 }

@@ -329,3 +329,60 @@ def test_refusals(lh):
         lh.lh_linear_nvfp4_ragged(x, torch.zeros(3, dtype=torch.int64, device=DEV), packed, codes, s)
     with pytest.raises(TypeError):
         lh.lh_linear_nvfp4_ragged(x, torch.zeros(2, dtype=torch.int32, device=DEV), packed, codes, s)
+
+
+LARGE = [(5, 300, 2064), (24, 4096, 1056), (40, 8192, 1056), (40, 8192, 1040), (300, 4096, 528), (300, 4096, 512),
+         (1100, 4096, 1040), (1100, 4096, 1024), (200, 2048, 2064), (4099, 4000, 2064), (4096, 4096, 2048)]
+
+
+@pytest.mark.parametrize("t,c_out,c_in", LARGE)
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_larger_layers(lh, t, c_out, c_in, dt):
+    """Sizes at which tiles of 16 to 256 tokens and splits of the sum are
+    chosen, whole and ragged at every end; the 64-bit reference is computed on
+    the GPU here.  The workspace's contents must not matter."""
+    print("case t=%d c_out=%d c_in=%d %s" % (t, c_out, c_in, dt), flush=True)
+    gen = torch.Generator(device=DEV).manual_seed(t)
+    packed = torch.randint(0, 256, (1, c_out, c_in // 2), dtype=torch.uint8, device=DEV, generator=gen)
+    codes = torch.randint(0x28, 0x50, (1, c_out, c_in // 16), dtype=torch.uint8, device=DEV, generator=gen)
+    s = torch.full((1,), 1e-3, device=DEV)
+    u = torch.from_numpy(units64(packed.cpu(), codes.cpu())[0]).to(DEV)
+    for n, m, w, grad in ((c_in, c_out, u, False), (c_out, c_in, u.t(), True)):
+        x = torch.randn((t, n), device=DEV, generator=gen).to(dt)
+        f = lh.lh_linear_nvfp4_grad if grad else lh.lh_linear_nvfp4
+        size = lh.lh_linear_nvfp4_workspace_bytes(t, c_in, c_out, dtype=dt, grad=grad)
+        ws = torch.full((max(size, 256),), 0xFF, dtype=torch.uint8, device=DEV)
+        got = [f(x, packed, codes, s, workspace=ws), f(x, packed, codes, s), f(x, packed, codes, s, workspace=None)]
+        assert torch.equal(got[0], got[1])
+        x64, scale = x.double(), float(s[0])
+        ref, mass = scale * (x64 @ w.t()), scale * (x64.abs() @ w.t().abs())
+        ulp = 2.0 ** -8 if dt == BF16 else 2.0 ** -24
+        tol = (8 * np.sqrt(n) * 2.0 ** -24 + 2.0 ** -23) * mass
+        tol = tol + ulp * (ref.abs() + tol)
+        for y in got[1:]:
+            assert bool(((y.double() - ref).abs() <= tol).all()), "gradient" if grad else "product"
+
+
+@pytest.mark.parametrize("n,c_out,c_in", [(128, 512, 512), (600, 512, 528), (9000, 300, 272), (20000, 512, 256),
+                                          (6, 300, 528)])
+def test_larger_ragged_calls(lh, n, c_out, c_in):
+    print("case n=%d c_out=%d c_in=%d" % (n, c_out, c_in), flush=True)
+    g = 16
+    rng = np.random.default_rng(n)
+    counts = rng.multinomial(n, rng.dirichlet(np.full(g, 0.4)))
+    off = np.concatenate([[0], np.cumsum(counts)])
+    packed, codes, s = weights(rng, g, c_out, c_in)
+    u = torch.from_numpy(units64(packed, codes)).to(DEV)
+    dev = [torch.from_numpy(off).to(DEV), packed.to(DEV), codes.to(DEV), s.to(DEV)]
+    for dt in (BF16, F32):
+        ulp = 2.0 ** -8 if dt == BF16 else 2.0 ** -24
+        for k, f, w in ((c_in, lh.lh_linear_nvfp4_ragged, u), (c_out, lh.lh_linear_nvfp4_ragged_grad, u.transpose(1, 2))):
+            x = torch.randn((n, k), device=DEV).to(dt)
+            y = f(x, *dev, max_group_rows=int(counts.max()))
+            for i in range(g):
+                r = slice(int(off[i]), int(off[i + 1]))
+                x64 = x[r].double()
+                ref, mass = float(s[i]) * (x64 @ w[i].t()), float(s[i]) * (x64.abs() @ w[i].t().abs())
+                tol = (8 * np.sqrt(k) * 2.0 ** -24 + 2.0 ** -23) * mass
+                tol = tol + ulp * (ref.abs() + tol)
+                assert bool(((y[r].double() - ref).abs() <= tol).all()), "group %d" % i

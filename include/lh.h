@@ -593,8 +593,8 @@ size_t lh_linear_nvfp4_workspace_bytes(int grad, int ragged, int x_dtype, int64_
  *   global_scale fp32 [n_groups] (S_g).  x_scale: fp32 [n_groups] or NULL
  *                (1): the S_g of activations given as lh_quantize_nvfp4 values.
  *   y            fp32 or bf16, [n_tokens][ld_y] per group, ld_y >= c_out;
- *                must not overlap x.  n_groups > 1: group_stride_y >=
- *                n_tokens * ld_y.
+ *                must not overlap x.  n_groups > 1: the groups of y must not
+ *                overlap (one after the other, or side by side in wide rows).
  *   workspace    NULL/0, or at least lh_linear_nvfp4_workspace_bytes(0, 0,
  *                x_dtype, n_tokens, c_in, c_out, n_groups, 0) bytes, 256-byte
  *                aligned.

@@ -657,6 +657,14 @@ def _dense(t: torch.Tensor | None, name: str, dtype, shape=None) -> None:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
+def _scratch(first: torch.Tensor, t: torch.Tensor):
+    """A caller's workspace and its bytes."""
+    _on_device(first, t)
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t, t.numel() * t.element_size()
+
+
 def _on_device(first: torch.Tensor, *others) -> None:
     """All given tensors on one ROCm device."""
     d = first.get_device()
@@ -751,7 +759,7 @@ def _linear(x, offsets, packed, scale_e4m3, global_scale, x_scale, y, out_dtype,
         if ws_bytes:
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
     elif isinstance(workspace, torch.Tensor):
-        ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
+        ws, ws_bytes = _scratch(x, workspace)
     xa = (_ptr(x3), _dtype(x3), rows, k, _ld(x3))
     wa = (_ptr(p3), _ptr(s3), _ptr(global_scale), m)
     ya = (_ptr(y3), _dtype(y3), _ld(y3))
@@ -818,7 +826,7 @@ def lh_moe_sort(expert_ids: torch.Tensor, n_groups: int, order: bool = True,
     [n_groups + 1], position int32 [n_tokens, top_k] (the row, or -1 - row of
     a dropped one) and, with order=True, order int32 [n_tokens * top_k] (the
     assignment of each row, or -1 - it)."""
-    _on_device(expert_ids, workspace)
+    _on_device(expert_ids)
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be [n_tokens, top_k]")
     if expert_ids.dtype not in (torch.int32, torch.int64):
@@ -829,10 +837,12 @@ def lh_moe_sort(expert_ids: torch.Tensor, n_groups: int, order: bool = True,
     i32 = dict(dtype=torch.int32, device=expert_ids.device)
     res = dict(offsets=torch.empty(n_groups + 1, dtype=torch.int64, device=expert_ids.device),
                position=torch.empty((t, k), **i32), order=torch.empty(t * k, **i32) if order else None)
+    nbytes = 0
     if workspace is None:
-        n = lh_moe_sort_workspace_bytes(t, k, n_groups)
-        workspace = torch.empty(n, dtype=torch.uint8, device=expert_ids.device) if n else None
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        nbytes = lh_moe_sort_workspace_bytes(t, k, n_groups)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=expert_ids.device) if nbytes else None
+    else:
+        workspace, nbytes = _scratch(expert_ids, workspace)
     _check(lib.lh_moe_sort(_ptr(expert_ids), LH_INDEX_I64 if expert_ids.dtype == torch.int64 else LH_INDEX_I32, t, k,
                            n_groups, _ptr(res["offsets"]), _ptr(res["position"]), _ptr(res["order"]),
                            _ptr(workspace), nbytes, _stream(expert_ids)))

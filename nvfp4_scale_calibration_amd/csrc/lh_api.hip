@@ -607,7 +607,9 @@ lh_status run_linear(const char* fn, lh::LinearArgs& a, int64_t x_len, int64_t y
     return fail(LH_ERR_SHAPE, "%s: negative size or stride", fn);
   if (a.c_in % 16 != 0) return fail(LH_ERR_SHAPE, "%s: c_in must be a multiple of 16", fn);
   if (a.ld_x < x_len || a.ld_y < y_len) return fail(LH_ERR_SHAPE, "%s: a leading dimension is smaller than its row", fn);
-  if (!a.ragged && a.n_groups > 1 && a.gstride_y < a.rows * a.ld_y)
+  // groups of the output one after the other, or side by side in wide rows
+  if (!a.ragged && a.n_groups > 1 && a.rows > 0 && a.gstride_y < (a.rows - 1) * a.ld_y + y_len &&
+      (a.gstride_y < y_len || a.ld_y < (a.n_groups - 1) * a.gstride_y + y_len))
     return fail(LH_ERR_SHAPE, "%s: the output's group stride would overlap groups", fn);
   const bool work = a.rows > 0 && a.n_groups > 0 && y_len > 0;
   const bool reads = work && x_len > 0;

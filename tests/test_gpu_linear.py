@@ -331,6 +331,37 @@ def test_refusals(lh):
         lh.lh_linear_nvfp4_ragged(x, torch.zeros(2, dtype=torch.int32, device=DEV), packed, codes, s)
 
 
+def test_a_workspace_on_the_host_or_with_gaps_is_refused(lh):
+    rng = np.random.default_rng(47)
+    packed, codes, s = [v.to(DEV) for v in weights(rng, 1, 32, 64)]
+    x = torch.zeros((40, 64), dtype=F32, device=DEV)
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty((1 << 20, 2), dtype=torch.uint8, device=DEV)[:, 0]):
+        with pytest.raises(ValueError):
+            lh.lh_linear_nvfp4(x, packed, codes, s, workspace=ws)
+        with pytest.raises(ValueError):
+            lh.lh_linear_nvfp4_grad(torch.zeros((40, 32), device=DEV), packed, codes, s, workspace=ws)
+        with pytest.raises(ValueError):
+            lh.lh_moe_sort(torch.zeros((4, 2), dtype=torch.int64, device=DEV), 3, workspace=ws)
+
+
+@pytest.mark.parametrize("t", [1, 2, 5, 70])
+def test_groups_side_by_side_in_wide_rows(lh, t):
+    """The output as [tokens, groups, columns]: the same values as group by group."""
+    g, c_out, c_in = 3, 48, 80
+    rng = np.random.default_rng(53)
+    packed, codes, s = [v.to(DEV) for v in weights(rng, g, c_out, c_in)]
+    x = torch.from_numpy(rng.standard_normal((t, g, c_in)).astype(np.float32)).to(DEV).transpose(0, 1)
+    wide = torch.full((t, g, c_out), 9.0, device=DEV)
+    lh.lh_linear_nvfp4(x, packed, codes, s, y=wide.transpose(0, 1))
+    assert torch.equal(wide.transpose(0, 1), lh.lh_linear_nvfp4(x.contiguous(), packed, codes, s))
+    dy = torch.from_numpy(rng.standard_normal((t, g, c_out)).astype(np.float32)).to(DEV).transpose(0, 1)
+    dwide = torch.full((t, g, c_in), 9.0, device=DEV)
+    lh.lh_linear_nvfp4_grad(dy, packed, codes, s, dx=dwide.transpose(0, 1))
+    assert torch.equal(dwide.transpose(0, 1), lh.lh_linear_nvfp4_grad(dy.contiguous(), packed, codes, s))
+    with pytest.raises(lh.LHError):
+        lh.lh_linear_nvfp4(x, packed, codes, s, y=torch.empty((t, c_out), device=DEV).expand(g, t, c_out))
+
+
 LARGE = [(5, 300, 2064), (24, 4096, 1056), (40, 8192, 1056), (40, 8192, 1040), (300, 4096, 528), (300, 4096, 512),
          (1100, 4096, 1040), (1100, 4096, 1024), (200, 2048, 2064), (4099, 4000, 2064), (4096, 4096, 2048)]
 

@@ -121,7 +121,11 @@ __device__ __forceinline__ void store4(uint16_t* p, int64_t n, const float (&v)[
 // ---------------------------------------------------------------------------
 // The general kernel: 64 outputs x 64 tokens per workgroup, four waves of
 // 32 x 32 quadrants (2 x 2 v_mfma_f32_16x16x32_bf16 tiles), K in steps of 64
-// through LDS.  Any size, stride and alignment.
+// through LDS.  Any size, stride and alignment: rows of bf16 that are not
+// 16-byte aligned, fp32 or odd rows for which the caller gave no workspace,
+// row strides past 32-bit offsets.  It decodes a weight once per 64 tokens,
+// through LDS, with a barrier per 64 weights, and is bound by that: 8192 x
+// (12288 x 4096) 1.6 ms, 0.52 PFLOP/s, against 0.68 ms of the kernels below.
 // ---------------------------------------------------------------------------
 constexpr int kT = 64;           // outputs and tokens per tile
 constexpr int kK = 64;           // contraction step
@@ -260,19 +264,19 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
 }
 
 // ---------------------------------------------------------------------------
-// The large product: kNT * 32 tokens x 256 outputs per workgroup of four
-// waves, one wave per SIMD for kNT = 8.
+// The large product: kNT * 32 tokens x 128 kRF outputs per workgroup of four
+// waves: 256 x 256 (one wave per SIMD), 128 x 256 and 64 x 128.
 //
-// Each wave owns 64 outputs alone (2 x kNT tiles of v_mfma_f32_32x32x16_bf16,
-// 32 kNT accumulators per lane), so every weight is decoded once per
+// Each wave owns 32 kRF outputs alone (kRF x kNT tiles of
+// v_mfma_f32_32x32x16_bf16, 16 kRF kNT accumulators per lane), so every weight is decoded once per
 // workgroup, in registers, straight into the MFMA operand: the packed bytes
 // never pass through LDS.  The contraction index may be walked in any order
 // as long as both operands agree: in a chunk of 128 weights of a row, the
 // lanes of half h (l / 32) take weights 64 h .. 64 h + 63, two 16-byte loads,
 // and MFMA step i (of 8) takes weights 64 h + 8 i ..  + 7 of both halves.
 //
-// Activations come through LDS, one chunk of 256 bytes a token in each of two
-// buffers, filled by direct global -> LDS loads (16 bytes a lane, four tokens
+// Activations come through LDS, one chunk of 256 bytes a token in each of
+// kDepth + 1 buffers, filled by direct global -> LDS loads (16 bytes a lane, four tokens
 // an instruction, whole lines).  Slot q ^ (token & 15) holds 16-byte piece q,
 // so that the 16 lanes which LDS serves together read one piece of 16 tokens
 // from distinct banks.
@@ -284,6 +288,15 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
 // (sched_barrier keeps each group where it is written).  The barrier of a
 // chunk stands before its last step, whose operands are in registers by then,
 // so that step's MFMAs cover the first reads of the next chunk.
+//
+// Measured: 8192 tokens x (12288 x 4096) 682 us, 1.21 PFLOP/s (a library's
+// bf16 product of that size 637 us); 32768 ragged rows on 64 experts of 1024 x
+// 2048 172 us, 0.80 PFLOP/s, of which the rows that fill up the experts' last
+// tiles are an eighth; 48 tokens x (12288 x 4096), 64 x 128 tiles in two parts,
+// 14.5 us and 3.8 for their sum.  Bound by the issue of vector instructions
+// between the MFMAs (decoding and LDS reads), the small tiles by the latency
+// of their few chunks.  Eight waves of 32 outputs instead of four of 64: 683
+// against 689 us with 256 tokens, 820 against 712 with 128.
 // ---------------------------------------------------------------------------
 constexpr int kChunk = 128;   // contraction elements per chunk
 
@@ -640,6 +653,12 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
 // in linear_big_kernel; weights 64 bytes a row, the wave's 1 KiB in one
 // instruction; codes one 32-bit word per lane, its two codes (kW4: one word
 // each).  kW4: rows that are not 16-byte aligned, in 4-byte pieces.
+//
+// Measured: 128 rows on 64 experts of 1024 x 2048 14.5 us (tiles of 64 tokens
+// by linear_big_kernel 15.1, of 16 by linear_skinny_kernel 19.2), 2048 rows 33
+// (37, 71).  Bound by latency: the 75 MB of weights that 60 experts hold would
+// take 14 us at a copy's rate where all are read.  More pairs of chunks in
+// flight gave nothing, nor did tiles of 64 tokens in this manner.
 // ---------------------------------------------------------------------------
 constexpr int kSmallM = 128;
 
@@ -810,6 +829,10 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
 // token, slot q ^ (token & 15) holding 16-byte piece q; 64 bytes a row of
 // weights; one 32-bit word per lane and operand for its two codes (kW4: one
 // word each).  kW4: rows that are not 16-byte aligned, in 4-byte pieces.
+//
+// Measured: 16 tokens x (4096 x 4096) 8.0 us (launch, one chunk's latency and
+// the join alone are 5), 8 tokens x (12288 x 4096) 13.1 us, 2.2 TB/s of weights;
+// linear_small_kernel 13.3 and 16.6.
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyM = 32;
 
@@ -986,6 +1009,11 @@ __global__ __launch_bounds__(64 * kW, 2) void linear_skinny_kernel(BigArgs b) {
 // step's operands in the first slots and decodes them in the later ones (72
 // vector operations; a weight is decoded by the two waves that share its
 // columns).
+//
+// Measured: 4096 tokens x (12288 x 4096) 381 us, 1.08 PFLOP/s; 32768 ragged
+// rows on 64 experts of 1024 x 2048 198 us, 0.69 PFLOP/s.  Bound by vector
+// issue as the product, with the pairing of rows on top (72 operations for 4
+// kNT MFMAs, against 64 for as many there).
 // ---------------------------------------------------------------------------
 constexpr int kGradK = 64;      // rows of W per stage
 constexpr int kGradM = 256;     // columns per workgroup
@@ -1218,7 +1246,9 @@ __global__ __launch_bounds__(kThreads, kWaves) void grad_big_kernel(GradArgs b) 
   }
 }
 
-// y = the splits' sums, added in split order.
+// y = the splits' sums, added in split order (so results do not change from
+// run to run, as they would with atomics).  Memory-bound: 333 x 4096 in four
+// parts, 27 MB, 8.8 us.
 template <typename TY>
 __global__ __launch_bounds__(kThreads) void split_sum_kernel(const float* __restrict__ part, int splits, int64_t rows,
                                                              int64_t n_groups, int64_t cols, TY* __restrict__ y,
@@ -1249,6 +1279,7 @@ __global__ __launch_bounds__(kThreads) void split_sum_kernel(const float* __rest
 // Rows of any alignment and length to bf16 rows of kp elements (zeros past
 // k), fp32 as three planes of kp elements behind each other: the sum over
 // all 3 kp of them, with the weights walked three times, is the product.
+// Memory-bound: 333 x 4096 fp32 5.6 us, launch included.
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void pack_rows_kernel(const TX* __restrict__ x, int64_t rows, int64_t k,
                                                              int64_t ld, int64_t n_groups, int64_t gstride, int64_t kp,
@@ -1292,6 +1323,9 @@ __global__ __launch_bounds__(kThreads) void pack_rows_kernel(const TX* __restric
 // not the weights (1.1 vector operations per weight and token, against 2 to
 // build an MFMA operand).  fp32 activations take fused multiply-adds instead.
 // The lanes' sums are added by xor shuffles at the end, in a fixed order.
+//
+// Measured: one token x (5120 x 17408) 12.8 us, 3.9 TB/s of weights and codes
+// (a copy of 2 GiB reaches 4.9); bound by that read and the launch.
 // ---------------------------------------------------------------------------
 constexpr int kSpan = 2048;
 

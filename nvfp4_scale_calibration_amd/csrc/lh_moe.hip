@@ -27,6 +27,8 @@ namespace {
 // wave walks its assignments again, 64 at a time: the lanes with the same
 // expert find each other by one ballot per bit of the expert number, so the
 // rank within the wave is a population count and the order is stable.
+// Bound by latency (a few dependent passes over 16 workgroups): 4096 x 8
+// assignments to 64 experts 8.7 us with both launches, 16 x 8 4.0 in one.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -190,7 +192,10 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(const TI* __rest
 // ---------------------------------------------------------------------------
 // Rows.  A thread moves 16 bytes of a row at a time; rows of any length and
 // alignment (the loads and stores are written for unaligned addresses, and
-// the last elements of a row go one by one).
+// the last elements of a row go one by one).  Memory-bound: 4096 tokens x 8
+// experts of 2048 bf16, dispatch 151 MB in 24 us (6.4 TB/s), combine 151 MB in
+// 29 us (5.2; 38 us where the rows were written just before), its gradient
+// 285 MB in 46 to 50 us (5.7).
 // ---------------------------------------------------------------------------
 template <typename T>
 struct Vec {

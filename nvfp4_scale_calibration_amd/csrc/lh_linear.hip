@@ -372,38 +372,32 @@ __device__ __forceinline__ uint32_t units2(uint32_t pk, float c) {
 }
 
 // A lane's share of one weight row's chunk: 64 weights and their 4 codes.
-// kPart: the row may end inside the chunk; the share then goes on with other
-// weights of the row, finite values that meet the zeros behind the
-// activations' row.
+// kPart: rows end inside their last chunk (`whole`: this is not it); blocks
+// past the end are replaced by the row's first, finite values that meet the
+// zeros behind the activations' row.
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x8_t __attribute__((ext_vector_type(8)));
 struct RawW {
   u32x8_t w;
-  uint32_t c;   // the four codes, or
-  uint4 c4;     // (kPart) one each
-  template <bool kPart, int i>
-  __device__ __forceinline__ float scale() const {
-    if constexpr (!kPart) return e4m3_to_f32<i>(c);
-    else return e4m3_to_f32<0>(i == 0 ? c4.x : i == 1 ? c4.y : i == 2 ? c4.z : c4.w);
-  }
+  uint32_t c;
 };
 template <bool kPart>
-__device__ __forceinline__ RawW load_raw(const uint8_t* row_q, const uint8_t* row_c, int64_t k, int64_t c_in) {
+__device__ __forceinline__ RawW load_raw(const uint8_t* row_q, const uint8_t* row_c, int64_t k, int64_t c_in,
+                                         bool whole) {
   RawW r;
-  if constexpr (!kPart) {
+  if (!kPart || whole) {
     const uint4 u = load_u128(row_q + k / 2), v = load_u128(row_q + k / 2 + 16);
     r.w = u32x8_t{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
     r.c = load_u32(row_c + k / 16);
   } else {
-    uint32_t code[4];
+    r.c = 0;
     static_for<4>([&](auto e) {
       const int64_t at = k + 16 * e < c_in ? k + 16 * e : 0;
       const uint2 v = load_u64(row_q + at / 2);
       r.w[2 * e] = v.x;
       r.w[2 * e + 1] = v.y;
-      code[e] = row_c[at / 16];
+      r.c |= (uint32_t)row_c[at / 16] << (8 * e);
     });
-    r.c4 = make_uint4(code[0], code[1], code[2], code[3]);
   }
   return r;
 }
@@ -472,8 +466,8 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   // steps by which activation operands are read ahead: one step of 8 or 16
   // MFMAs covers the way through LDS, one of 1 or 2 does not
   constexpr int kR = kNT >= 4 ? 1 : 3;
-  // loads issued behind the next chunk's by its barrier (the counter holds 63)
-  constexpr int kAheadAll = (kDepth - 1) * (kLoads + (kPart ? 8 : 3) * kRF), kAhead = kAheadAll < 63 ? kAheadAll : 63;
+  // loads issued behind the next chunk's by its barrier, at least (the counter holds 63)
+  constexpr int kAheadAll = (kDepth - 1) * (kLoads + 3 * kRF), kAhead = kAheadAll < 63 ? kAheadAll : 63;
   __shared__ __attribute__((aligned(1024))) uint8_t xs[kBufs * kBuf];
   int64_t tile, mt;
   big_tile(blockIdx.x, b.a.ragged, b.m_tiles, b.t_tiles, tile, mt);
@@ -512,7 +506,7 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   RawW ring[kBufs][kRF];  // this chunk's weights, the next ones'
   auto wload = [&](auto d, int chunk) {
     const int w = chunk % b.w_chunks;
-    static_for<kRF>([&](auto f) { ring[d][f] = load_raw<kPart>(wq[f], wc[f], (int64_t)w * kChunk + 64 * h, c_in); });
+    static_for<kRF>([&](auto f) { ring[d][f] = load_raw<kPart>(wq[f], wc[f], (int64_t)w * kChunk + 64 * h, c_in, w + 1 < b.w_chunks); });
   };
 
   uint4 fa[2][kRF];
@@ -534,7 +528,7 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   auto decode = [&](auto set, auto u, auto s, auto f, auto e) {
     constexpr int i = s & 7;
     const RawW& r = ring[(u + (s >> 3)) % kBufs][f];
-    const uint32_t v = units2<e>(r.w[i], r.template scale<kPart, (i >> 1)>());
+    const uint32_t v = units2<e>(r.w[i], e4m3_to_f32<(i >> 1)>(r.c));
     if constexpr (e == 0) fa[set][f].x = v;
     else if constexpr (e == 1) fa[set][f].y = v;
     else if constexpr (e == 2) fa[set][f].z = v;

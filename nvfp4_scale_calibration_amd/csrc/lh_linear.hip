@@ -264,26 +264,27 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
 }
 
 // ---------------------------------------------------------------------------
-// The large product: kNT * 32 tokens x 128 kRF outputs per workgroup of four
-// waves: 256 x 256 (one wave per SIMD), 128 x 256 and 64 x 128.
+// The large product: kNT * 32 tokens x 32 kRF kMW outputs per workgroup of kMW
+// waves: 256 x 256 (four waves, one per SIMD), 128 x 256, 64 x 128, and 64 x 256
+// of eight waves.
 //
 // Each wave owns 32 kRF outputs alone (kRF x kNT tiles of
-// v_mfma_f32_32x32x16_bf16, 16 kRF kNT accumulators per lane), so every weight is decoded once per
-// workgroup, in registers, straight into the MFMA operand: the packed bytes
-// never pass through LDS.  The contraction index may be walked in any order
-// as long as both operands agree: in a chunk of 128 weights of a row, the
-// lanes of half h (l / 32) take weights 64 h .. 64 h + 63, two 16-byte loads,
-// and MFMA step i (of 8) takes weights 64 h + 8 i ..  + 7 of both halves.
+// v_mfma_f32_32x32x16_bf16, 16 kRF kNT accumulators per lane), so every weight
+// is decoded once per workgroup, in registers, straight into the MFMA operand:
+// the packed bytes never pass through LDS.  The contraction index may be walked
+// in any order as long as both operands agree: in a chunk of 128 weights of a
+// row, the lanes of half h (l / 32) take weights 64 h .. 64 h + 63, two 16-byte
+// loads, and MFMA step i (of 8) takes weights 64 h + 8 i ..  + 7 of both halves.
 //
 // Activations come through LDS, one chunk of 256 bytes a token in each of
-// kDepth + 1 buffers, filled by direct global -> LDS loads (16 bytes a lane, four tokens
-// an instruction, whole lines).  Slot q ^ (token & 15) holds 16-byte piece q,
-// so that the 16 lanes which LDS serves together read one piece of 16 tokens
-// from distinct banks.
+// kDepth + 1 buffers, filled by direct global -> LDS loads (16 bytes a lane,
+// four tokens an instruction, whole lines).  Slot q ^ (token & 15) holds
+// 16-byte piece q, so that the 16 lanes which LDS serves together read one
+// piece of 16 tokens from distinct banks.
 //
-// Per step a wave issues 2 kNT MFMAs, and between them reads the next step's
-// kNT activation operands, decodes its two weight operands (32 vector
-// operations) and issues its share of the next chunk's loads: with one wave
+// Per step a wave issues kRF kNT MFMAs, and between them reads a later step's
+// kNT activation operands, decodes its kRF weight operands (16 vector
+// operations each) and issues its share of the next chunk's loads: with one wave
 // per SIMD the matrix pipe is covered only by what is interleaved by hand
 // (sched_barrier keeps each group where it is written).  The barrier of a
 // chunk stands before its last step, whose operands are in registers by then,
@@ -295,8 +296,9 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
 // tiles are an eighth; 48 tokens x (12288 x 4096), 64 x 128 tiles in two parts,
 // 14.5 us and 3.8 for their sum.  Bound by the issue of vector instructions
 // between the MFMAs (decoding and LDS reads), the small tiles by the latency
-// of their few chunks.  Eight waves of 32 outputs instead of four of 64: 683
-// against 689 us with 256 tokens, 820 against 712 with 128.
+// of their few chunks.  Eight waves of 32 outputs instead of four: 64
+// tokens x 256 outputs 40.4 us at 1024 x (4096 x 4096), where 64 x 128 takes
+// 45.7; with 256 tokens 683 against 689 us, with 128 820 against 712: not kept.
 // ---------------------------------------------------------------------------
 constexpr int kChunk = 128;   // contraction elements per chunk
 
@@ -456,13 +458,13 @@ __device__ __forceinline__ void store_rows(const f32x16_t (&acc)[kRF][kNT], floa
   }
 }
 
-template <int kNT, int kRF, int kDepth, int kWaves, bool kPart>
-__global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b) {
+template <int kNT, int kRF, int kMW, int kDepth, int kWaves, bool kPart>
+__global__ __launch_bounds__(64 * kMW, kWaves) void linear_big_kernel(BigArgs b) {
   constexpr int kBT = 32 * kNT;              // tokens
   constexpr int kWM = 32 * kRF;              // outputs per wave
   constexpr int kBuf = kBT * 256;            // bytes of an LDS buffer
   constexpr int kBufs = kDepth + 1;
-  constexpr int kLoads = 2 * kNT;            // direct loads per wave and chunk
+  constexpr int kLoads = 8 * kNT / kMW;      // direct loads per wave and chunk
   // steps by which activation operands are read ahead: one step of 8 or 16
   // MFMAs covers the way through LDS, one of 1 or 2 does not
   constexpr int kR = kNT >= 4 ? 1 : 3;
@@ -476,22 +478,24 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t c_in = b.a.c_in, c_out = b.a.c_out;
-  const int64_t m0 = mt * 4 * kWM + kWM * wave;  // the wave's first output
+  const int64_t m0 = (mt * kMW + wave) * kWM;  // the wave's first output
   // this workgroup's share of the chunks
   const int c_first = (int)((int64_t)b.chunks * blockIdx.y / b.splits);
   const int end = (int)((int64_t)b.chunks * (blockIdx.y + 1) / b.splits) - 1;  // its last one
 
-  // direct loads: instruction i of a wave fills tokens 4 (wave + 4 i) .. + 3
-  const int trow = 4 * wave + (lane >> 4);                 // token & 15
-  const uint32_t piece = (lane & 15) ^ trow;               // the piece that slot lane & 15 holds
+  // direct loads: instruction i of a wave fills tokens 4 (wave + kMW i) .. + 3;
+  // slot lane & 15 of token t holds piece (lane & 15) ^ (t & 15)
   const uint16_t* xg = b.x + uniform((b.a.ragged ? 0 : p.g * b.gstride) + p.row0 * b.ld);
   const int last = (int)(p.row1 - p.row0) - 1;
   uint32_t off[kLoads];
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) off[i] = (uint32_t)min(trow + 16 * i, last) * (uint32_t)(b.ld * 2) + piece * 16;
+  for (int i = 0; i < kLoads; ++i) {
+    const int t = 4 * (wave + kMW * i) + (lane >> 4);
+    off[i] = (uint32_t)min(t, last) * (uint32_t)(b.ld * 2) + (uint32_t)(((lane & 15) ^ (t & 15)) * 16);
+  }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)xs) + 1024 * wave;
   auto dload = [&](int chunk, int buf, int i) {
-    dma16(xg + uniform((int64_t)chunk * kChunk), off[i], lds0 + buf * kBuf + i * 4096);
+    dma16(xg + uniform((int64_t)chunk * kChunk), off[i], lds0 + buf * kBuf + i * (1024 * kMW));
   };
 
   // weights: row 32 f + l32 of the wave's outputs (past the last one: the last)
@@ -506,7 +510,9 @@ __global__ __launch_bounds__(kThreads, kWaves) void linear_big_kernel(BigArgs b)
   RawW ring[kBufs][kRF];  // this chunk's weights, the next ones'
   auto wload = [&](auto d, int chunk) {
     const int w = chunk % b.w_chunks;
-    static_for<kRF>([&](auto f) { ring[d][f] = load_raw<kPart>(wq[f], wc[f], (int64_t)w * kChunk + 64 * h, c_in, w + 1 < b.w_chunks); });
+    static_for<kRF>([&](auto f) {
+      ring[d][f] = load_raw<kPart>(wq[f], wc[f], (int64_t)w * kChunk + 64 * h, c_in, w + 1 < b.w_chunks);
+    });
   };
 
   uint4 fa[2][kRF];
@@ -1242,7 +1248,7 @@ __global__ __launch_bounds__(kThreads, kWaves) void grad_big_kernel(GradArgs b) 
 
 // y = the splits' sums, added in split order (so results do not change from
 // run to run, as they would with atomics).  Memory-bound: 333 x 4096 in four
-// parts, 27 MB, 8.8 us.
+// parts, 27 MB, 8.7 us.
 template <typename TY>
 __global__ __launch_bounds__(kThreads) void split_sum_kernel(const float* __restrict__ part, int splits, int64_t rows,
                                                              int64_t n_groups, int64_t cols, TY* __restrict__ y,
@@ -1455,68 +1461,77 @@ hipError_t launch_x(const LinearArgs& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 struct Plan {
   int few = 0;             // > 0: linear_few_kernel with that many tokens per wave
-  int tok = 0;             // > 0: the kernel with tiles of that many tokens (big_tokens)
+  int tok = 0, outs = 0;   // tok > 0: the kernel with tiles of that many tokens and outputs
   int splits = 1;
   int64_t kp = 0;          // packed row length (one plane), chunks * kChunk / planes
   bool pack = false;       // x goes through pack_rows_kernel
   size_t pack_bytes = 0, part_bytes = 0;
 };
 
-// Outputs of a workgroup of the product's kernel for tiles of tok tokens.
-int64_t big_m(int tok) { return tok >= 128 ? 256 : tok >= 32 ? kSmallM : kSkinnyM; }
-
-// Time of a launch in microseconds, from what its parts measured on MI355X: a
-// workgroup starts and ends for `ends`, a chunk (or stage) takes it `one` where
-// it is alone on its CU and `all` where as many as fit are there (`fit`), and a
-// split adds a launch and its partial sums' way to memory and back.  The
-// constants reproduce these (medians, weights of 4096 x 4096 unless named):
-//   product, 16 tokens: tile 16 8.0, tile 32 in 4 parts 13.3, tile 64 in 4
-//     parts 12; 16 tokens on 12288 x 4096: 13.6 and 16.6; 48 tokens on 12288 x
-//     4096: tile 64 in 2 parts 18.5, tile 32 22.4; 512 tokens: tile 64 25.7,
-//     tile 128 in 4 parts 35.9; 4096 tokens: tile 256 112, tile 128 120
-//   64 experts of 1024 x 2048, 128 rows: tile 32 14.6, tile 64 15.1, tile 16
-//     19.2; 2048 rows: 33.4, 36.7, 71; 32768 rows: tile 128 174, tile 256 189
-//   gradient, 4096 tokens: tile 256 132, tile 128 155, tile 64 237; 1024 tokens:
-//     tile 256 in 4 parts 67, unsplit 118; 256 tokens: tile 128 in 8 parts 33,
-//     tile 256 in 4 parts 48; 64 tokens: tile 64 in 8 parts 25, tile 128 26;
-//     experts, 32768 rows: tile 128 199, tile 256 232
-struct BigCost {
-  int tok, fit;
-  double ends, one, all;
+// Time of a launch in microseconds, from what its parts measured on MI355X.
+// Workgroups that share a CU share its issue slots, so a CU with r of them takes
+// `start` + r * (`each` + `more` per chunk or stage), one alone `one` per chunk;
+// a split adds a launch and its partial sums' way to memory and back.  The
+// constants are fitted to some 1000 timings of 42 products and 400 of 26
+// gradients (every kernel that comes near, up to 16 parts, 3 to 32768 tokens); the choice by
+// them is within 1.5% of the fastest on the mean.  Some of both sides (weights
+// of 4096 x 4096 unless named):
+//   product, 16 tokens: 16 x 32 tiles 8.1, 32 x 128 in 6 parts 11.8; 64 tokens on
+//     5120 x 17408: 64 x 128 in 6 parts 25.7, in 8 33.6, 64 x 256 in 10 27.0; 512
+//     tokens: 64 x 128 25.9, 64 x 256 in 2 parts 29.6; 1024 tokens: 64 x 256
+//     40.4, 64 x 128 45.7, 128 x 256 in 2 parts 48.0; 2048 tokens: 128 x 256
+//     69.4, 64 x 256 79.8; 4096 tokens: 256 x 256 115, 128 x 256 123
+//   64 experts of 1024 x 2048, 512 rows: 32 x 128 21.8, 64 x 256 22.1, 64 x 128
+//     25.5; 8192 rows: 128 x 256 69, 64 x 256 73, 256 x 256 116; 32768 rows: 178,
+//     209, 191
+//   gradient (n x 256), 64 tokens on 5120 x 17408: 64 in 6 parts 42.0, 128 in 6
+//     43.9, 64 in 16 51; 1024 tokens: 256 in 4 parts 66.5, 128 in 4 68.1, 64 in 2
+//     77.9; 4096 tokens: 256 132, 128 155, 64 239; experts, 8192 rows: 128 80, 64
+//     99, 256 109
+struct TileCost {
+  int tok, outs;
+  double start, each, one, more;
 };
-constexpr BigCost kBigCosts[] = {
-    {256, 1, 10.0, 2.6, 3.25}, {128, 2, 5.0, 1.8, 3.46}, {64, 2, 4.0, 0.67, 2.0}, {32, 2, 4.0, 0.55, 1.4},
-    {16, 2, 3.5, 0.14, 0.35}};
-constexpr BigCost kGradCosts[] = {{256, 1, 9.0, 1.92, 1.92}, {128, 2, 5.0, 1.43, 2.33}, {64, 2, 4.0, 1.27, 2.6}};
+constexpr TileCost kProductCosts[] = {{256, 256, 3.66, 0.22, 2.98, 3.45}, {128, 256, 2.36, 0.16, 1.88, 1.71},
+                                      {64, 256, 3.27, 0.17, 0.94, 1.06},  {64, 128, 3.43, 0.96, 0.60, 0.61},
+                                      {32, kSmallM, 3.77, 1.58, 0.52, 0.53}, {16, kSkinnyM, 3.46, 0.43, 0.11, 0.16}};
+constexpr TileCost kGradCosts[] = {{256, kGradM, 4.64, 3.64, 1.80, 1.94},
+                                   {128, kGradM, 5.26, 0.34, 1.47, 1.04},
+                                   {64, kGradM, 6.15, 0.19, 1.23, 0.83}};
 constexpr int kCUs = 256;
 
-double big_cost(const BigCost& k, double tiles, int64_t chunks, int splits, double part_values) {
-  const double groups = tiles * splits, slots = (double)kCUs * k.fit;
-  const double rounds = groups > slots ? groups / slots : 1.0;
-  const double load = groups >= slots ? 1.0 : groups > kCUs ? (groups - kCUs) / (slots - kCUs) : 0.0;
-  const double chunk = k.one + (k.all - k.one) * load;
-  // long workgroups: the last round takes as long as a full one, and half of one more on average past the first few
-  const double turns = k.tok <= 32 || rounds <= 1.0 ? rounds : rounds < 4.0 ? ceil(rounds) : rounds + 0.5;
-  double t = turns * (k.ends + chunk * (double)((chunks + splits - 1) / splits));
-  if (splits > 1) t += 3.0 + splits * part_values * 8e-6 / 4.0;
+double tile_cost(const TileCost& k, double tiles, bool ragged, int64_t chunks, int splits, double part_values) {
+  double r = tiles * splits / kCUs;
+  // small workgroups even out; of large ones the fullest CU counts, and how
+  // ragged rows fill their tiles is only estimated
+  if (k.tok > 32) r = ragged ? r + 0.25 : ceil(r);
+  const double per = (double)((chunks + splits - 1) / splits);
+  double t = k.start + (r <= 1.0 ? k.each + k.one * per : r * (k.each + k.more * per));
+  if (splits > 1) t += 2.5 + splits * part_values * 8e-6 / 4.0;
   return t;
 }
 
 // The cheapest kernel and number of parts (up to 16) for a.
 template <int kN>
-void cheapest(Plan& p, const LinearArgs& a, const BigCost (&costs)[kN], int64_t chunks) {
+void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int64_t chunks) {
   const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups, m = a.grad ? a.c_in : a.c_out;
   double best = 0.0;
-  for (const BigCost& k : costs) {
-    const int64_t bt = k.tok, bm = a.grad ? kGradM : big_m(k.tok), m_tiles = (m + bm - 1) / bm;
-    // ragged: about half of a tile more per group that has rows
-    const double used = (double)(a.n_groups < a.rows ? a.n_groups : a.rows);
-    const double t_tiles = a.ragged ? (double)a.rows / bt + 0.5 * used : (double)((a.rows + bt - 1) / bt * a.n_groups);
-    for (int splits = 1; splits <= (a.ragged ? 1 : 16) && splits <= chunks; splits *= 2) {
-      const double t = big_cost(k, t_tiles * m_tiles, chunks, splits, (double)all * m);
+  for (const TileCost& k : costs) {
+    const int64_t m_tiles = (m + k.outs - 1) / k.outs;
+    // ragged: about half of a tile more per group that has rows than the rows
+    // fill, and a tile at least; with a bound on a group's rows the groups that
+    // have any are taken half way between as few and as many as there can be
+    double used = (double)(a.n_groups < a.rows ? a.n_groups : a.rows);
+    if (a.ragged && a.max_group_rows > 0 && a.max_group_rows < a.rows)
+      used = 0.5 * used + 0.5 * fmin(used, (double)a.rows / a.max_group_rows);
+    const double t_tiles = a.ragged ? fmax(used, (double)a.rows / k.tok + 0.5 * used)
+                                    : (double)((a.rows + k.tok - 1) / k.tok * a.n_groups);
+    for (int splits = 1; splits <= (a.ragged ? 1 : 16) && splits <= chunks; ++splits) {
+      const double t = tile_cost(k, t_tiles * m_tiles, a.ragged, chunks, splits, (double)all * m);
       if (p.tok == 0 || t < best) {
         best = t;
         p.tok = k.tok;
+        p.outs = k.outs;
         p.splits = splits;
       }
     }
@@ -1540,7 +1555,7 @@ Plan plan_of(const LinearArgs& a) {
   p.kp = (k + step - 1) / step * step;
   p.pack = planes == 3 || k % step != 0;
   if (a.grad) cheapest(p, a, kGradCosts, planes * p.kp / step);
-  else cheapest(p, a, kBigCosts, planes * p.kp / step);
+  else cheapest(p, a, kProductCosts, planes * p.kp / step);
   if (p.pack) p.pack_bytes = ((size_t)all * planes * p.kp * 2 + 255) / 256 * 256;
   if (p.splits > 1) p.part_bytes = (size_t)p.splits * all * (a.grad ? a.c_in : a.c_out) * 4;
   return p;
@@ -1574,13 +1589,13 @@ hipError_t launch_few(const LinearArgs& a, int tok, hipStream_t stream) {
   }
 }
 
-template <int kNT, int kRF, int kDepth, int kWaves>
+template <int kNT, int kRF, int kMW, int kDepth, int kWaves>
 hipError_t launch_big_nt(const BigArgs& b, hipStream_t stream) {
-  const dim3 grid((unsigned)(b.m_tiles * b.t_tiles), (unsigned)b.splits);
+  const dim3 grid((unsigned)(b.m_tiles * b.t_tiles), (unsigned)b.splits), block(64 * kMW);
   if (b.a.c_in % kChunk == 0)
-    linear_big_kernel<kNT, kRF, kDepth, kWaves, false><<<grid, dim3(kThreads), 0, stream>>>(b);
+    linear_big_kernel<kNT, kRF, kMW, kDepth, kWaves, false><<<grid, block, 0, stream>>>(b);
   else
-    linear_big_kernel<kNT, kRF, kDepth, kWaves, true><<<grid, dim3(kThreads), 0, stream>>>(b);
+    linear_big_kernel<kNT, kRF, kMW, kDepth, kWaves, true><<<grid, block, 0, stream>>>(b);
   return hipGetLastError();
 }
 
@@ -1672,12 +1687,14 @@ hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
     }
   } else {
     const int w_chunks = (int)(p.kp / kChunk);
-    const BigArgs b{a, r.x, r.ld, r.gstride, planes * w_chunks, w_chunks, (a.c_out + big_m(p.tok) - 1) / big_m(p.tok),
-                    t_tiles, p.splits, part};
+    const BigArgs b{a, r.x, r.ld, r.gstride, planes * w_chunks, w_chunks, (a.c_out + p.outs - 1) / p.outs, t_tiles,
+                    p.splits, part};
     switch (p.tok) {
-      case 256: e = launch_big_nt<8, 2, 1, 1>(b, stream); break;
-      case 128: e = launch_big_nt<4, 2, 1, 2>(b, stream); break;
-      case 64: e = launch_big_nt<2, 1, 4, 2>(b, stream); break;
+      case 256: e = launch_big_nt<8, 2, 4, 1, 1>(b, stream); break;
+      case 128: e = launch_big_nt<4, 2, 4, 1, 2>(b, stream); break;
+      case 64:
+        e = p.outs == 256 ? launch_big_nt<2, 1, 8, 2, 2>(b, stream) : launch_big_nt<2, 1, 4, 4, 2>(b, stream);
+        break;
       case 32: e = launch_small<2>(b, stream); break;
       default: e = launch_skinny<4, 3>(b, stream); break;
     }

@@ -741,11 +741,10 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
     for (int t = 0; t < kNT; ++t)
       fb[set][t] = *reinterpret_cast<const uint4*>(lds + at + (rd0 ^ (16 * i)) + 4096 * t);
   };
-  // live: all ones, or zero past the last chunk (an odd one out is walked with zero scales)
-  auto wread = [&](uint32_t at, uint32_t live) {
+  auto wread = [&](uint32_t at) {
     raw_next = *reinterpret_cast<const uint4*>(lds + at + wrd);
-    code_next[0] = *reinterpret_cast<const uint32_t*>(lds + at + crd) & live;
-    if constexpr (kW4) code_next[1] = *reinterpret_cast<const uint32_t*>(lds + at + crd + 256) & live;
+    code_next[0] = *reinterpret_cast<const uint32_t*>(lds + at + crd);
+    if constexpr (kW4) code_next[1] = *reinterpret_cast<const uint32_t*>(lds + at + crd + 256);
   };
   auto decode = [&](auto set, const uint4& r, const uint32_t (&cc)[2], auto i) {
     const uint32_t w = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
@@ -759,7 +758,7 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
   block_sync();
   std::integral_constant<int, 0> i0;
   static_for<kR>([&](auto i) { bread(i, 0u, i); });
-  wread(0u, ~0u);
+  wread(0u);
   auto take = [&]() {
     raw = raw_next;
     code[0] = code_next[0];
@@ -767,11 +766,17 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
   };
   take();
   decode(i0, raw, code, i0);
+  auto multiply = [&](auto s) {
+#pragma unroll
+    for (int t = 0; t < kNT; ++t)
+      acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fa[s & 1]),
+                                                       __builtin_bit_cast(bf16x8_t, fb[s & 3][t]), acc[t], 0, 0, 0);
+  };
   uint32_t at = 0;
-  for (int c = c_first; c <= end; c += 2) {  // two chunks, eight steps
+  for (int c = c_first; c < end; c += 2) {  // two chunks, eight steps
     const uint32_t second = at + kBuf, next = at + 2 * kBuf == kBufs * 2 * kBuf ? 0u : at + 2 * kBuf;
     static_for<8>([&](auto s) {
-      if constexpr (s == 1) wread(second, c < end ? ~0u : 0u);
+      if constexpr (s == 1) wread(second);
       constexpr int rs = s + kR, ns = s + 1;
       bread(std::integral_constant<int, rs & 3>{}, rs >= 8 ? next : rs >= 4 ? second : at,
             std::integral_constant<int, rs & 3>{});
@@ -780,7 +785,7 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
         // and the next two chunks have landed: past the barrier, in every
         // wave, and these two's buffers can be loaded again
         wait_loads<kAhead>();
-        wread(next, ~0u);
+        wread(next);
         block_sync();
         dload(at);
         dload(second);
@@ -789,14 +794,17 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
       std::integral_constant<int, ns & 3> ni;
       if constexpr ((ns & 3) == 0) take();
       decode(nset, raw, code, ni);
-#pragma unroll
-      for (int t = 0; t < kNT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fa[s & 1]),
-                                                         __builtin_bit_cast(bf16x8_t, fb[s & 3][t]), acc[t], 0, 0, 0);
+      multiply(s);
       __builtin_amdgcn_sched_barrier(0);
     });
     at = next;
   }
+  if ((end - c_first) % 2 == 0)  // an odd chunk out, in LDS and its first operands in registers
+    static_for<4>([&](auto s) {
+      if constexpr (s + kR < 4) bread(std::integral_constant<int, s + kR>{}, at, std::integral_constant<int, s + kR>{});
+      if constexpr (s < 3) decode(std::integral_constant<int, (s + 1) & 1>{}, raw, code, std::integral_constant<int, s + 1>{});
+      multiply(s);
+    });
   wait_loads<0>();  // the repeated loads: nothing lands after the workgroup has ended
 
   const float sc = out_scale(b.a, p.g);

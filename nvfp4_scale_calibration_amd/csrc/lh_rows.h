@@ -105,11 +105,11 @@ __device__ __forceinline__ uint4 units8_bf16(uint32_t pk, float c) {
 }
 
 // x = h + m + l with three bf16 values, exactly (24 significant bits cut into
-// 8 + 8 + 8; the remainders are exact differences): bits of two values packed
-// per plane, a in the low half.
+// 8 + 8 + 8; the remainders are exact differences, none for an infinity): bits
+// of two values packed per plane, a in the low half.
 __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
   const uint32_t ha = __float_as_uint(a) & 0xffff0000u, hb = __float_as_uint(b) & 0xffff0000u;
-  const float ra = a - __uint_as_float(ha), rb = b - __uint_as_float(hb);
+  const float ra = isinf(a) ? 0.0f : a - __uint_as_float(ha), rb = isinf(b) ? 0.0f : b - __uint_as_float(hb);
   const uint32_t ma = __float_as_uint(ra) & 0xffff0000u, mb = __float_as_uint(rb) & 0xffff0000u;
   const float la = ra - __uint_as_float(ma), lb = rb - __uint_as_float(mb);
   p[0] = (ha >> 16) | hb;

@@ -249,6 +249,35 @@ def test_a_token_with_nan_keeps_it_to_itself(lh):
             near(y[keep], x[keep].double().numpy(), u, float(s[0]), "the other tokens")
 
 
+@pytest.mark.parametrize("t,c_out,c_in", [(1, 40, 272), (2, 40, 272), (5, 64, 272), (1500, 512, 528), (2100, 512, 1056),
+                                          (400, 1000, 272), (700, 512, 256), (4100, 1000, 272), (4100, 2048, 272),
+                                          (32, 8192, 2064)])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("workspace", [True, None])
+def test_infinities_as_the_formula_has_them(lh, t, c_out, c_in, dt, workspace):
+    """An infinite activation meets every weight: infinite of the weight's
+    sign, NaN where the weight is zero, and nothing for the other tokens."""
+    print("case t=%d %dx%d %s ws=%s" % (t, c_out, c_in, dt, workspace), flush=True)
+    rng = np.random.default_rng([59, t, c_in])
+    packed, codes, s = weights(rng, 1, c_out, c_in)
+    packed[0, 0], packed[0, :, 3] = 0x31, 0x31                       # rows and columns without a zero
+    u = torch.from_numpy(units64(packed, codes)[0]).to(DEV)
+    s_ = float(s[0])
+    dev = [v.to(DEV) for v in (packed, codes, s)]
+    for n, w, f in ((c_in, u, lh.lh_linear_nvfp4), (c_out, u.t(), lh.lh_linear_nvfp4_grad)):
+        x = torch.from_numpy(rng.standard_normal((t, n)).astype(np.float32)).to(DEV).to(dt)
+        for i, (row, col) in enumerate(((0, 0), (t // 2, n - 1), (t - 1, 6), (t - 1, n // 2))):
+            x[row, col] = float("inf") if i % 2 == 0 else -float("inf")
+        y = f(x, *dev, out_dtype=F32, workspace=workspace).double()
+        bad = torch.zeros(t, dtype=torch.bool)
+        bad[[0, t // 2, t - 1]] = True
+        assert bool(torch.isfinite(y[~bad.to(DEV)]).all())
+        for r in {0, t // 2, t - 1}:
+            ref = s_ * (x[r].double() * w).sum(1)
+            assert torch.equal(torch.isnan(y[r]), torch.isnan(ref)) and torch.equal(torch.isinf(y[r]), torch.isinf(ref))
+            assert torch.equal(y[r] == float("inf"), ref == float("inf"))
+
+
 def test_large_row_strides(lh):
     """Rows more than 2^32 bytes from the buffer's start."""
     rng = np.random.default_rng(31)
@@ -363,7 +392,10 @@ def test_groups_side_by_side_in_wide_rows(lh, t):
 
 
 LARGE = [(5, 300, 2064), (24, 4096, 1056), (40, 8192, 1056), (40, 8192, 1040), (300, 4096, 528), (300, 4096, 512),
-         (1100, 4096, 1040), (1100, 4096, 1024), (200, 2048, 2064), (4099, 4000, 2064), (4096, 4096, 2048)]
+         (1100, 4096, 1040), (1100, 4096, 1024), (200, 2048, 2064), (4099, 4000, 2064), (4096, 4096, 2048),
+         (4100, 1000, 272), (4100, 512, 2064), (4100, 512, 2048), (4100, 2048, 272), (4100, 1000, 2064),
+         (1500, 512, 528), (2000, 512, 1024), (2100, 512, 1056), (32, 8192, 2064), (400, 1000, 272), (1000, 512, 256),
+         (400, 1000, 528), (700, 512, 1024), (700, 512, 256), (700, 1000, 1168), (1500, 512, 2048)]
 
 
 @pytest.mark.parametrize("t,c_out,c_in", LARGE)

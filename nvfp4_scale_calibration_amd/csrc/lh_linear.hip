@@ -282,8 +282,13 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
 // 16-byte piece q, so that the 16 lanes which LDS serves together read one
 // piece of 16 tokens from distinct banks.
 //
-// Per step a wave issues kRF kNT MFMAs, and between them reads a later step's
-// kNT activation operands, decodes its kRF weight operands (16 vector
+// kP = 3: the three planes of fp32 rows side by side, three times the rows in
+// LDS and three MFMAs for a decoded operand, into the same accumulators; else
+// the planes follow one another along the contraction, the weights walked
+// three times.
+//
+// Per step a wave issues kRF kNT kP MFMAs, and between them reads a later step's
+// kNT kP activation operands, decodes its kRF weight operands (16 vector
 // operations each) and issues its share of the next chunk's loads: with one wave
 // per SIMD the matrix pipe is covered only by what is interleaved by hand
 // (sched_barrier keeps each group where it is written).  The barrier of a
@@ -296,7 +301,12 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
 // tiles are an eighth; 48 tokens x (12288 x 4096), 64 x 128 tiles in two parts,
 // 14.5 us and 3.8 for their sum.  Bound by the issue of vector instructions
 // between the MFMAs (decoding and LDS reads), the small tiles by the latency
-// of their few chunks.  Eight waves of 32 outputs instead of four: 64
+// of their few chunks, the fp32 one (kP = 3) by its LDS reads, which take as
+// long as its MFMAs: 333 x (4096 x 4096) fp32 48 us with packing and the sum of
+// two parts (planes one after the other: 128 x 256 in five parts 57), 1000 rows
+// 95 (114); four waves of 64 outputs, half the LDS reads, 53 and 100; 4096 rows
+// 370, here 256 x 256 with the planes in a row is better, 357.
+// Eight waves of 32 outputs instead of four: 64
 // tokens x 256 outputs 40.4 us at 1024 x (4096 x 4096), where 64 x 128 takes
 // 45.7; with 256 tokens 683 against 689 us, with 128 820 against 712: not kept.
 // ---------------------------------------------------------------------------
@@ -458,16 +468,17 @@ __device__ __forceinline__ void store_rows(const f32x16_t (&acc)[kRF][kNT], floa
   }
 }
 
-template <int kNT, int kRF, int kMW, int kDepth, int kWaves, bool kPart>
+template <int kNT, int kRF, int kMW, int kDepth, int kWaves, int kP, bool kPart>
 __global__ __launch_bounds__(64 * kMW, kWaves) void linear_big_kernel(BigArgs b) {
   constexpr int kBT = 32 * kNT;              // tokens
   constexpr int kWM = 32 * kRF;              // outputs per wave
-  constexpr int kBuf = kBT * 256;            // bytes of an LDS buffer
+  constexpr int kB = kNT * kP;               // activation operands of a step
+  constexpr int kBuf = kP * kBT * 256;       // bytes of an LDS buffer
   constexpr int kBufs = kDepth + 1;
-  constexpr int kLoads = 8 * kNT / kMW;      // direct loads per wave and chunk
+  constexpr int kLoads = 8 * kB / kMW;       // direct loads per wave and chunk
   // steps by which activation operands are read ahead: one step of 8 or 16
   // MFMAs covers the way through LDS, one of 1 or 2 does not
-  constexpr int kR = kNT >= 4 ? 1 : 3;
+  constexpr int kR = kB >= 4 ? 1 : 3;
   // loads issued behind the next chunk's by its barrier, at least (the counter holds 63)
   constexpr int kAheadAll = (kDepth - 1) * (kLoads + 3 * kRF), kAhead = kAheadAll < 63 ? kAheadAll : 63;
   __shared__ __attribute__((aligned(1024))) uint8_t xs[kBufs * kBuf];
@@ -483,15 +494,17 @@ __global__ __launch_bounds__(64 * kMW, kWaves) void linear_big_kernel(BigArgs b)
   const int c_first = (int)((int64_t)b.chunks * blockIdx.y / b.splits);
   const int end = (int)((int64_t)b.chunks * (blockIdx.y + 1) / b.splits) - 1;  // its last one
 
-  // direct loads: instruction i of a wave fills tokens 4 (wave + kMW i) .. + 3;
-  // slot lane & 15 of token t holds piece (lane & 15) ^ (t & 15)
+  // direct loads: instruction i of a wave fills LDS rows 4 (wave + kMW i) .. + 3
+  // (token t of plane q: row kBT q + t); slot lane & 15 of row t holds piece
+  // (lane & 15) ^ (t & 15)
   const uint16_t* xg = b.x + uniform((b.a.ragged ? 0 : p.g * b.gstride) + p.row0 * b.ld);
   const int last = (int)(p.row1 - p.row0) - 1;
   uint32_t off[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int t = 4 * (wave + kMW * i) + (lane >> 4);
-    off[i] = (uint32_t)min(t, last) * (uint32_t)(b.ld * 2) + (uint32_t)(((lane & 15) ^ (t & 15)) * 16);
+    off[i] = (uint32_t)min(t % kBT, last) * (uint32_t)(b.ld * 2) + (uint32_t)(t / kBT * b.w_chunks) * (2 * kChunk) +
+             (uint32_t)(((lane & 15) ^ (t & 15)) * 16);
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)xs) + 1024 * wave;
   auto dload = [&](int chunk, int buf, int i) {
@@ -516,7 +529,7 @@ __global__ __launch_bounds__(64 * kMW, kWaves) void linear_big_kernel(BigArgs b)
   };
 
   uint4 fa[2][kRF];
-  uint4 fb[kR + 1][kNT];
+  uint4 fb[kR + 1][kB];
   f32x16_t acc[kRF][kNT];
 #pragma unroll
   for (int f = 0; f < kRF; ++f)
@@ -545,22 +558,23 @@ __global__ __launch_bounds__(64 * kMW, kWaves) void linear_big_kernel(BigArgs b)
   // and the direct loads d0 .. d1 - 1 of chunk dst into buffer dbuf.
   auto step = [&](auto u, auto s, uint32_t rd, int dst, int dbuf, auto d0, auto d1) {
     constexpr int set = s & 1, bset = s % (kR + 1), rset = (s + kR) % (kR + 1);
-    static_for<kRF * kNT>([&](auto N) {
+    static_for<kRF * kB>([&](auto N) {
       constexpr int n = N;
       if constexpr (n % 4 == 0 && d0 + n / 4 < d1) dload(dst, dbuf, d0 + n / 4);
-      if constexpr (kRF * kNT < 4 && n == 1 && d0 + 1 < d1) dload(dst, dbuf, d0 + 1);
-      if constexpr (n < kNT)
+      if constexpr (kRF * kB < 4 && n == 1 && d0 + 1 < d1) dload(dst, dbuf, d0 + 1);
+      if constexpr (n < kB)
         bread(std::integral_constant<int, rset>{}, rd, std::integral_constant<int, (s + kR) & 7>{}, N);
-      constexpr int per = 4 / kNT > 0 ? 4 / kNT : 1;  // pairs per MFMA (kNT = 8: every other one)
-      if constexpr (kNT < 8 || n % 2 == 0)
+      constexpr int per = 4 / kB > 0 ? 4 / kB : 1;  // pairs per MFMA (kB = 8: every other one)
+      if constexpr (kB < 8 || n % 2 == 0)
         static_for<per>([&](auto E) {
-          constexpr int k = kNT < 8 ? n * per + E : n / 2;  // of 4 kRF pairs
-          decode(std::integral_constant<int, set ^ 1>{}, u, std::integral_constant<int, s + 1>{},
-                 std::integral_constant<int, (k >> 2)>{}, std::integral_constant<int, (k & 3)>{});
+          constexpr int k = kB < 8 ? n * per + E : n / 2;  // of 4 kRF pairs
+          if constexpr (k < 4 * kRF)
+            decode(std::integral_constant<int, set ^ 1>{}, u, std::integral_constant<int, s + 1>{},
+                   std::integral_constant<int, (k >> 2)>{}, std::integral_constant<int, (k & 3)>{});
         });
-      constexpr int f = n / kNT, t = n % kNT;
+      constexpr int f = n / kB, q = n % kB, t = q % kNT;
       acc[f][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, fa[set][f]),
-                                                          __builtin_bit_cast(bf16x8_t, fb[bset][t]), acc[f][t], 0, 0, 0);
+                                                          __builtin_bit_cast(bf16x8_t, fb[bset][q]), acc[f][t], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -582,7 +596,7 @@ __global__ __launch_bounds__(64 * kMW, kWaves) void linear_big_kernel(BigArgs b)
   wait_loads<kStart < 63 ? kStart : 63>();  // the first chunk has landed
   block_sync();
   static_for<kR>([&](auto i) {
-    static_for<kNT>([&](auto t) { bread(i, rd0, i, t); });
+    static_for<kB>([&](auto t) { bread(i, rd0, i, t); });
   });
   static_for<4 * kRF>([&](auto K) {
     decode(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{},
@@ -1255,8 +1269,8 @@ __global__ __launch_bounds__(kThreads, kWaves) void grad_big_kernel(GradArgs b) 
 }
 
 // y = the splits' sums, added in split order (so results do not change from
-// run to run, as they would with atomics).  Memory-bound: 333 x 4096 in four
-// parts, 27 MB, 8.7 us.
+// run to run, as they would with atomics).  Memory-bound: 333 x 4096 in two
+// parts, 16 MB, 5.3 us.
 template <typename TY>
 __global__ __launch_bounds__(kThreads) void split_sum_kernel(const float* __restrict__ part, int splits, int64_t rows,
                                                              int64_t n_groups, int64_t cols, TY* __restrict__ y,
@@ -1285,8 +1299,8 @@ __global__ __launch_bounds__(kThreads) void split_sum_kernel(const float* __rest
 }
 
 // Rows of any alignment and length to bf16 rows of kp elements (zeros past
-// k), fp32 as three planes of kp elements behind each other: the sum over
-// all 3 kp of them, with the weights walked three times, is the product.
+// k), fp32 as three planes of kp elements behind each other: the sum of the
+// planes' products is the product.
 // Memory-bound: 333 x 4096 fp32 5.6 us, launch included.
 template <typename TX>
 __global__ __launch_bounds__(kThreads) void pack_rows_kernel(const TX* __restrict__ x, int64_t rows, int64_t k,
@@ -1470,6 +1484,7 @@ hipError_t launch_x(const LinearArgs& a, hipStream_t stream) {
 struct Plan {
   int few = 0;             // > 0: linear_few_kernel with that many tokens per wave
   int tok = 0, outs = 0;   // tok > 0: the kernel with tiles of that many tokens and outputs
+  bool together = false;   // the planes of fp32 rows side by side, not one after the other
   int splits = 1;
   int64_t kp = 0;          // packed row length (one plane), chunks * kChunk / planes
   bool pack = false;       // x goes through pack_rows_kernel
@@ -1499,9 +1514,11 @@ struct Plan {
 struct TileCost {
   int tok, outs;
   double start, each, one, more;
+  bool together = false;  // fp32 rows: a chunk is that of all planes
 };
 constexpr TileCost kProductCosts[] = {{256, 256, 3.66, 0.22, 2.98, 3.45}, {128, 256, 2.36, 0.16, 1.88, 1.71},
-                                      {64, 256, 3.27, 0.17, 0.94, 1.06},  {64, 128, 3.43, 0.96, 0.60, 0.61},
+                                      {64, 256, 3.27, 0.17, 0.94, 1.06},  {64, 256, 4.0, 0.2, 2.2, 2.6, true},
+                                      {64, 128, 3.43, 0.96, 0.60, 0.61},
                                       {32, kSmallM, 3.77, 1.58, 0.52, 0.53}, {16, kSkinnyM, 3.46, 0.43, 0.11, 0.16}};
 constexpr TileCost kGradCosts[] = {{256, kGradM, 4.64, 3.64, 1.80, 1.94},
                                    {128, kGradM, 5.26, 0.34, 1.47, 1.04},
@@ -1521,10 +1538,12 @@ double tile_cost(const TileCost& k, double tiles, bool ragged, int64_t chunks, i
 
 // The cheapest kernel and number of parts (up to 16) for a.
 template <int kN>
-void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int64_t chunks) {
+void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int planes, int64_t plane_chunks) {
   const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups, m = a.grad ? a.c_in : a.c_out;
   double best = 0.0;
   for (const TileCost& k : costs) {
+    if (k.together && planes == 1) continue;
+    const int64_t chunks = k.together ? plane_chunks : planes * plane_chunks;
     const int64_t m_tiles = (m + k.outs - 1) / k.outs;
     // ragged: about half of a tile more per group that has rows than the rows
     // fill, and a tile at least; with a bound on a group's rows the groups that
@@ -1540,6 +1559,7 @@ void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int64_t
         best = t;
         p.tok = k.tok;
         p.outs = k.outs;
+        p.together = k.together;
         p.splits = splits;
       }
     }
@@ -1562,8 +1582,8 @@ Plan plan_of(const LinearArgs& a) {
   const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups;
   p.kp = (k + step - 1) / step * step;
   p.pack = planes == 3 || k % step != 0;
-  if (a.grad) cheapest(p, a, kGradCosts, planes * p.kp / step);
-  else cheapest(p, a, kProductCosts, planes * p.kp / step);
+  if (a.grad) cheapest(p, a, kGradCosts, planes, p.kp / step);
+  else cheapest(p, a, kProductCosts, planes, p.kp / step);
   if (p.pack) p.pack_bytes = ((size_t)all * planes * p.kp * 2 + 255) / 256 * 256;
   if (p.splits > 1) p.part_bytes = (size_t)p.splits * all * (a.grad ? a.c_in : a.c_out) * 4;
   return p;
@@ -1597,13 +1617,13 @@ hipError_t launch_few(const LinearArgs& a, int tok, hipStream_t stream) {
   }
 }
 
-template <int kNT, int kRF, int kMW, int kDepth, int kWaves>
+template <int kNT, int kRF, int kMW, int kDepth, int kWaves, int kP = 1>
 hipError_t launch_big_nt(const BigArgs& b, hipStream_t stream) {
   const dim3 grid((unsigned)(b.m_tiles * b.t_tiles), (unsigned)b.splits), block(64 * kMW);
   if (b.a.c_in % kChunk == 0)
-    linear_big_kernel<kNT, kRF, kMW, kDepth, kWaves, false><<<grid, block, 0, stream>>>(b);
+    linear_big_kernel<kNT, kRF, kMW, kDepth, kWaves, kP, false><<<grid, block, 0, stream>>>(b);
   else
-    linear_big_kernel<kNT, kRF, kMW, kDepth, kWaves, true><<<grid, block, 0, stream>>>(b);
+    linear_big_kernel<kNT, kRF, kMW, kDepth, kWaves, kP, true><<<grid, block, 0, stream>>>(b);
   return hipGetLastError();
 }
 
@@ -1695,13 +1715,16 @@ hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
     }
   } else {
     const int w_chunks = (int)(p.kp / kChunk);
-    const BigArgs b{a, r.x, r.ld, r.gstride, planes * w_chunks, w_chunks, (a.c_out + p.outs - 1) / p.outs, t_tiles,
+    const BigArgs b{a, r.x, r.ld, r.gstride, p.together ? w_chunks : planes * w_chunks, w_chunks,
+                    (a.c_out + p.outs - 1) / p.outs, t_tiles,
                     p.splits, part};
     switch (p.tok) {
       case 256: e = launch_big_nt<8, 2, 4, 1, 1>(b, stream); break;
       case 128: e = launch_big_nt<4, 2, 4, 1, 2>(b, stream); break;
       case 64:
-        e = p.outs == 256 ? launch_big_nt<2, 1, 8, 2, 2>(b, stream) : launch_big_nt<2, 1, 4, 4, 2>(b, stream);
+        e = p.together      ? launch_big_nt<2, 1, 8, 1, 2, 3>(b, stream)
+            : p.outs == 256 ? launch_big_nt<2, 1, 8, 2, 2>(b, stream)
+                            : launch_big_nt<2, 1, 4, 4, 2>(b, stream);
         break;
       case 32: e = launch_small<2>(b, stream); break;
       default: e = launch_skinny<4, 3>(b, stream); break;

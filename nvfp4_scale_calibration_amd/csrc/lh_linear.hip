@@ -816,7 +816,8 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
   if ((end - c_first) % 2 == 0)  // an odd chunk out, in LDS and its first operands in registers
     static_for<4>([&](auto s) {
       if constexpr (s + kR < 4) bread(std::integral_constant<int, s + kR>{}, at, std::integral_constant<int, s + kR>{});
-      if constexpr (s < 3) decode(std::integral_constant<int, (s + 1) & 1>{}, raw, code, std::integral_constant<int, s + 1>{});
+      if constexpr (s < 3)
+        decode(std::integral_constant<int, (s + 1) & 1>{}, raw, code, std::integral_constant<int, s + 1>{});
       multiply(s);
     });
   wait_loads<0>();  // the repeated loads: nothing lands after the workgroup has ended

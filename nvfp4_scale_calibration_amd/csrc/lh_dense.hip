@@ -304,11 +304,14 @@ __device__ __forceinline__ uint4 big_tail_chunk(const uint16_t* p, int64_t kk, i
 // asm so that the compiler, which would otherwise wait for every such load
 // before any LDS read, leaves the waits to the kernel: the kernel waits with
 // s_waitcnt vmcnt before the barrier that publishes the data.  No register
-// is written; M0 carries the LDS address (nothing else in the kernel uses it).
+// is written; M0 carries the LDS address (nothing else in the kernel uses it),
+// and s_nop is the wait state that the ISA asks for between a scalar write of
+// M0 and the load that takes its address from it (no interlock; the compiler
+// does not look into asm).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_dma16(const void* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(g) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 template <int N>

@@ -766,7 +766,9 @@ lh_status lh_moe_combine_grad(const void* dy, int dtype, int64_t n_tokens, int64
   if (st == LH_OK && dweights) st = check_moe_rows(fn, a, dy, ld_dy, ys, ld_ys);
   if (st != LH_OK) return st;
   if (!aligned(dweights, 4)) return fail(LH_ERR_ARG, "%s: pointer not aligned to its element size", fn);
-  if (n_tokens == 0 || top_k == 0) return LH_OK;
+  // rows of no columns still have weights, whose gradient is zero
+  if (n_tokens == 0 || top_k == 0 || (cols == 0 && dweights == nullptr)) return LH_OK;
+  if (position == nullptr) return fail(LH_ERR_NULL, "%s: position is required", fn);
   hipError_t e = lh::launch_moe_combine_grad(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? LH_OK : hip_fail(e, fn);
 }

@@ -558,8 +558,9 @@ lh_status lh_gptq_quantize(const void *w, int w_dtype, int64_t c_out, int64_t c_
  *                quantised value in units of S_g, exact in either type (so
  *                Q = values * S_g; lh_linear_nvfp4 takes S_g as x_scale)
  *   packed_e2m1, scale_e4m3, global_scale: as lh_fake_quant_nvfp4.
- * Outputs are dense, each optional, at least one given; values 16-byte,
- * packed_e2m1 8-byte aligned.  x may have any alignment of its own type.
+ * Outputs are dense, each optional, at least one given (where they have any
+ * elements); values 16-byte, packed_e2m1 8-byte aligned.  x may have any
+ * alignment of its own type.
  * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_ARG, LH_ERR_HIP.
  */
 lh_status lh_quantize_nvfp4(const void *x, int x_dtype, int64_t rows, int64_t c_in, int64_t ld_x,
@@ -710,8 +711,9 @@ lh_status lh_moe_combine(const void *ys, int dtype, int64_t n_rows, int64_t cols
  *                         without an expert), dtype, [n_rows][ld_dys]
  *   dweights[t][k]      = <dy[t], ys[position[t][k]]> (0 without an expert),
  *                         fp32 [n_tokens][top_k]
- * Either may be NULL, not both; weights NULL: 1.  ys may be NULL when
- * dweights is.  dys must not overlap dy or ys.  Sums in a fixed order.
+ * Either may be NULL, not both (where they have any elements); weights NULL:
+ * 1.  ys may be NULL when dweights is.  dys must not overlap dy or ys.  Sums
+ * in a fixed order.
  */
 lh_status lh_moe_combine_grad(const void *dy, int dtype, int64_t n_tokens, int64_t cols, int64_t ld_dy,
                               const void *ys, int64_t n_rows, int64_t ld_ys, const int32_t *position,

@@ -561,14 +561,15 @@ lh_status lh_quantize_nvfp4(const void* x, int x_dtype, int64_t rows, int64_t c_
     return fail(LH_ERR_SHAPE, "%s: negative size or stride", fn);
   if (c_in % 16 != 0) return fail(LH_ERR_SHAPE, "%s: c_in must be a multiple of 16", fn);
   if (ld_x < c_in) return fail(LH_ERR_SHAPE, "%s: ld_x < c_in", fn);
-  if (!values && !packed_e2m1 && !scale_e4m3 && !global_scale)
+  const bool blocks = n_groups > 0 && rows > 0 && c_in > 0;  // else the outputs per value or block have no elements
+  if (blocks && !values && !packed_e2m1 && !scale_e4m3 && !global_scale)
     return fail(LH_ERR_ARG, "%s: no output requested", fn);
   if (n_groups > 0 && amax == nullptr) return fail(LH_ERR_NULL, "%s: amax is NULL", fn);
-  if (n_groups > 0 && rows > 0 && c_in > 0 && x == nullptr) return fail(LH_ERR_NULL, "%s: x is NULL", fn);
+  if (blocks && x == nullptr) return fail(LH_ERR_NULL, "%s: x is NULL", fn);
   if (!aligned(x, elem_size(x_dtype)) || !aligned(amax, 4) || !aligned(global_scale, 4) || !aligned(values, 16) ||
       !aligned(packed_e2m1, 8))
     return fail(LH_ERR_ARG, "%s: misaligned pointer (values needs 16 bytes, packed_e2m1 8)", fn);
-  if (n_groups == 0) return LH_OK;
+  if (n_groups == 0 || (!blocks && global_scale == nullptr)) return LH_OK;
   lh::QuantizeArgs a{x, x_dtype, rows, c_in, ld_x, n_groups, group_stride_x, amax, values, v_dtype, packed_e2m1,
                      scale_e4m3, global_scale};
   hipError_t e = lh::launch_quantize(a, static_cast<hipStream_t>(stream));
@@ -758,11 +759,13 @@ lh_status lh_moe_combine_grad(const void* dy, int dtype, int64_t n_tokens, int64
                               const float* weights, void* dys, int64_t ld_dys, float* dweights, void* stream) {
   const char* fn = "lh_moe_combine_grad";
   g_msg[0] = '\0';
-  if (dys == nullptr && dweights == nullptr) return fail(LH_ERR_ARG, "%s: no output requested", fn);
+  // outputs without elements may be NULL
+  if (dys == nullptr && dweights == nullptr && n_tokens > 0 && top_k > 0 && cols > 0)
+    return fail(LH_ERR_ARG, "%s: no output requested", fn);
   lh::MoeRowsArgs a{dtype, dy, ld_dy, ys, ld_ys, n_rows, n_tokens, cols, top_k, position, weights, dys, ld_dys,
                     dweights};
   lh_status st = LH_OK;
-  if (dys) st = check_moe_rows(fn, a, dy, ld_dy, dys, ld_dys);
+  if (dys || !dweights) st = check_moe_rows(fn, a, dy, ld_dy, dys, ld_dys);
   if (st == LH_OK && dweights) st = check_moe_rows(fn, a, dy, ld_dy, ys, ld_ys);
   if (st != LH_OK) return st;
   if (!aligned(dweights, 4)) return fail(LH_ERR_ARG, "%s: pointer not aligned to its element size", fn);

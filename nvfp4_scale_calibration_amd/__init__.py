@@ -176,9 +176,10 @@ def _group_stride(t3: torch.Tensor) -> int:
 
 
 def _ld(t3: torch.Tensor) -> int:
-    """Row stride; a dimension of size 1 has no meaningful stride (torch may
-    report 1), so the contiguous extent is passed instead."""
-    return t3.stride(1) if t3.shape[1] > 1 else t3.shape[2]
+    """Row stride; a dimension of size 1, or any of a tensor without elements,
+    has no meaningful stride (torch may report 1 or 0), so the contiguous
+    extent is passed instead."""
+    return t3.stride(1) if t3.shape[1] > 1 and t3.numel() > 0 else t3.shape[2]
 
 
 def lh_abi_version() -> int:
@@ -641,8 +642,14 @@ def lh_gptq_quantize(w: torch.Tensor, best_idx: torch.Tensor, amax: torch.Tensor
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor (a single row has no meaningful one)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    """Row stride of a 2-D tensor (a single row, or none, has no meaningful one)."""
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+
+
+def _whole_rows(t: torch.Tensor) -> bool:
+    """Whether a row's elements follow one another (in a single column, or
+    without elements, they do whatever the stride)."""
+    return t.stride(-1) == 1 or t.shape[-1] == 1 or t.numel() == 0
 
 
 def _dense(t: torch.Tensor | None, name: str, dtype, shape=None) -> None:
@@ -688,7 +695,7 @@ def lh_quantize_nvfp4(x: torch.Tensor, amax: torch.Tensor, values: bool | torch.
     lh_fake_quant_nvfp4."""
     _on_device(x, amax)
     x3 = _as3(x)
-    if x3.shape[-1] > 0 and x3.stride(-1) != 1:
+    if not _whole_rows(x3):
         raise ValueError("last dim of x must be contiguous")
     g, rows, c_in = x3.shape
     _dense(amax, "amax", torch.float32, (g,))
@@ -737,7 +744,7 @@ def _linear(x, offsets, packed, scale_e4m3, global_scale, x_scale, y, out_dtype,
     rows = x3.shape[1]
     if x3.shape[2] != k:
         raise ValueError("the input has %d columns, the weights need %d" % (x3.shape[2], k))
-    if x3.shape[2] > 0 and x3.stride(-1) != 1:
+    if not _whole_rows(x3):
         raise ValueError("last dim of the input must be contiguous")
     if offsets is None:
         if x3.shape[0] != g:
@@ -749,7 +756,7 @@ def _linear(x, offsets, packed, scale_e4m3, global_scale, x_scale, y, out_dtype,
     shape = tuple(x.shape[:-1]) + (m,)
     if y is None:
         y = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
-    elif tuple(y.shape) != shape or (m > 0 and y.stride(-1) != 1):
+    elif tuple(y.shape) != shape or not _whole_rows(y):
         raise ValueError("the output must have shape %s and a contiguous last dim" % (shape,))
     y3 = _as3(y)
     ws, ws_bytes = None, 0
@@ -850,7 +857,7 @@ def lh_moe_sort(expert_ids: torch.Tensor, n_groups: int, order: bool = True,
 
 
 def _rows2(t: torch.Tensor, name: str, cols: int | None = None, like: torch.Tensor | None = None) -> torch.Tensor:
-    if t.dim() != 2 or (t.shape[1] > 0 and t.stride(1) != 1):
+    if t.dim() != 2 or not _whole_rows(t):
         raise ValueError("%s must be 2-D with contiguous rows" % name)
     if cols is not None and t.shape[1] != cols:
         raise ValueError("%s has %d columns, expected %d" % (name, t.shape[1], cols))

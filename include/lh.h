@@ -688,7 +688,8 @@ lh_status lh_moe_sort(const void *expert_ids, int ids_type, int64_t n_tokens, in
  * gradient is lh_moe_combine without weights.
  *   x  [n_tokens][ld_x], xs [n_rows][ld_xs], both dtype (fp32 or bf16) with
  *   `cols` columns (any number), n_rows >= n_tokens * top_k; entries of
- *   position beyond n_rows are ignored.
+ *   position beyond n_rows are ignored, rows that no entry names (past
+ *   n_tokens * top_k, with the positions of lh_moe_sort) are not written.
  * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_ARG, LH_ERR_HIP.
  */
 lh_status lh_moe_dispatch(const void *x, int dtype, int64_t n_tokens, int64_t cols, int64_t ld_x,
@@ -708,7 +709,9 @@ lh_status lh_moe_combine(const void *ys, int dtype, int64_t n_rows, int64_t cols
 /*
  * The gradients of lh_moe_combine:
  *   dys[position[t][k]] = weights[t][k] * dy[t]   (zero rows for assignments
- *                         without an expert), dtype, [n_rows][ld_dys]
+ *                         without an expert), dtype, [n_rows][ld_dys]; rows
+ *                         that no entry names are not written (their
+ *                         gradient is zero)
  *   dweights[t][k]      = <dy[t], ys[position[t][k]]> (0 without an expert),
  *                         fp32 [n_tokens][top_k]
  * Either may be NULL, not both (where they have any elements); weights NULL:

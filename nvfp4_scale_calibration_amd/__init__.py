@@ -868,7 +868,8 @@ def _rows2(t: torch.Tensor, name: str, cols: int | None = None, like: torch.Tens
 
 def lh_moe_dispatch(x: torch.Tensor, position: torch.Tensor, xs: torch.Tensor | None = None) -> torch.Tensor:
     """Tokens' rows to their experts: xs[position[t, k]] = x[t], zero rows for
-    dropped assignments; xs [n_tokens * top_k, cols] unless given."""
+    dropped assignments; xs [n_tokens * top_k, cols] unless given.  Rows that
+    position does not name are not written."""
     _on_device(x, position, xs)
     _rows2(x, "x")
     t, cols = x.shape
@@ -911,7 +912,10 @@ def lh_moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, position: torch.Tens
                         dweights: torch.Tensor | bool = True):
     """Gradients of lh_moe_combine: (dys, dweights) with dys[position[t, k]] =
     weights[t, k] dy[t] (zero rows for dropped assignments) and dweights[t, k]
-    = <dy[t], ys[position[t, k]]>; None where not requested (False)."""
+    = <dy[t], ys[position[t, k]]>; None where not requested (False).  Rows of
+    ys beyond the assignments have no gradient: zero, or in a dys of the
+    caller's left as they are.  (As many rows as assignments: position names
+    each once, as lh_moe_sort leaves it.)"""
     _on_device(dy, ys, position, weights)
     _rows2(dy, "dy")
     t, cols = dy.shape
@@ -921,8 +925,9 @@ def lh_moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, position: torch.Tens
         raise ValueError("position must be [n_tokens, top_k]")
     k = position.shape[1]
     _dense(weights, "weights", torch.float32, (t, k))
-    if dys is True:
-        dys = torch.empty(ys.shape, dtype=ys.dtype, device=ys.device)
+    if dys is True:  # the kernel writes the rows that position names
+        new = torch.empty if ys.shape[0] == t * k else torch.zeros
+        dys = new(ys.shape, dtype=ys.dtype, device=ys.device)
     elif dys is False:
         dys = None
     if dys is not None:

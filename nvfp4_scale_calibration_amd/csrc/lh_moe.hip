@@ -260,7 +260,7 @@ __device__ __forceinline__ int64_t row_of(int entry, int64_t n_rows) {
 // weights, row addresses) then comes through the scalar cache.
 __device__ __forceinline__ int64_t wave_unit() {
   const uint32_t w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  return (int64_t)blockIdx.x * (kThreads / 64) + w;
+  return block_id() * (kThreads / 64) + w;
 }
 
 // Assignments of a token that are looked up and moved together: their loads
@@ -339,12 +339,13 @@ __global__ __launch_bounds__(kThreads) void moe_combine_kernel(const T* __restri
 // (the lanes exchange halves of the values), then over the waves in order.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void moe_combine_grad_kernel(
-    const T* __restrict__ dy, int64_t ld_dy, const T* __restrict__ ys, int64_t ld_ys, int64_t n_rows, int64_t cols,
-    int top_k, const int* __restrict__ position, const float* __restrict__ weights, T* __restrict__ dys,
+    const T* __restrict__ dy, int64_t ld_dy, int64_t n_tok, const T* __restrict__ ys, int64_t ld_ys, int64_t n_rows,
+    int64_t cols, int top_k, const int* __restrict__ position, const float* __restrict__ weights, T* __restrict__ dys,
     int64_t ld_dys, float* __restrict__ dw) {
   constexpr int kN = Vec<T>::kN;
   __shared__ float part[kThreads / 64][kAtOnce];
-  const int64_t t = blockIdx.x;
+  const int64_t t = block_id();
+  if (t >= n_tok) return;  // the whole workgroup
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   for (int k0 = 0; k0 < top_k; k0 += kAtOnce) {
     int64_t row[kAtOnce];  // the same for the whole workgroup
@@ -430,17 +431,17 @@ hipError_t launch_sort_typed(const MoeSortArgs& a, hipStream_t stream) {
 }
 
 template <typename T>
-unsigned row_grid(int64_t n_tok, int64_t cols, int64_t& spans) {
+dim3 row_grid(int64_t n_tok, int64_t cols, int64_t& spans) {
   const int64_t per = 64 * (16 / (int64_t)sizeof(T));
   spans = (cols + per - 1) / per;
-  return (unsigned)((n_tok * spans + kThreads / 64 - 1) / (kThreads / 64));
+  return grid_of((n_tok * spans + kThreads / 64 - 1) / (kThreads / 64));
 }
 
 template <typename T>
 hipError_t launch_dispatch_typed(const MoeRowsArgs& a, hipStream_t stream) {
   int64_t spans;
-  const unsigned grid = row_grid<T>(a.n_tok, a.cols, spans);
-  moe_dispatch_kernel<T><<<dim3(grid), dim3(kThreads), 0, stream>>>(
+  const dim3 grid = row_grid<T>(a.n_tok, a.cols, spans);
+  moe_dispatch_kernel<T><<<grid, dim3(kThreads), 0, stream>>>(
       static_cast<const T*>(a.tok), a.ld_tok, a.n_tok, a.cols, (int)a.top_k, spans, a.position,
       static_cast<T*>(a.rows_out), a.ld_out, a.n_rows);
   return hipGetLastError();
@@ -449,8 +450,8 @@ hipError_t launch_dispatch_typed(const MoeRowsArgs& a, hipStream_t stream) {
 template <typename T>
 hipError_t launch_combine_typed(const MoeRowsArgs& a, hipStream_t stream) {
   int64_t spans;
-  const unsigned grid = row_grid<T>(a.n_tok, a.cols, spans);
-  moe_combine_kernel<T><<<dim3(grid), dim3(kThreads), 0, stream>>>(
+  const dim3 grid = row_grid<T>(a.n_tok, a.cols, spans);
+  moe_combine_kernel<T><<<grid, dim3(kThreads), 0, stream>>>(
       static_cast<const T*>(a.rows), a.ld_rows, a.n_rows, a.n_tok, a.cols, (int)a.top_k, spans, a.position, a.weights,
       static_cast<T*>(a.rows_out), a.ld_out);
   return hipGetLastError();
@@ -458,8 +459,8 @@ hipError_t launch_combine_typed(const MoeRowsArgs& a, hipStream_t stream) {
 
 template <typename T>
 hipError_t launch_combine_grad_typed(const MoeRowsArgs& a, hipStream_t stream) {
-  moe_combine_grad_kernel<T><<<dim3((unsigned)a.n_tok), dim3(kThreads), 0, stream>>>(
-      static_cast<const T*>(a.tok), a.ld_tok, static_cast<const T*>(a.rows), a.ld_rows, a.n_rows, a.cols,
+  moe_combine_grad_kernel<T><<<grid_of(a.n_tok), dim3(kThreads), 0, stream>>>(
+      static_cast<const T*>(a.tok), a.ld_tok, a.n_tok, static_cast<const T*>(a.rows), a.ld_rows, a.n_rows, a.cols,
       (int)a.top_k, a.position, a.weights, static_cast<T*>(a.rows_out), a.ld_out, a.dweights);
   return hipGetLastError();
 }

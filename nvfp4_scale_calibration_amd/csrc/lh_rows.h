@@ -25,6 +25,16 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl(f, std::make_integer_sequence<int, N>{});
 }
 
+// A grid of `blocks` > 0 workgroups, numbered by block_id().  A launch takes fewer
+// than 2^32 threads along a dimension (what is more wraps around, without an
+// error), so workgroups past 2^20 go on along y.  The last ones may lie past
+// `blocks`.
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t x = blocks < (1 << 20) ? blocks : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ int64_t block_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // A wave-uniform value into scalar registers.
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);

@@ -57,3 +57,36 @@ def test_rows_without_columns(lh):
     assert dys.shape == (4, 0) and dw.tolist() == [[0, 0], [0, 0]]
     assert lh.lh_moe_dispatch(torch.empty((2, 0), device=DEV), position).shape == (4, 0)
     assert lh.lh_moe_combine(torch.empty((4, 0), device=DEV), position).shape == (2, 0)
+
+
+def some(gen, rows, cols):
+    return torch.randint(-8, 9, (rows, cols), generator=gen, device=DEV, dtype=torch.int8).to(BF16)
+
+
+def test_gradients_of_many_tokens(lh):
+    """One workgroup per token: 2^24 of them are 2^32 threads."""
+    t, c = (1 << 24) + 3, 8
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    position = torch.randperm(t, generator=gen, device=DEV).to(torch.int32).view(t, 1)
+    dy, ys = some(gen, t, c), some(gen, t, c)
+    w = torch.exp2(torch.randint(-3, 3, (t, 1), generator=gen, device=DEV).float())
+    dys, dw = lh.lh_moe_combine_grad(dy, ys, position, w)
+    at = position.view(-1).long()
+    assert torch.equal(dys[at], (w * dy.float()).to(BF16))
+    assert torch.equal(dw.view(-1), (dy.float() * ys[at].float()).sum(-1))
+
+
+def test_rows_of_many_tokens(lh):
+    """One wave per token: 2^26 of them are 2^32 threads.  (torch's own indexing
+    of that many rows returns the first few alone: slices here.)"""
+    t, c = (1 << 26) + 3, 8
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    position = torch.randperm(t, generator=gen, device=DEV).to(torch.int32).view(t, 1)
+    x = some(gen, t, c)
+    xs = lh.lh_moe_dispatch(x, position)
+    for i in range(0, t, 1 << 22):
+        at = position[i:i + (1 << 22), 0]
+        assert torch.equal(xs.index_select(0, at), x[i:i + (1 << 22)]), "rows from token %d on" % i
+    y = lh.lh_moe_combine(xs, position)
+    for i in range(0, t, 1 << 22):
+        assert torch.equal(y[i:i + (1 << 22)], x[i:i + (1 << 22)]), "tokens from %d on" % i

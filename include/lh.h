@@ -599,7 +599,9 @@ size_t lh_linear_nvfp4_workspace_bytes(int grad, int ragged, int x_dtype, int64_
  *   workspace    NULL/0, or at least lh_linear_nvfp4_workspace_bytes(0, 0,
  *                x_dtype, n_tokens, c_in, c_out, n_groups, 0) bytes, 256-byte
  *                aligned.
- * c_in % 16 == 0, c_out any.  c_in = 0 writes zeros.
+ * c_in % 16 == 0, c_out any.  c_in = 0 writes zeros.  A call of more than
+ * 2^23 tiles of outputs (8 outputs of a token at least, 256 x 256 at most) may
+ * be too large for one launch and is then refused (LH_ERR_SHAPE).
  * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_WORKSPACE,
  * LH_ERR_ARG, LH_ERR_HIP.
  */

@@ -627,6 +627,8 @@ lh_status run_linear(const char* fn, lh::LinearArgs& a, int64_t x_len, int64_t y
     return fail(LH_ERR_WORKSPACE, "%s: workspace smaller than lh_linear_nvfp4_workspace_bytes()", fn);
   if (!work) return LH_OK;
   hipError_t e = lh::launch_linear(a, static_cast<hipStream_t>(stream));
+  if (e == hipErrorInvalidConfiguration)
+    return fail(LH_ERR_SHAPE, "%s: more tiles of outputs than one launch takes", fn);
   return e == hipSuccess ? LH_OK : hip_fail(e, fn);
 }
 

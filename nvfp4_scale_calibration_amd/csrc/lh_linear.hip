@@ -1280,7 +1280,7 @@ __global__ __launch_bounds__(kThreads) void split_sum_kernel(const float* __rest
                                                              int64_t n_groups, int64_t cols, TY* __restrict__ y,
                                                              int64_t ld_y, int64_t gstride_y) {
   const int64_t vecs = (cols + 3) / 4;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = block_id() * kThreads + threadIdx.x;
   const int64_t r = i / vecs, c = 4 * (i - r * vecs);
   if (r >= rows * n_groups) return;
   const int64_t n = cols - c, step = n_groups * rows * cols;
@@ -1311,7 +1311,7 @@ __global__ __launch_bounds__(kThreads) void pack_rows_kernel(const TX* __restric
                                                              int64_t ld, int64_t n_groups, int64_t gstride, int64_t kp,
                                                              uint16_t* __restrict__ out) {
   constexpr int kPlanes = sizeof(TX) == 4 ? 3 : 1;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t i = block_id() * kThreads + threadIdx.x;
   const int64_t vecs = kp / 8, r = i / vecs, c = 8 * (i - r * vecs);
   if (r >= rows * n_groups) return;
   const int64_t g = r / rows;
@@ -1468,12 +1468,19 @@ int64_t token_tiles(const LinearArgs& a, int64_t bt) {
   return a.rows / bt + (a.n_groups < a.rows ? a.n_groups : a.rows);
 }
 
+// Whether that many workgroups fit one launch, which takes fewer than 2^32
+// threads along x (more would wrap around, without an error).
+bool one_launch(int64_t m_tiles, int64_t t_tiles, int threads) {
+  return (double)m_tiles * (double)t_tiles * threads < 0x1p32;
+}
+
 template <bool kGrad, typename TX, typename TY>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t stream) {
   const int64_t m = kGrad ? a.c_in : a.c_out;
   const int64_t m_tiles = (m + kT - 1) / kT;
-  linear_tile_kernel<kGrad, TX, TY><<<dim3((unsigned)(m_tiles * token_tiles(a, kT))), dim3(kThreads), 0, stream>>>(
-      a, m_tiles);
+  const int64_t t_tiles = token_tiles(a, kT);
+  if (!one_launch(m_tiles, t_tiles, kThreads)) return hipErrorInvalidConfiguration;
+  linear_tile_kernel<kGrad, TX, TY><<<dim3((unsigned)(m_tiles * t_tiles)), dim3(kThreads), 0, stream>>>(a, m_tiles);
   return hipGetLastError();
 }
 
@@ -1597,8 +1604,10 @@ template <int kTok, int kRows, typename TX, typename TY>
 hipError_t launch_few_typed(const LinearArgs& a, hipStream_t stream) {
   const int64_t per = kRows * (kThreads / 64);
   const int64_t row_groups = (a.c_out + per - 1) / per;
-  linear_few_kernel<kTok, kRows, TX, TY><<<dim3((unsigned)(row_groups * token_tiles(a, kTok))), dim3(kThreads), 0,
-                                           stream>>>(a, row_groups);
+  const int64_t t_tiles = token_tiles(a, kTok);
+  if (!one_launch(row_groups, t_tiles, kThreads)) return hipErrorInvalidConfiguration;
+  linear_few_kernel<kTok, kRows, TX, TY><<<dim3((unsigned)(row_groups * t_tiles)), dim3(kThreads), 0, stream>>>(
+      a, row_groups);
   return hipGetLastError();
 }
 // Rows per wave: two for one bf16 token (5120 x 17408: 12.9 us, four rows
@@ -1678,40 +1687,41 @@ hipError_t pack_rows(const LinearArgs& a, const Plan& p, Rows& r, hipStream_t st
   const int64_t groups = a.ragged ? 1 : a.n_groups, k = a.grad ? a.c_out : a.c_in;
   uint16_t* out = static_cast<uint16_t*>(a.ws);
   r = Rows{out, planes * p.kp, a.rows * planes * p.kp};
-  const unsigned grid = (unsigned)((a.rows * groups * (p.kp / 8) + kThreads - 1) / kThreads);
+  const dim3 grid = grid_of((a.rows * groups * (p.kp / 8) + kThreads - 1) / kThreads);
   if (planes == 3)
-    pack_rows_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(static_cast<const float*>(a.x), a.rows, k,
-                                                                      a.ld_x, groups, a.gstride_x, p.kp, out);
+    pack_rows_kernel<float><<<grid, dim3(kThreads), 0, stream>>>(static_cast<const float*>(a.x), a.rows, k, a.ld_x,
+                                                                 groups, a.gstride_x, p.kp, out);
   else
-    pack_rows_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(static_cast<const uint16_t*>(a.x), a.rows, k,
-                                                                         a.ld_x, groups, a.gstride_x, p.kp, out);
+    pack_rows_kernel<uint16_t><<<grid, dim3(kThreads), 0, stream>>>(static_cast<const uint16_t*>(a.x), a.rows, k,
+                                                                    a.ld_x, groups, a.gstride_x, p.kp, out);
   return hipGetLastError();
 }
 
 hipError_t sum_splits(const LinearArgs& a, const Plan& p, const float* part, hipStream_t stream) {
   const int64_t groups = a.ragged ? 1 : a.n_groups, cols = a.grad ? a.c_in : a.c_out;
-  const unsigned grid = (unsigned)((a.rows * groups * ((cols + 3) / 4) + kThreads - 1) / kThreads);
+  const dim3 grid = grid_of((a.rows * groups * ((cols + 3) / 4) + kThreads - 1) / kThreads);
   if (a.y_dtype == 1)
-    split_sum_kernel<uint16_t><<<dim3(grid), dim3(kThreads), 0, stream>>>(part, p.splits, a.rows, groups, cols,
-                                                                         static_cast<uint16_t*>(a.y), a.ld_y, a.gstride_y);
+    split_sum_kernel<uint16_t><<<grid, dim3(kThreads), 0, stream>>>(
+        part, p.splits, a.rows, groups, cols, static_cast<uint16_t*>(a.y), a.ld_y, a.gstride_y);
   else
-    split_sum_kernel<float><<<dim3(grid), dim3(kThreads), 0, stream>>>(part, p.splits, a.rows, groups, cols,
-                                                                      static_cast<float*>(a.y), a.ld_y, a.gstride_y);
+    split_sum_kernel<float><<<grid, dim3(kThreads), 0, stream>>>(part, p.splits, a.rows, groups, cols,
+                                                                 static_cast<float*>(a.y), a.ld_y, a.gstride_y);
   return hipGetLastError();
 }
 
 hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
   const int planes = a.x_dtype == 1 ? 1 : 3;
+  const int64_t m_tiles = ((a.grad ? a.c_in : a.c_out) + p.outs - 1) / p.outs;
+  int64_t t_tiles = token_tiles(a, p.tok);
+  if (a.ragged) t_tiles = (t_tiles + 7) / 8 * 8;
+  if (!one_launch(m_tiles, t_tiles, 512)) return hipErrorInvalidConfiguration;  // 512: the most threads of any tile
   Rows r;
   hipError_t e = pack_rows(a, p, r, stream);
   if (e != hipSuccess) return e;
   float* const part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.pack_bytes);
-  int64_t t_tiles = token_tiles(a, p.tok);
-  if (a.ragged) t_tiles = (t_tiles + 7) / 8 * 8;
   if (a.grad) {
     const int w_stages = (int)(p.kp / kGradK);
-    const GradArgs b{a, r.x, r.ld, r.gstride, planes * w_stages, w_stages, (a.c_in + kGradM - 1) / kGradM, t_tiles,
-                     p.splits, part};
+    const GradArgs b{a, r.x, r.ld, r.gstride, planes * w_stages, w_stages, m_tiles, t_tiles, p.splits, part};
     switch (p.tok) {
       case 256: e = launch_grad_nt<4, 2, 1>(b, stream); break;
       case 128: e = launch_grad_nt<2, 1, 2>(b, stream); break;
@@ -1719,8 +1729,7 @@ hipError_t launch_big(const LinearArgs& a, const Plan& p, hipStream_t stream) {
     }
   } else {
     const int w_chunks = (int)(p.kp / kChunk);
-    const BigArgs b{a, r.x, r.ld, r.gstride, p.together ? w_chunks : planes * w_chunks, w_chunks,
-                    (a.c_out + p.outs - 1) / p.outs, t_tiles,
+    const BigArgs b{a, r.x, r.ld, r.gstride, p.together ? w_chunks : planes * w_chunks, w_chunks, m_tiles, t_tiles,
                     p.splits, part};
     switch (p.tok) {
       case 256: e = launch_big_nt<8, 2, 4, 1, 1>(b, stream); break;

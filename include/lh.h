@@ -553,7 +553,12 @@ lh_status lh_gptq_quantize(const void *w, int w_dtype, int64_t c_out, int64_t c_
  * bf16; c_in % 16 == 0), with the per-tensor amax of the calibration (or of
  * lh_absmax; tokens given as groups get a scale each).  Per 16 values:
  *   code = the E4M3 code of LH_RULE_MAX, r = Cast(x / s), s = fl32(c * S_g),
- * bit for bit as lh_select_scales(LH_RULE_MAX) and lh_fake_quant_nvfp4.
+ * bit for bit as lh_select_scales(LH_RULE_MAX) and lh_fake_quant_nvfp4,
+ * wherever the former finds a finite error (it gives other blocks code 1).
+ * An infinity takes the largest code and leaves as +-6 times it.  A NaN counts
+ * for nothing in its block's maximum and leaves as +-6 times the block's code:
+ * E2M1 has none.  With an infinite or NaN amax (lh_absmax of such values)
+ * global_scale is infinite or NaN too, and the other outputs mean nothing.
  *   values       v_dtype (fp32 or bf16) [n_groups][rows][c_in]: r * c, the
  *                quantised value in units of S_g, exact in either type (so
  *                Q = values * S_g; lh_linear_nvfp4 takes S_g as x_scale)

@@ -692,7 +692,8 @@ def lh_quantize_nvfp4(x: torch.Tensor, amax: torch.Tensor, values: bool | torch.
     from the calibration or lh_absmax.  Returns a dict with the requested
     outputs: values [g, rows, c_in] = r * c in units of S_g (exact; x's dtype
     unless values_dtype says otherwise), packed, scale_e4m3, global_scale as
-    lh_fake_quant_nvfp4."""
+    lh_fake_quant_nvfp4.  The format has no infinity and no NaN: they leave as
+    the block's largest value, and show in global_scale where amax is theirs."""
     _on_device(x, amax)
     x3 = _as3(x)
     if not _whole_rows(x3):

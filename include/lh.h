@@ -592,8 +592,11 @@ size_t lh_linear_nvfp4_workspace_bytes(int grad, int ragged, int x_dtype, int64_
  * packed_e2m1 [n_groups][c_out][c_in/2], low nibble = even column, and
  * scale_e4m3 [n_groups][c_out][c_in/16]; codes 0x01..0x7E).
  * r * c is exact in bf16 and bf16 activations enter as they are; fp32
- * activations as three bf16 values that add up to them exactly.  Products
- * are exact, sums fp32 on matrix cores; one rounding to y_dtype at the end.
+ * activations as three bf16 values that add up to them exactly (those below
+ * 2^-110 but for less than 2^-133).  Products are exact and sums fp32, on
+ * matrix cores; for up to two tokens (eight rows in all of a ragged call) the
+ * sums of a block's 16 exact products x * r are, which its code then
+ * multiplies, with one rounding per block.  One rounding to y_dtype at the end.
  * The order of a sum depends only on the arguments, never on the run.
  *   x            fp32 or bf16, [n_tokens][ld_x] per group, ld_x >= c_in.
  *   global_scale fp32 [n_groups] (S_g).  x_scale: fp32 [n_groups] or NULL

@@ -11,7 +11,8 @@
 // weights' side, and the global scale is one multiplication per output.
 // (The matrix cores' own block scales are powers of two per 32 elements and
 // cannot hold an E4M3 scale per 16.)  fp32 activations are cut into three
-// bf16 values that add up to them exactly, so their products are exact too.
+// bf16 values that add up to them exactly (from 2^-110 on; split3 says what
+// tinier ones lose), so their products are exact too.
 //
 // MFMA orientation: operand A = weights (rows = outputs), operand B =
 // activations (columns = tokens), so that a lane's accumulators are

@@ -116,7 +116,8 @@ __device__ __forceinline__ uint4 units8_bf16(uint32_t pk, float c) {
 
 // x = h + m + l with three bf16 values, exactly (24 significant bits cut into
 // 8 + 8 + 8; the remainders are exact differences, none for an infinity): bits
-// of two values packed per plane, a in the low half.
+// of two values packed per plane, a in the low half.  Where |x| < 2^-110 the
+// low bits reach below 2^-133, a subnormal bf16's last place, and are dropped.
 __device__ __forceinline__ void split3(float a, float b, uint32_t (&p)[3]) {
   const uint32_t ha = __float_as_uint(a) & 0xffff0000u, hb = __float_as_uint(b) & 0xffff0000u;
   const float ra = isinf(a) ? 0.0f : a - __uint_as_float(ha), rb = isinf(b) ? 0.0f : b - __uint_as_float(hb);

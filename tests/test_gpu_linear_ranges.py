@@ -22,6 +22,34 @@ def lh():
     return m
 
 
+@pytest.mark.parametrize("t,c_out,c_in", [(1, 300, 512), (2, 300, 512), (8, 512, 512), (40, 512, 512), (200, 512, 512),
+                                          (600, 512, 512), (2100, 512, 512)])
+@pytest.mark.parametrize("e", [-105, -112, -120, -127])
+def test_tiny_activations(lh, t, c_out, c_in, e):
+    """bf16 ones are exact down to the subnormal numbers.  Of fp32 ones below
+    2^-110 what lies under 2^-133, the last place of a subnormal bf16, can be
+    lost: less than 2^-133 |u| per product.  Besides, sums of n exact terms in
+    fp32: 8 sqrt(n) 2^-24 of the terms' magnitudes (the probabilistic bound),
+    two roundings for the scale, one for the output, and one half of the last
+    place of a subnormal sum (2^-150) per addition."""
+    rng = np.random.default_rng([67, t, e + 200])
+    packed, _, _ = weights(rng, 1, c_out, c_in)
+    codes = torch.from_numpy(rng.integers(0x60, 0x78, (1, c_out, c_in // 16), dtype=np.uint8))
+    u = torch.from_numpy(units64(packed, codes)[0]).to(DEV)
+    dev = [v.to(DEV) for v in (packed, codes, torch.full((1,), 2.0 ** 100))]
+    for dt in (BF16, F32):
+        for n, w, f in ((c_in, u, lh.lh_linear_nvfp4), (c_out, u.t().contiguous(), lh.lh_linear_nvfp4_grad)):
+            x = torch.from_numpy(rng.standard_normal((t, n)) * 2.0 ** e).to(dt).to(DEV)
+            ref, mass = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+            tol = (8 * n ** 0.5 * 2.0 ** -24 + 2.0 ** -22) * mass + 3 * n * 2.0 ** -150
+            if dt == F32:
+                tol = tol + 2.0 ** -133 * w.abs().sum(1)
+            for workspace in (True, None):
+                y = f(x, *dev, out_dtype=F32, workspace=workspace).double() / 2.0 ** 100
+                assert bool(((y - ref).abs() <= tol).all()), "%s: worst %.3g of its tolerance" % (
+                    dt, ((y - ref).abs() / tol).max().item())
+
+
 def test_rows_to_pack_beyond_one_grid_dimension(lh):
     """(2^23 + 16) rows of 4112 bf16 are packed by more than 2^32 threads."""
     t, c_out, c_in = (1 << 23) + 16, 16, 4112

@@ -22,6 +22,34 @@ def lh():
     return m
 
 
+# few, 16-, 32-, 64-, 128- and 256-token tiles, whole and ragged rows, parts and none
+SIZES = [(1, 40, 272), (2, 40, 272), (5, 64, 272), (32, 8192, 2064), (40, 1000, 512), (700, 512, 256), (1500, 512, 528),
+         (2100, 512, 1056), (4100, 1000, 272), (4100, 2048, 272)]
+
+
+@pytest.mark.parametrize("t,c_out,c_in", SIZES)
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("workspace", [True, None])
+def test_a_nan_reaches_every_output_of_its_token(lh, t, c_out, c_in, dt, workspace):
+    print("case t=%d %dx%d %s ws=%s" % (t, c_out, c_in, dt, workspace), flush=True)
+    rng = np.random.default_rng([61, t, c_in])
+    packed, codes, s = weights(rng, 1, c_out, c_in)
+    packed[0, 0, :] = 0                              # zero weights too: 0 x NaN is NaN
+    dev = [v.to(DEV) for v in (packed, codes, s)]
+    for n, f in ((c_in, lh.lh_linear_nvfp4), (c_out, lh.lh_linear_nvfp4_grad)):
+        for bits in (0x7fc00000, -0x400000, 0x7f810000 if dt == BF16 else 0x7f800001):   # quiet, negative, signalling
+            x = torch.from_numpy(rng.standard_normal((t, n)).astype(np.float32))
+            rows = sorted({0, t // 2, t - 1})
+            for r, col in zip(rows, (0, n - 1, n // 2)):
+                x[r, col] = torch.tensor(bits, dtype=torch.int32).view(torch.float32)
+            x = (x.view(torch.int32) >> 16).to(torch.int16).view(BF16) if dt == BF16 else x
+            assert torch.isnan(x).any(1).nonzero().flatten().tolist() == rows
+            y = f(x.to(DEV), *dev, out_dtype=F32, workspace=workspace).cpu()
+            hit = torch.zeros(t, dtype=torch.bool)
+            hit[rows] = True
+            assert bool(torch.isnan(y[hit]).all()) and bool(torch.isfinite(y[~hit]).all())
+
+
 @pytest.mark.parametrize("t,c_out,c_in", [(1, 300, 512), (2, 300, 512), (8, 512, 512), (40, 512, 512), (200, 512, 512),
                                           (600, 512, 512), (2100, 512, 512)])
 @pytest.mark.parametrize("e", [-105, -112, -120, -127])

@@ -64,7 +64,9 @@ def build(force: bool = True, verbose: bool = False, resource_usage: bool = Fals
     objs = [os.path.join(obj_dir, name) for name in OBJECTS]
     for name, parts in OBJECTS.items():
         if len(parts) > 1:
-            subprocess.run(["ld", "-r", "-o", os.path.join(obj_dir, name), *(made[src] for src in parts)], check=True)
+            # by the toolchain's own linker, as the library below
+            subprocess.run([HIPCC, "--offload-arch=gfx950", "-Wno-unused-command-line-argument", "-r", "-nostdlib",
+                            "-o", os.path.join(obj_dir, name), *(made[src] for src in parts)], check=True)
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)

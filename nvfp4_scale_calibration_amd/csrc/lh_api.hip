@@ -550,6 +550,12 @@ lh_status lh_gptq_quantize(const void* w, int w_dtype, int64_t c_out, int64_t c_
 // ---------------------------------------------------------------------------
 // Activation quantisation, products with packed weights, expert routing.
 // ---------------------------------------------------------------------------
+// Whether a buffer of that many elements lies beyond any memory; below it the
+// sums and products of sizes here and in the launches stay far from overflow.
+static bool beyond_memory(int64_t a, int64_t b, int64_t c = 1) {
+  return (double)a * (double)b * (double)c >= 0x1p60;
+}
+
 lh_status lh_quantize_nvfp4(const void* x, int x_dtype, int64_t rows, int64_t c_in, int64_t ld_x, int64_t n_groups,
                             int64_t group_stride_x, const float* amax, void* values, int v_dtype,
                             uint8_t* packed_e2m1, uint8_t* scale_e4m3, float* global_scale, void* stream) {
@@ -561,6 +567,8 @@ lh_status lh_quantize_nvfp4(const void* x, int x_dtype, int64_t rows, int64_t c_
     return fail(LH_ERR_SHAPE, "%s: negative size or stride", fn);
   if (c_in % 16 != 0) return fail(LH_ERR_SHAPE, "%s: c_in must be a multiple of 16", fn);
   if (ld_x < c_in) return fail(LH_ERR_SHAPE, "%s: ld_x < c_in", fn);
+  if (beyond_memory(n_groups, rows, ld_x) || beyond_memory(n_groups, group_stride_x))
+    return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
   const bool blocks = n_groups > 0 && rows > 0 && c_in > 0;  // else the outputs per value or block have no elements
   if (blocks && !values && !packed_e2m1 && !scale_e4m3 && !global_scale)
     return fail(LH_ERR_ARG, "%s: no output requested", fn);
@@ -579,7 +587,8 @@ lh_status lh_quantize_nvfp4(const void* x, int x_dtype, int64_t rows, int64_t c_
 size_t lh_linear_nvfp4_workspace_bytes(int grad, int ragged, int x_dtype, int64_t n_rows, int64_t c_in, int64_t c_out,
                                        int64_t n_groups, int64_t max_group_rows) {
   if (!valid_dtype(x_dtype) || n_rows <= 0 || c_in <= 0 || c_out <= 0 || n_groups <= 0 || c_in % 16 != 0 ||
-      max_group_rows < 0)
+      max_group_rows < 0 || beyond_memory(n_groups, c_out, c_in) ||
+      beyond_memory(ragged ? 1 : n_groups, n_rows, c_in + c_out))
     return 0;
   lh::LinearArgs a{};
   a.grad = grad != 0;
@@ -608,6 +617,10 @@ lh_status run_linear(const char* fn, lh::LinearArgs& a, int64_t x_len, int64_t y
     return fail(LH_ERR_SHAPE, "%s: negative size or stride", fn);
   if (a.c_in % 16 != 0) return fail(LH_ERR_SHAPE, "%s: c_in must be a multiple of 16", fn);
   if (a.ld_x < x_len || a.ld_y < y_len) return fail(LH_ERR_SHAPE, "%s: a leading dimension is smaller than its row", fn);
+  const int64_t batch = a.ragged ? 1 : a.n_groups;
+  if (beyond_memory(a.n_groups, a.c_out, a.c_in) || beyond_memory(batch, a.rows, a.ld_x) ||
+      beyond_memory(batch, a.rows, a.ld_y) || beyond_memory(batch, a.gstride_x) || beyond_memory(batch, a.gstride_y))
+    return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
   // groups of the output one after the other, or side by side in wide rows
   if (!a.ragged && a.n_groups > 1 && a.rows > 0 && a.gstride_y < (a.rows - 1) * a.ld_y + y_len &&
       (a.gstride_y < y_len || a.ld_y < (a.n_groups - 1) * a.gstride_y + y_len))
@@ -642,6 +655,8 @@ lh_status check_moe_rows(const char* fn, const lh::MoeRowsArgs& a, const void* t
     return fail(LH_ERR_SHAPE, "%s: n_tokens * top_k must be below 2^31", fn);
   if (a.n_rows < a.n_tok * a.top_k) return fail(LH_ERR_SHAPE, "%s: n_rows < n_tokens * top_k", fn);
   if (ld_tok < a.cols || ld_rows < a.cols) return fail(LH_ERR_SHAPE, "%s: a leading dimension < cols", fn);
+  if (beyond_memory(a.n_tok, ld_tok) || beyond_memory(a.n_tok * a.top_k, ld_rows))
+    return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
   const bool work = a.n_tok > 0 && a.cols > 0;
   if (work && (tok == nullptr || (a.top_k > 0 && (rows == nullptr || a.position == nullptr))))
     return fail(LH_ERR_NULL, "%s: the tokens' and the experts' rows and position are required", fn);

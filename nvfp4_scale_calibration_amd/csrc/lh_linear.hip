@@ -1548,9 +1548,11 @@ double tile_cost(const TileCost& k, double tiles, bool ragged, int64_t chunks, i
   return t;
 }
 
-// The cheapest kernel and number of parts (up to 16) for a.
+// The cheapest kernel and number of parts for a.  parts: whether there is a
+// place for partial sums (up to 16 parts then; 32 tokens on 4096 x 17408 weights
+// without one: 16 x 32 tiles 22.5 us, the 64 x 256 chosen with parts 125).
 template <int kN>
-void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int planes, int64_t plane_chunks) {
+void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int planes, int64_t plane_chunks, bool parts) {
   const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups, m = a.grad ? a.c_in : a.c_out;
   double best = 0.0;
   for (const TileCost& k : costs) {
@@ -1565,7 +1567,7 @@ void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int pla
       used = 0.5 * used + 0.5 * fmin(used, (double)a.rows / a.max_group_rows);
     const double t_tiles = a.ragged ? fmax(used, (double)a.rows / k.tok + 0.5 * used)
                                     : (double)((a.rows + k.tok - 1) / k.tok * a.n_groups);
-    for (int splits = 1; splits <= (a.ragged ? 1 : 16) && splits <= chunks; ++splits) {
+    for (int splits = 1; splits <= (parts && !a.ragged ? 16 : 1) && splits <= chunks; ++splits) {
       const double t = tile_cost(k, t_tiles * m_tiles, a.ragged, chunks, splits, (double)all * m);
       if (p.tok == 0 || t < best) {
         best = t;
@@ -1578,7 +1580,8 @@ void cheapest(Plan& p, const LinearArgs& a, const TileCost (&costs)[kN], int pla
   }
 }
 
-Plan plan_of(const LinearArgs& a) {
+// parts: whether the call has a workspace, as linear_ws_bytes has it for its answer.
+Plan plan_of(const LinearArgs& a, bool parts) {
   Plan p;
   if (a.rows <= 0 || a.c_in <= 0 || a.c_out <= 0) return p;
   // Up to two tokens, or eight ragged rows: linear_few_kernel (5120 x 17408
@@ -1594,8 +1597,8 @@ Plan plan_of(const LinearArgs& a) {
   const int64_t all = a.ragged ? a.rows : a.rows * a.n_groups;
   p.kp = (k + step - 1) / step * step;
   p.pack = planes == 3 || k % step != 0;
-  if (a.grad) cheapest(p, a, kGradCosts, planes, p.kp / step);
-  else cheapest(p, a, kProductCosts, planes, p.kp / step);
+  if (a.grad) cheapest(p, a, kGradCosts, planes, p.kp / step, parts);
+  else cheapest(p, a, kProductCosts, planes, p.kp / step, parts);
   if (p.pack) p.pack_bytes = ((size_t)all * planes * p.kp * 2 + 255) / 256 * 256;
   if (p.splits > 1) p.part_bytes = (size_t)p.splits * all * (a.grad ? a.c_in : a.c_out) * 4;
   return p;
@@ -1761,14 +1764,13 @@ bool direct_rows(const LinearArgs& a, const Plan& p) {
 }  // namespace
 
 size_t linear_ws_bytes(const LinearArgs& a) {
-  const Plan p = plan_of(a);
+  const Plan p = plan_of(a, true);
   return p.pack_bytes + p.part_bytes;
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t stream) {
-  Plan p = plan_of(a);
+  const Plan p = plan_of(a, a.ws != nullptr);
   if (p.few > 0) return launch_few(a, p.few, stream);
-  if (a.ws == nullptr) p.splits = 1;  // no place for partial sums
   if (p.tok > 0 && direct_rows(a, p)) return launch_big(a, p, stream);
   if (a.grad) return a.x_dtype == 1 ? launch_x<true, uint16_t>(a, stream) : launch_x<true, float>(a, stream);
   return a.x_dtype == 1 ? launch_x<false, uint16_t>(a, stream) : launch_x<false, float>(a, stream);

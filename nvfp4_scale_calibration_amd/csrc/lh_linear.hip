@@ -1507,15 +1507,19 @@ struct Plan {
 // Workgroups that share a CU share its issue slots, so a CU with r of them takes
 // `start` + r * (`each` + `more` per chunk or stage), one alone `one` per chunk;
 // a split adds a launch and its partial sums' way to memory and back.  The
-// constants are fitted to some 1000 timings of 42 products and 400 of 26
-// gradients (every kernel that comes near, up to 16 parts, 3 to 32768 tokens); the choice by
-// them is within 1.5% of the fastest on the mean.  Some of both sides (weights
-// of 4096 x 4096 unless named):
+// constants are fitted to timings of every kernel that comes near, up to 16
+// parts, 3 to 32768 tokens (all of them in profiles/product_tiles.md).  What
+// they pick is slower than the fastest by 0.8% on the mean of 44 products, 1.2%
+// of 19 gradients, 1.7% of 9 experts' products and 2.8% of as many gradients
+// (at worst 25%: 2048 rows on 64 experts).  The line of the planes side by side
+// is set by hand from a dozen calls.  Some of both sides (weights of 4096 x
+// 4096 unless named):
 //   product, 16 tokens: 16 x 32 tiles 8.1, 32 x 128 in 6 parts 11.8; 64 tokens on
 //     5120 x 17408: 64 x 128 in 6 parts 25.7, in 8 33.6, 64 x 256 in 10 27.0; 512
 //     tokens: 64 x 128 25.9, 64 x 256 in 2 parts 29.6; 1024 tokens: 64 x 256
 //     40.4, 64 x 128 45.7, 128 x 256 in 2 parts 48.0; 2048 tokens: 128 x 256
-//     69.4, 64 x 256 79.8; 4096 tokens: 256 x 256 115, 128 x 256 123
+//     69.4, 64 x 256 79.8; 4096 tokens: 256 x 256 115, 128 x 256 123; 8192 tokens
+//     on 12288 x 4096: 692, 715
 //   64 experts of 1024 x 2048, 512 rows: 32 x 128 21.8, 64 x 256 22.1, 64 x 128
 //     25.5; 8192 rows: 128 x 256 69, 64 x 256 73, 256 x 256 116; 32768 rows: 178,
 //     209, 191
@@ -1528,7 +1532,7 @@ struct TileCost {
   double start, each, one, more;
   bool together = false;  // fp32 rows: a chunk is that of all planes
 };
-constexpr TileCost kProductCosts[] = {{256, 256, 3.66, 0.22, 2.98, 3.45}, {128, 256, 2.36, 0.16, 1.88, 1.71},
+constexpr TileCost kProductCosts[] = {{256, 256, 3.66, 0.22, 2.98, 3.45}, {128, 256, 2.36, 0.16, 1.88, 1.75},
                                       {64, 256, 3.27, 0.17, 0.94, 1.06},  {64, 256, 4.0, 0.2, 2.2, 2.6, true},
                                       {64, 128, 3.43, 0.96, 0.60, 0.61},
                                       {32, kSmallM, 3.77, 1.58, 0.52, 0.53}, {16, kSkinnyM, 3.46, 0.43, 0.11, 0.16}};

@@ -598,7 +598,8 @@ size_t lh_linear_nvfp4_workspace_bytes(int grad, int ragged, int x_dtype, int64_
  * sums of a block's 16 exact products x * r are, which its code then
  * multiplies, with one rounding per block.  One rounding to y_dtype at the end.
  * The order of a sum depends only on the arguments, never on the run.
- *   x            fp32 or bf16, [n_tokens][ld_x] per group, ld_x >= c_in.
+ *   x            fp32 or bf16, [n_tokens][ld_x] per group, ld_x >= c_in.  bf16
+ *                rows that do not start 16-byte aligned take a slower kernel.
  *   global_scale fp32 [n_groups] (S_g).  x_scale: fp32 [n_groups] or NULL
  *                (1): the S_g of activations given as lh_quantize_nvfp4 values.
  *   y            fp32 or bf16, [n_tokens][ld_y] per group, ld_y >= c_out;

@@ -296,17 +296,17 @@ __global__ __launch_bounds__(kThreads) void linear_tile_kernel(LinearArgs a, int
 // chunk stands before its last step, whose operands are in registers by then,
 // so that step's MFMAs cover the first reads of the next chunk.
 //
-// Measured: 8192 tokens x (12288 x 4096) 682 us, 1.21 PFLOP/s (a library's
+// Measured: 8192 tokens x (12288 x 4096) 682 to 692 us, 1.2 PFLOP/s (a library's
 // bf16 product of that size 637 us); 32768 ragged rows on 64 experts of 1024 x
-// 2048 172 us, 0.80 PFLOP/s, of which the rows that fill up the experts' last
-// tiles are an eighth; 48 tokens x (12288 x 4096), 64 x 128 tiles in two parts,
-// 14.5 us and 3.8 for their sum.  Bound by the issue of vector instructions
+// 2048 174 us, 0.79 PFLOP/s, of which the rows that fill up the experts' last
+// tiles are an eighth; 48 tokens x (12288 x 4096), 64 x 256 tiles in four parts,
+// 15.9 us and 4.0 for their sum (traced).  Bound by the issue of vector instructions
 // between the MFMAs (decoding and LDS reads), the small tiles by the latency
 // of their few chunks, the fp32 one (kP = 3) by its LDS reads, which take as
 // long as its MFMAs: 333 x (4096 x 4096) fp32 48 us with packing and the sum of
 // two parts (planes one after the other: 128 x 256 in five parts 57), 1000 rows
 // 95 (114); four waves of 64 outputs, half the LDS reads, 53 and 100; 4096 rows
-// 370, here 256 x 256 with the planes in a row is better, 357.
+// 379, here 256 x 256 with the planes in a row is better, 358.
 // Eight waves of 32 outputs instead of four: 64
 // tokens x 256 outputs 40.4 us at 1024 x (4096 x 4096), where 64 x 128 takes
 // 45.7; with 256 tokens 683 against 689 us, with 128 820 against 712: not kept.
@@ -355,17 +355,21 @@ __device__ __forceinline__ void big_tile(int64_t b, bool ragged, int64_t m_tiles
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 // The same for 4 bytes, 2 bytes and 1 byte (zero-extended to 4) per lane: lane l at lds + 4 l.
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 __device__ __forceinline__ void dma2(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 __device__ __forceinline__ void dma1(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 #pragma clang diagnostic pop
 // A barrier that waits for this wave's LDS reads but for none of its loads
@@ -672,11 +676,12 @@ __global__ __launch_bounds__(64 * kMW, kWaves) void linear_big_kernel(BigArgs b)
 // instruction; codes one 32-bit word per lane, its two codes (kW4: one word
 // each).  kW4: rows that are not 16-byte aligned, in 4-byte pieces.
 //
-// Measured: 128 rows on 64 experts of 1024 x 2048 14.5 us (tiles of 64 tokens
-// by linear_big_kernel 15.1, of 16 by linear_skinny_kernel 19.2), 2048 rows 33
-// (37, 71).  Bound by latency: the 75 MB of weights that 60 experts hold would
-// take 14 us at a copy's rate where all are read.  More pairs of chunks in
-// flight gave nothing, nor did tiles of 64 tokens in this manner.
+// Measured: 128 rows on 64 experts of 1024 x 2048 14.5 to 16.7 us (tiles of 64
+// tokens by linear_big_kernel 15.1, of 16 by linear_skinny_kernel 19.2, where
+// this took 14.5), 18.1 where the weights are not in the last-level cache.  Bound
+// by latency: 26 to 36 experts have rows in these routings, whose 31 to 43 MB of
+// weights would take 6 to 9 us at a copy's rate.  More pairs of chunks in flight
+// gave nothing, nor did tiles of 64 tokens in this manner.
 // ---------------------------------------------------------------------------
 constexpr int kSmallM = 128;
 
@@ -857,7 +862,7 @@ __global__ __launch_bounds__(512, 2) void linear_small_kernel(BigArgs b) {
 // weights; one 32-bit word per lane and operand for its two codes (kW4: one
 // word each).  kW4: rows that are not 16-byte aligned, in 4-byte pieces.
 //
-// Measured: 16 tokens x (4096 x 4096) 8.0 us (launch, one chunk's latency and
+// Measured: 16 tokens x (4096 x 4096) 8.0 to 9.4 us (launch, one chunk's latency and
 // the join alone are 5), 8 tokens x (12288 x 4096) 13.1 us, 2.2 TB/s of weights;
 // linear_small_kernel 13.3 and 16.6.
 // ---------------------------------------------------------------------------
@@ -1037,8 +1042,8 @@ __global__ __launch_bounds__(64 * kW, 2) void linear_skinny_kernel(BigArgs b) {
 // vector operations; a weight is decoded by the two waves that share its
 // columns).
 //
-// Measured: 4096 tokens x (12288 x 4096) 381 us, 1.08 PFLOP/s; 32768 ragged
-// rows on 64 experts of 1024 x 2048 198 us, 0.69 PFLOP/s.  Bound by vector
+// Measured: 4096 tokens x (12288 x 4096) 389 to 396 us, 1.05 PFLOP/s; 32768
+// ragged rows on 64 experts of 1024 x 2048 209 us, 0.66 PFLOP/s.  Bound by vector
 // issue as the product, with the pairing of rows on top (72 operations for 4
 // kNT MFMAs, against 64 for as many there).
 // ---------------------------------------------------------------------------
@@ -1351,8 +1356,10 @@ __global__ __launch_bounds__(kThreads) void pack_rows_kernel(const TX* __restric
 // build an MFMA operand).  fp32 activations take fused multiply-adds instead.
 // The lanes' sums are added by xor shuffles at the end, in a fixed order.
 //
-// Measured: one token x (5120 x 17408) 12.8 us, 3.9 TB/s of weights and codes
-// (a copy of 2 GiB reaches 4.9); bound by that read and the launch.
+// Measured: one token x (5120 x 17408) 12.7 us, 3.9 TB/s of weights and codes, with
+// three such layers in turn, which the last-level cache holds; 14.8 us, 3.4
+// TB/s, with sixteen, which it does not (a copy of 2 GiB reaches 4.9).  Bound by
+// that read and the launch.
 // ---------------------------------------------------------------------------
 constexpr int kSpan = 2048;
 

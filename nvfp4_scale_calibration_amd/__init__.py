@@ -176,10 +176,9 @@ def _group_stride(t3: torch.Tensor) -> int:
 
 
 def _ld(t3: torch.Tensor) -> int:
-    """Row stride; a dimension of size 1, or any of a tensor without elements,
-    has no meaningful stride (torch may report 1 or 0), so the contiguous
-    extent is passed instead."""
-    return t3.stride(1) if t3.shape[1] > 1 and t3.numel() > 0 else t3.shape[2]
+    """Row stride; a dimension of size 1 has no meaningful stride (torch may
+    report 1), so the contiguous extent is passed instead."""
+    return t3.stride(1) if t3.shape[1] > 1 else t3.shape[2]
 
 
 def lh_abi_version() -> int:
@@ -642,8 +641,9 @@ def lh_gptq_quantize(w: torch.Tensor, best_idx: torch.Tensor, amax: torch.Tensor
 
 
 def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor (a single row, or none, has no meaningful one)."""
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+    """Row stride of a 2-D or 3-D tensor (a single row, or a tensor without
+    elements, has no meaningful one)."""
+    return t.stride(-2) if t.shape[-2] > 1 and t.numel() > 0 else t.shape[-1]
 
 
 def _whole_rows(t: torch.Tensor) -> bool:
@@ -715,7 +715,7 @@ def lh_quantize_nvfp4(x: torch.Tensor, amax: torch.Tensor, values: bool | torch.
                scale_e4m3=out(scale_e4m3, (g, rows, c_in // BLOCK), torch.uint8, "scale_e4m3"),
                global_scale=out(global_scale, (g,), torch.float32, "global_scale"))
     v = res["values"]
-    _check(lib.lh_quantize_nvfp4(_ptr(x3), _dtype(x3), rows, c_in, _ld(x3), g, _group_stride(x3), _ptr(amax),
+    _check(lib.lh_quantize_nvfp4(_ptr(x3), _dtype(x3), rows, c_in, _row_stride(x3), g, _group_stride(x3), _ptr(amax),
                                  _ptr(v), LH_DTYPE_F32 if v is None else _dtype(v), _ptr(res["packed"]),
                                  _ptr(res["scale_e4m3"]), _ptr(res["global_scale"]), _stream(x)))
     return {k: t for k, t in res.items() if t is not None}
@@ -768,9 +768,9 @@ def _linear(x, offsets, packed, scale_e4m3, global_scale, x_scale, y, out_dtype,
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=x.device)
     elif isinstance(workspace, torch.Tensor):
         ws, ws_bytes = _scratch(x, workspace)
-    xa = (_ptr(x3), _dtype(x3), rows, k, _ld(x3))
+    xa = (_ptr(x3), _dtype(x3), rows, k, _row_stride(x3))
     wa = (_ptr(p3), _ptr(s3), _ptr(global_scale), m)
-    ya = (_ptr(y3), _dtype(y3), _ld(y3))
+    ya = (_ptr(y3), _dtype(y3), _row_stride(y3))
     end = (_ptr(ws), ws_bytes, _stream(x))
     xs = () if grad else (_ptr(x_scale),)
     if offsets is None:

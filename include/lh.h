@@ -73,7 +73,8 @@ typedef enum lh_status {
 
 typedef enum lh_dtype {
     LH_DTYPE_F32 = 0,  /* IEEE binary32                                       */
-    LH_DTYPE_BF16 = 1  /* bfloat16 (upper half of binary32), RNE-rounded data */
+    LH_DTYPE_BF16 = 1, /* bfloat16 (upper half of binary32), RNE-rounded data */
+    LH_DTYPE_E4M3 = 2  /* OCP E4M3FN with a power of two per 32 values (only where said) */
 } lh_dtype;
 
 typedef enum lh_layout {
@@ -733,6 +734,148 @@ lh_status lh_moe_combine_grad(const void *dy, int dtype, int64_t n_tokens, int64
                               const void *ys, int64_t n_rows, int64_t ld_ys, const int32_t *position,
                               int64_t top_k, const float *weights, void *dys, int64_t ld_dys,
                               float *dweights, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Low-rank adapters beside the frozen projections, for many requests at once,
+ * their gradients, and the activations that a backward pass needs kept in 8
+ * bits.
+ *
+ * Rows that follow one another and belong together (a request's tokens, an
+ * expert's rows) form a segment; every segment takes one adapter or none.
+ * Both factors of adapter g are stored with the rank first, so that product
+ * and gradients read whole rows of them: a [n_adapters][rank][c_in], b
+ * [n_adapters][rank][c_out] (b is the transpose of a matrix that is applied
+ * from the left), dense, fp32 or bf16.  The calls share these arguments:
+ *   row_offsets  device int64 [n_segments + 1], 8-byte aligned: segment i has
+ *                the rows row_offsets[i] .. row_offsets[i+1]-1; expected
+ *                non-decreasing within [0, n_rows].  No offset can lead outside
+ *                a buffer; where segments overlap, the rows that they share get
+ *                the adapter of one of them.  NULL: every row is a segment of its own
+ *                (n_segments == n_rows), or all rows are one (n_segments == 1).
+ *   adapter_ids  ids_type (an lh_index) [n_segments], device; an id outside
+ *                [0, n_adapters) means no adapter.  NULL: segment i takes
+ *                adapter i (n_segments <= n_adapters; ids_type is ignored).
+ *   rank         0 .. 256, the same for all adapters (shorter ones end in
+ *                zeros).
+ *   scale        fp32 [n_adapters] (device), or NULL (1).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Scratch bytes that lh_lora (grad = 0) and lh_lora_grad (grad = 1) need, from
+ * the sizes alone.
+ */
+size_t lh_lora_workspace_bytes(int grad, int64_t n_rows, int64_t n_segments, int64_t c_in, int64_t c_out,
+                               int64_t rank);
+
+/*
+ * Low-rank adapters beside a projection: for every row t of a segment with
+ * adapter g
+ *   s[t][r] = sum_c x[t][c] a[g][r][c]
+ *   y[t][o] = base[t][o] + scale[g] * sum_r s[t][r] b[g][r][o]
+ * Rows of a segment without an adapter get y = base and s = 0; rows of no
+ * segment are not written.  Sums are fp32 in an order that depends on the
+ * sizes alone, products exact or rounded to fp32; where bf16 factors meet s on
+ * the matrix cores, s is cut into two bf16 values for a bf16 y (2^-16 of s is
+ * lost, 2^-8 below y's own rounding) and into three for an fp32 y (nothing).
+ * One rounding to y_dtype at the end.  Infinities and NaN follow the formula,
+ * in their own row only.
+ *   x      fp32 or bf16 [n_rows][ld_x], ld_x >= c_in.
+ *   base   y_dtype [n_rows][ld_base], ld_base >= c_out, or NULL (0).  It may be
+ *          y itself (with ld_base == ld_y): the projection's output is then
+ *          added to in place.  Otherwise no buffers may overlap.
+ *   y      fp32 or bf16 [n_rows][ld_y], ld_y >= c_out.
+ *   s      fp32 [n_rows][rank], dense, or NULL: what lh_lora_weight_grad needs.
+ *   workspace  at least lh_lora_workspace_bytes(0, ...) bytes, 256-byte
+ *          aligned (may be NULL where that is 0).
+ * Rows of any length and alignment of their type; 16-byte aligned ones are
+ * fastest.
+ * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_WORKSPACE,
+ * LH_ERR_ARG, LH_ERR_HIP.
+ */
+lh_status lh_lora(const void *x, int x_dtype, int64_t n_rows, int64_t c_in, int64_t ld_x,
+                  const int64_t *row_offsets, const void *adapter_ids, int ids_type, int64_t n_segments,
+                  const void *a, const void *b, int w_dtype, int64_t n_adapters, int64_t rank,
+                  const float *scale, const void *base, int64_t ld_base, int64_t c_out, void *y, int y_dtype,
+                  int64_t ld_y, float *s, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * lh_lora's gradient to its input, the same with the factors' roles exchanged:
+ *   ds[t][r] = sum_o dy[t][o] b[g][r][o]
+ *   dx[t][c] = base[t][c] + scale[g] * sum_r ds[t][r] a[g][r][c]
+ * base is usually the projection's own gradient (lh_linear_nvfp4_grad).
+ * Arguments, workspace (grad = 1) and errors as lh_lora, dy in the place of x
+ * and dx of y.
+ */
+lh_status lh_lora_grad(const void *dy, int dy_dtype, int64_t n_rows, int64_t c_out, int64_t ld_dy,
+                       const int64_t *row_offsets, const void *adapter_ids, int ids_type, int64_t n_segments,
+                       const void *a, const void *b, int w_dtype, int64_t n_adapters, int64_t rank,
+                       const float *scale, const void *base, int64_t ld_base, int64_t c_in, void *dx,
+                       int dx_dtype, int64_t ld_dx, float *ds, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* Scratch bytes that lh_lora_weight_grad needs, from the sizes alone. */
+size_t lh_lora_weight_grad_workspace_bytes(int64_t n_rows, int64_t n_segments, int64_t n_adapters, int64_t rank,
+                                           int64_t c_in, int64_t c_out);
+
+/*
+ * lh_lora's gradients to the adapters, from what lh_lora (s) and lh_lora_grad
+ * (ds) left:
+ *   da[g][r][c] = beta * da[g][r][c] + scale[g] * sum_t ds[t][r] x[t][c]
+ *   db[g][r][o] = beta * db[g][r][o] + scale[g] * sum_t s[t][r] dy[t][o]
+ * over the rows t of all segments with adapter g.  Either output may be NULL,
+ * not both (where they have any elements), and so may what only it needs.
+ * beta == 0 never reads the outputs; an adapter without rows gets beta times
+ * what it had.  fp32 sums in an order that depends on sizes and offsets alone.
+ * s, ds and x of rows without an adapter are not read.
+ *   x        x_dtype LH_DTYPE_F32, LH_DTYPE_BF16, or LH_DTYPE_E4M3 for a
+ *            checkpoint of lh_checkpoint_pack (dense: ld_x == c_in), whose
+ *            values enter as lh_checkpoint_unpack gives them in bf16.
+ *   x_scale  the checkpoint's scales, or NULL.
+ *   dy       fp32 or bf16 [n_rows][ld_dy].
+ *   s, ds    fp32 [n_rows][rank], dense.
+ *   da, db   out_dtype (fp32 or bf16), [n_adapters][rank][c_in] and
+ *            [n_adapters][rank][c_out], dense.
+ *   workspace  at least lh_lora_weight_grad_workspace_bytes() bytes, 256-byte
+ *            aligned (may be NULL where that is 0).
+ * n_adapters <= 1024.
+ * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_WORKSPACE,
+ * LH_ERR_ARG, LH_ERR_HIP.
+ */
+lh_status lh_lora_weight_grad(const void *x, int x_dtype, const uint8_t *x_scale, int64_t c_in, int64_t ld_x,
+                              const void *dy, int dy_dtype, int64_t c_out, int64_t ld_dy, const float *s,
+                              const float *ds, int64_t n_rows, const int64_t *row_offsets,
+                              const void *adapter_ids, int ids_type, int64_t n_segments, int64_t n_adapters,
+                              int64_t rank, const float *scale, float beta, void *da, void *db, int out_dtype,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Activations in 8 bits: every 32 values of a row (fewer at its end) share a
+ * power of two 2^e, the smallest with e >= -127 and no value beyond 448 2^e,
+ * and are rounded to E4M3 after the division by it (nearest, ties to even;
+ * the division is exact).
+ *   values  uint8 [n_rows][cols]: the OCP E4M3FN codes
+ *   scales  uint8 [n_rows][ceil(cols / 32)]: e + 127 (OCP E8M0)
+ * A value is off by at most 2^-4 of itself, or 2^-17 of its block's largest
+ * where that is more (e = -127 aside).  Infinities and NaN become NaN and count
+ * for nothing in their block's maximum.
+ *   x  fp32 or bf16 [n_rows][ld_x], ld_x >= cols, any alignment of its type.
+ * Outputs are dense.  Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE,
+ * LH_ERR_ARG, LH_ERR_HIP.
+ */
+lh_status lh_checkpoint_pack(const void *x, int x_dtype, int64_t n_rows, int64_t cols, int64_t ld_x,
+                             uint8_t *values, uint8_t *scales, void *stream);
+
+/*
+ * The activations back: x[t][c] = E4M3 value * 2^(scales - 127), exact in fp32
+ * and bf16 (in bf16 but for values below 2^-133, which are rounded; a block
+ * whose largest value was above 1.9375 * 2^127 may give infinities).  A scale
+ * byte of 255 is E8M0's NaN.  x fp32 or bf16 [n_rows][ld_x], ld_x >= cols, any
+ * alignment of its type.  Errors as lh_checkpoint_pack.
+ */
+lh_status lh_checkpoint_unpack(const uint8_t *values, const uint8_t *scales, int64_t n_rows, int64_t cols, void *x,
+                               int x_dtype, int64_t ld_x, void *stream);
 
 #ifdef __cplusplus
 }

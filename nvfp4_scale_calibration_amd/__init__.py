@@ -23,12 +23,13 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblh.so")
 
-LH_DTYPE_F32, LH_DTYPE_BF16 = 0, 1
+LH_DTYPE_F32, LH_DTYPE_BF16, LH_DTYPE_E4M3 = 0, 1, 2
 LH_LAYOUT_CHANNEL_MAJOR, LH_LAYOUT_TOKEN_MAJOR = 0, 1
 LH_INDEX_I32, LH_INDEX_I64 = 0, 1
 LH_RULE_SWEEP, LH_RULE_MAX, LH_RULE_FOUR_OVER_SIX, LH_RULE_AMAX_SEARCH = 0, 1, 2, 3
 N_CANDIDATES = 126
 BLOCK = 16
+CHECKPOINT_BLOCK = 32  # values that share a power of two in an 8-bit checkpoint
 
 
 class LHError(RuntimeError):
@@ -118,6 +119,20 @@ def _load() -> ctypes.CDLL:
     lib.lh_moe_combine.restype = I
     lib.lh_moe_combine_grad.argtypes = [P, I, I64, I64, I64, P, I64, I64, P, I64, P, P, I64, P, P]
     lib.lh_moe_combine_grad.restype = I
+    lib.lh_lora_workspace_bytes.argtypes = [I, I64, I64, I64, I64, I64]
+    lib.lh_lora_workspace_bytes.restype = SZ
+    for f in (lib.lh_lora, lib.lh_lora_grad):
+        f.argtypes = [P, I, I64, I64, I64, P, P, I, I64, P, P, I, I64, I64, P, P, I64, I64, P, I, I64, P, P, SZ, P]
+        f.restype = I
+    lib.lh_lora_weight_grad_workspace_bytes.argtypes = [I64, I64, I64, I64, I64, I64]
+    lib.lh_lora_weight_grad_workspace_bytes.restype = SZ
+    lib.lh_lora_weight_grad.argtypes = [P, I, P, I64, I64, P, I, I64, I64, P, P, I64, P, P, I, I64, I64, I64, P, F, P,
+                                        P, I, P, SZ, P]
+    lib.lh_lora_weight_grad.restype = I
+    lib.lh_checkpoint_pack.argtypes = [P, I, I64, I64, I64, P, P, P]
+    lib.lh_checkpoint_pack.restype = I
+    lib.lh_checkpoint_unpack.argtypes = [P, P, I64, I64, P, I, I64, P]
+    lib.lh_checkpoint_unpack.restype = I
     return lib
 
 
@@ -130,7 +145,9 @@ EXPORTS = ("lh_abi_version", "lh_status_string", "lh_last_error_message", "lh_ab
            "lh_output_error", "lh_scaled_histogram", "lh_gptq_workspace_bytes", "lh_gptq_prepare",
            "lh_gptq_quantize", "lh_quantize_nvfp4", "lh_linear_nvfp4_workspace_bytes", "lh_linear_nvfp4",
            "lh_linear_nvfp4_grad", "lh_linear_nvfp4_ragged", "lh_linear_nvfp4_ragged_grad",
-           "lh_moe_sort_workspace_bytes", "lh_moe_sort", "lh_moe_dispatch", "lh_moe_combine", "lh_moe_combine_grad")
+           "lh_moe_sort_workspace_bytes", "lh_moe_sort", "lh_moe_dispatch", "lh_moe_combine", "lh_moe_combine_grad",
+           "lh_lora_workspace_bytes", "lh_lora", "lh_lora_grad", "lh_lora_weight_grad_workspace_bytes",
+           "lh_lora_weight_grad", "lh_checkpoint_pack", "lh_checkpoint_unpack")
 
 
 def _check(status: int) -> None:
@@ -947,3 +964,221 @@ def lh_moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, position: torch.Tens
                                    _row_stride(ys), _ptr(position), k, _ptr(weights), _ptr(dys),
                                    0 if dys is None else _row_stride(dys), _ptr(dweights), _stream(dy)))
     return dys, dweights
+
+
+def _launch(first: torch.Tensor, f, *args) -> None:
+    """The call with first's device as the current one, on that device's current stream."""
+    d = first.get_device()
+    if d == torch.cuda.current_device():
+        _check(f(*args, _stream(first)))
+    else:
+        with torch.cuda.device(d):
+            _check(f(*args, _stream(first)))
+
+
+def _segments(first: torch.Tensor, n_rows: int, n_adapters: int, offsets, adapter_ids):
+    """The arguments that say which rows take which adapter: (offsets, ids, type of the ids, segments)."""
+    if offsets is not None:
+        _dense(offsets, "offsets", torch.int64)
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError("offsets must be [n_segments + 1]")
+        n = offsets.shape[0] - 1
+    else:
+        n = n_rows if adapter_ids is not None and adapter_ids.shape != (1,) else 1
+    kind = LH_INDEX_I32
+    if adapter_ids is not None:
+        if adapter_ids.dtype == torch.int64:
+            kind = LH_INDEX_I64
+        elif adapter_ids.dtype != torch.int32:
+            raise TypeError("adapter_ids must be int32 or int64, got %s" % adapter_ids.dtype)
+        _dense(adapter_ids, "adapter_ids", adapter_ids.dtype, (n,))
+    elif n > n_adapters:
+        raise ValueError("without adapter_ids the %d segments need an adapter each (there are %d)" % (n, n_adapters))
+    _on_device(first, offsets, adapter_ids)
+    return _ptr(offsets), _ptr(adapter_ids), kind, n
+
+
+def lh_lora_workspace_bytes(n_rows: int, n_segments: int, c_in: int, c_out: int, rank: int, grad: bool = False) -> int:
+    return int(lib.lh_lora_workspace_bytes(int(grad), n_rows, n_segments, c_in, c_out, rank))
+
+
+def _lora(x, a, b, scale, offsets, adapter_ids, base, y, s, out_dtype, workspace, grad):
+    """The product and its gradient: x [n_rows, .] into rows of the other factor's columns."""
+    _on_device(x, a, b, scale, base, y)
+    _rows2(x, "the input")
+    a3, b3 = _as3(a), _as3(b)
+    n, rank, c_in = a3.shape
+    c_out = b3.shape[2]
+    if b3.shape[:2] != a3.shape[:2]:
+        raise ValueError("a and b must agree in adapters and rank, got %s and %s" % (tuple(a.shape), tuple(b.shape)))
+    if b3.dtype != a3.dtype:
+        raise TypeError("a and b must have one type, got %s and %s" % (a.dtype, b.dtype))
+    _dense(a3, "a", a3.dtype)
+    _dense(b3, "b", b3.dtype)
+    _dense(scale, "scale", torch.float32, (n,))
+    k, m = (c_out, c_in) if grad else (c_in, c_out)
+    rows, cols = x.shape
+    if cols != k:
+        raise ValueError("the input has %d columns, the adapters need %d" % (cols, k))
+    if y is None:
+        y = torch.empty((rows, m), dtype=out_dtype or (x if base is None else base).dtype, device=x.device)
+    _rows2(y, "the output", m)
+    if base is not None:
+        _rows2(base, "base", m, y)
+    if y.shape[0] != rows or base is not None and base.shape[0] != rows:
+        raise ValueError("the output and base must have the input's %d rows" % rows)
+    off, ids, kind, segments = _segments(x, rows, n, offsets, adapter_ids)
+    if s is True:
+        s = torch.empty((rows, rank), dtype=torch.float32, device=x.device)
+    elif s is False:
+        s = None
+    if s is not None:
+        _on_device(x, s)
+        _dense(s, "s", torch.float32, (rows, rank))
+    if workspace is None:
+        nbytes = int(lib.lh_lora_workspace_bytes(int(grad), rows, segments, c_in, c_out, rank))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    else:
+        ws, nbytes = _scratch(x, workspace)
+    _launch(x, lib.lh_lora_grad if grad else lib.lh_lora, _ptr(x), _dtype(x), rows, k, _row_stride(x), off, ids, kind,
+            segments, _ptr(a3), _ptr(b3), _dtype(a3), n, rank, _ptr(scale), _ptr(base),
+            m if base is None else _row_stride(base), m, _ptr(y), _dtype(y), _row_stride(y), _ptr(s), _ptr(ws), nbytes)
+    return y if s is None else (y, s)
+
+
+def lh_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor | None = None,
+            offsets: torch.Tensor | None = None, adapter_ids: torch.Tensor | None = None,
+            base: torch.Tensor | None = None, y: torch.Tensor | None = None, s: torch.Tensor | bool = False,
+            out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None):
+    """y = base + scale[g] (x a[g]^T) b[g], row by row with the adapter g of the
+    row's segment.  x [n_rows, c_in]; a [n_adapters, rank, c_in] and b
+    [n_adapters, rank, c_out] (2-D: one adapter), rank-major both; scale fp32
+    [n_adapters].  offsets (device int64 [n_segments + 1]): segment i has the
+    rows offsets[i] .. offsets[i+1]-1; without them every row is a segment (or
+    all rows are one, with one adapter id or none).  adapter_ids (int32 or int64
+    [n_segments], device): each segment's adapter, an id outside the adapters
+    for none; without them segment i takes adapter i.  base [n_rows, c_out]:
+    the projection's output (y=base adds to it in place); rows of no segment
+    are not written.  y in base's dtype, else x's, unless out_dtype or y says
+    otherwise.  With s=True (or a fp32 [n_rows, rank] tensor) returns (y, s), s
+    = x a^T for lh_lora_weight_grad."""
+    return _lora(x, a, b, scale, offsets, adapter_ids, base, y, s, out_dtype, workspace, False)
+
+
+def lh_lora_grad(dy: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor | None = None,
+                 offsets: torch.Tensor | None = None, adapter_ids: torch.Tensor | None = None,
+                 base: torch.Tensor | None = None, dx: torch.Tensor | None = None, ds: torch.Tensor | bool = False,
+                 out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None):
+    """dx = base + scale[g] (dy b[g]^T) a[g], the gradient of lh_lora to its
+    input; base is the projection's own (lh_linear_nvfp4_grad).  With ds=True
+    (or a fp32 [n_rows, rank] tensor) returns (dx, ds), ds = dy b^T for
+    lh_lora_weight_grad.  Other arguments as lh_lora."""
+    return _lora(dy, a, b, scale, offsets, adapter_ids, base, dx, ds, out_dtype, workspace, True)
+
+
+def lh_lora_weight_grad_workspace_bytes(n_rows: int, n_segments: int, n_adapters: int, rank: int, c_in: int,
+                                        c_out: int) -> int:
+    return int(lib.lh_lora_weight_grad_workspace_bytes(n_rows, n_segments, n_adapters, rank, c_in, c_out))
+
+
+def lh_lora_weight_grad(x: torch.Tensor, dy: torch.Tensor, s: torch.Tensor | None, ds: torch.Tensor | None,
+                        n_adapters: int, scale: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                        adapter_ids: torch.Tensor | None = None, x_scale: torch.Tensor | None = None,
+                        da: torch.Tensor | bool = True, db: torch.Tensor | bool = True, beta: float = 0.0,
+                        out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None):
+    """Gradients of lh_lora to its adapters: (da, db) with da[g] = scale[g]
+    sum_t ds[t]^T x[t] [n_adapters, rank, c_in] and db[g] = scale[g] sum_t
+    s[t]^T dy[t] [n_adapters, rank, c_out] over the rows of the segments with
+    adapter g; None where not requested (False).  x as lh_lora had it, or the
+    values of lh_checkpoint_pack (uint8) with x_scale its scales; s and ds from
+    lh_lora and lh_lora_grad (None where only the other gradient is asked for).
+    beta: what is added of da's and db's earlier contents, for which both must
+    be given.  fp32 unless out_dtype, da or db says otherwise."""
+    _on_device(x, dy, s, ds, scale, x_scale)
+    p = ds if s is None else s
+    if p is None:
+        raise ValueError("s or ds is needed")
+    rows, rank = p.shape
+    _dense(s, "s", torch.float32, (rows, rank))
+    _dense(ds, "ds", torch.float32, (rows, rank))
+    _dense(scale, "scale", torch.float32, (n_adapters,))
+    if x.dim() != 2 or dy.dim() != 2 or x.shape[0] != rows or dy.shape[0] != rows:
+        raise ValueError("x and dy must be 2-D with the %d rows of s and ds" % rows)
+    _rows2(dy, "dy")
+    c_in, c_out = x.shape[1], dy.shape[1]
+    if x_scale is None:
+        _rows2(x, "x")
+        x_code, ld_x = _dtype(x), _row_stride(x)
+    else:
+        _dense(x, "the checkpoint's values", torch.uint8)
+        _dense(x_scale, "x_scale", torch.uint8, (rows, -(-c_in // CHECKPOINT_BLOCK)))
+        x_code, ld_x = LH_DTYPE_E4M3, c_in
+    if beta != 0.0 and not all(isinstance(t, torch.Tensor) or t is False for t in (da, db)):
+        raise ValueError("beta needs the earlier da and db")
+    given = [t.dtype for t in (da, db) if isinstance(t, torch.Tensor)]
+    dtype = given[0] if given else out_dtype or torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("the gradients must be float32 or bfloat16, got %s" % dtype)
+
+    def out(t, cols, name):
+        if t is True:
+            return torch.empty((n_adapters, rank, cols), dtype=dtype, device=x.device)
+        if t is False:
+            return None
+        _on_device(x, t)
+        _dense(t, name, dtype, (n_adapters, rank, cols))
+        return t
+
+    da, db = out(da, c_in, "da"), out(db, c_out, "db")
+    if da is not None and ds is None or db is not None and s is None:
+        raise ValueError("da needs ds and db needs s")
+    off, ids, kind, segments = _segments(x, rows, n_adapters, offsets, adapter_ids)
+    if workspace is None:
+        nbytes = int(lib.lh_lora_weight_grad_workspace_bytes(rows, segments, n_adapters, rank, c_in, c_out))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    else:
+        ws, nbytes = _scratch(x, workspace)
+    _launch(x, lib.lh_lora_weight_grad, _ptr(x), x_code, _ptr(x_scale), c_in, ld_x, _ptr(dy), _dtype(dy), c_out,
+            _row_stride(dy), _ptr(s), _ptr(ds), rows, off, ids, kind, segments, n_adapters, rank, _ptr(scale),
+            float(beta), _ptr(da), _ptr(db), LH_DTYPE_BF16 if dtype == torch.bfloat16 else LH_DTYPE_F32, _ptr(ws),
+            nbytes)
+    return da, db
+
+
+def lh_checkpoint_pack(x: torch.Tensor, values: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """Activations [n_rows, cols] in 8 bits: (values, scales), uint8 [n_rows,
+    cols] OCP E4M3FN codes and uint8 [n_rows, ceil(cols / 32)] E8M0 exponents of
+    the power of two that 32 values of a row share (the smallest with which none
+    exceeds 448).  Infinities and NaN become NaN."""
+    _on_device(x, values, scales)
+    _rows2(x, "x")
+    rows, cols = x.shape
+    blocks = -(-cols // CHECKPOINT_BLOCK)
+    if values is None:
+        values = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((rows, blocks), dtype=torch.uint8, device=x.device)
+    _dense(values, "values", torch.uint8, (rows, cols))
+    _dense(scales, "scales", torch.uint8, (rows, blocks))
+    _launch(x, lib.lh_checkpoint_pack, _ptr(x), _dtype(x), rows, cols, _row_stride(x), _ptr(values), _ptr(scales))
+    return values, scales
+
+
+def lh_checkpoint_unpack(values: torch.Tensor, scales: torch.Tensor, x: torch.Tensor | None = None,
+                         out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The activations of lh_checkpoint_pack back: value * 2^(scale - 127), in x (bf16 or
+    fp32 [n_rows, cols]) or a new tensor of out_dtype."""
+    _on_device(values, scales, x)
+    _dense(values, "values", torch.uint8)
+    if values.dim() != 2:
+        raise ValueError("values must be [n_rows, cols]")
+    rows, cols = values.shape
+    _dense(scales, "scales", torch.uint8, (rows, -(-cols // CHECKPOINT_BLOCK)))
+    if x is None:
+        x = torch.empty((rows, cols), dtype=out_dtype, device=values.device)
+    _rows2(x, "x", cols)
+    if x.shape[0] != rows:
+        raise ValueError("x must have the values' rows")
+    _launch(values, lib.lh_checkpoint_unpack, _ptr(values), _ptr(scales), rows, cols, _ptr(x), _dtype(x),
+            _row_stride(x))
+    return x

@@ -16,13 +16,13 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblh.so")
 # object -> its sources: lh_quant.o holds everything that reads or writes the
-# packed format or feeds such a kernel (one relocatable object from three
-# sources, so that the library links from the same five objects)
+# packed formats, feeds such a kernel or works beside it (one relocatable object
+# from several sources, so that the library links from the same five objects)
 OBJECTS = {
     "lh_api.o": ["lh_api.hip"],
     "lh_hessian.o": ["lh_hessian.hip"],
     "lh_sweep.o": ["lh_sweep.hip"],
-    "lh_quant.o": ["lh_quant.hip", "lh_linear.hip", "lh_moe.hip"],
+    "lh_quant.o": ["lh_quant.hip", "lh_linear.hip", "lh_moe.hip", "lh_lora.hip", "lh_checkpoint.hip"],
     "lh_dense.o": ["lh_dense.hip"],
 }
 SOURCES = [src for parts in OBJECTS.values() for src in parts]

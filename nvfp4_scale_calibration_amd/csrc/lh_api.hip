@@ -796,6 +796,192 @@ lh_status lh_moe_combine_grad(const void* dy, int dtype, int64_t n_tokens, int64
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
+// Low-rank adapters and 8-bit checkpoints.
+// ---------------------------------------------------------------------------
+namespace {
+
+// What the adapters' entry points share: the segments and the adapters' sizes.
+lh_status check_segments(const char* fn, int64_t n_rows, const lh::SegmentArgs& g, int ids_type, int64_t rank) {
+  if (g.ids != nullptr && ids_type != LH_INDEX_I32 && ids_type != LH_INDEX_I64)
+    return fail(LH_ERR_DTYPE, "%s: ids_type must be 0 (int32) or 1 (int64)", fn);
+  if (n_rows < 0 || g.n < 0 || g.n_adapters < 0 || rank < 0) return fail(LH_ERR_SHAPE, "%s: negative size", fn);
+  if (rank > lh::kLoraMaxRank) return fail(LH_ERR_SHAPE, "%s: rank must be at most 256", fn);
+  if (g.offsets == nullptr && g.n != 1 && g.n != n_rows)
+    return fail(LH_ERR_SHAPE, "%s: without row_offsets n_segments must be n_rows or 1", fn);
+  if (g.ids == nullptr && g.n > g.n_adapters)
+    return fail(LH_ERR_SHAPE, "%s: without adapter_ids there must be an adapter for every segment", fn);
+  if (beyond_memory(n_rows, lh::kLoraMaxRank) || beyond_memory(g.n, 1))
+    return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
+  if (!aligned(g.offsets, 8) || !aligned(g.ids, ids_type == LH_INDEX_I64 ? 8 : 4))
+    return fail(LH_ERR_ARG, "%s: row_offsets or adapter_ids not aligned to its element size", fn);
+  return LH_OK;
+}
+
+// The checks that the product and its gradient share.
+lh_status run_lora(const char* fn, lh::LoraArgs& a, int ids_type, void* stream) {
+  g_msg[0] = '\0';
+  if (!valid_dtype(a.x_dtype) || !valid_dtype(a.w_dtype) || !valid_dtype(a.y_dtype))
+    return fail(LH_ERR_DTYPE, "%s: the types of input, adapters and output must be 0 (f32) or 1 (bf16)", fn);
+  const lh_status st = check_segments(fn, a.rows, a.seg, ids_type, a.rank);
+  if (st != LH_OK) return st;
+  if (a.c_x < 0 || a.c_y < 0) return fail(LH_ERR_SHAPE, "%s: negative size", fn);
+  if (a.ld_x < a.c_x || a.ld_y < a.c_y || (a.base != nullptr && a.ld_base < a.c_y))
+    return fail(LH_ERR_SHAPE, "%s: a leading dimension is smaller than its row", fn);
+  if (beyond_memory(a.rows, a.ld_x) || beyond_memory(a.rows, a.ld_y) || beyond_memory(a.rows, a.ld_base) ||
+      beyond_memory(a.seg.n_adapters, lh::kLoraMaxRank, a.c_x) || beyond_memory(a.seg.n_adapters, lh::kLoraMaxRank, a.c_y))
+    return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
+  if (a.base != nullptr && a.base == a.y && a.ld_base != a.ld_y && a.rows > 1)
+    return fail(LH_ERR_SHAPE, "%s: base is the output itself, but with another leading dimension", fn);
+  const bool outputs = a.rows > 0 && (a.c_y > 0 || (a.s != nullptr && a.rank > 0));
+  const bool work = outputs && a.seg.n > 0;
+  const bool adds = work && a.rank > 0 && a.seg.n_adapters > 0;
+  if (work && a.c_y > 0 && a.y == nullptr) return fail(LH_ERR_NULL, "%s: the output is NULL", fn);
+  if (adds && a.c_x > 0 && (a.x == nullptr || a.in == nullptr))
+    return fail(LH_ERR_NULL, "%s: the input and the adapters are required", fn);
+  if (adds && a.c_y > 0 && a.out == nullptr) return fail(LH_ERR_NULL, "%s: the adapters are required", fn);
+  if (a.ws == nullptr && a.ws_bytes > 0) return fail(LH_ERR_NULL, "%s: workspace is NULL but workspace_bytes > 0", fn);
+  if (!aligned(a.x, elem_size(a.x_dtype)) || !aligned(a.in, elem_size(a.w_dtype)) ||
+      !aligned(a.out, elem_size(a.w_dtype)) || !aligned(a.base, elem_size(a.y_dtype)) ||
+      !aligned(a.y, elem_size(a.y_dtype)) || !aligned(a.scale, 4) || !aligned(a.s, 4) || !aligned(a.ws, 256))
+    return fail(LH_ERR_ARG, "%s: misaligned pointer (workspace needs 256 bytes)", fn);
+  if (work && a.ws_bytes < lh::lora_ws_bytes(a.rows, a.seg.n, a.c_x, a.c_y, a.rank))
+    return fail(LH_ERR_WORKSPACE, "%s: workspace smaller than lh_lora_workspace_bytes()", fn);
+  if (!work) return LH_OK;
+  const hipError_t e = lh::launch_lora(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lh_lora_workspace_bytes(int grad, int64_t n_rows, int64_t n_segments, int64_t c_in, int64_t c_out,
+                               int64_t rank) {
+  if (n_rows <= 0 || n_segments <= 0 || c_in < 0 || c_out < 0 || rank <= 0 || rank > lh::kLoraMaxRank ||
+      beyond_memory(n_rows, c_in) || beyond_memory(n_rows, c_out) || beyond_memory(n_rows, lh::kLoraMaxRank))
+    return 0;
+  return grad ? lh::lora_ws_bytes(n_rows, n_segments, c_out, c_in, rank)
+              : lh::lora_ws_bytes(n_rows, n_segments, c_in, c_out, rank);
+}
+
+lh_status lh_lora(const void* x, int x_dtype, int64_t n_rows, int64_t c_in, int64_t ld_x, const int64_t* row_offsets,
+                  const void* adapter_ids, int ids_type, int64_t n_segments, const void* a, const void* b, int w_dtype,
+                  int64_t n_adapters, int64_t rank, const float* scale, const void* base, int64_t ld_base,
+                  int64_t c_out, void* y, int y_dtype, int64_t ld_y, float* s, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  lh::LoraArgs l{x, x_dtype, n_rows, c_in, ld_x, {row_offsets, adapter_ids, ids_type == LH_INDEX_I64, n_segments, n_adapters},
+                 a, b, w_dtype, rank, scale, base, base ? ld_base : 0, c_out, y, y_dtype, ld_y, s, workspace, workspace_bytes};
+  return run_lora("lh_lora", l, ids_type, stream);
+}
+
+lh_status lh_lora_grad(const void* dy, int dy_dtype, int64_t n_rows, int64_t c_out, int64_t ld_dy,
+                       const int64_t* row_offsets, const void* adapter_ids, int ids_type, int64_t n_segments,
+                       const void* a, const void* b, int w_dtype, int64_t n_adapters, int64_t rank, const float* scale,
+                       const void* base, int64_t ld_base, int64_t c_in, void* dx, int dx_dtype, int64_t ld_dx,
+                       float* ds, void* workspace, size_t workspace_bytes, void* stream) {
+  lh::LoraArgs l{dy, dy_dtype, n_rows, c_out, ld_dy, {row_offsets, adapter_ids, ids_type == LH_INDEX_I64, n_segments, n_adapters},
+                 b, a, w_dtype, rank, scale, base, base ? ld_base : 0, c_in, dx, dx_dtype, ld_dx, ds, workspace, workspace_bytes};
+  return run_lora("lh_lora_grad", l, ids_type, stream);
+}
+
+size_t lh_lora_weight_grad_workspace_bytes(int64_t n_rows, int64_t n_segments, int64_t n_adapters, int64_t rank,
+                                           int64_t c_in, int64_t c_out) {
+  if (n_rows <= 0 || n_segments <= 0 || n_adapters <= 0 || n_adapters > lh::kLoraMaxAdapters || rank <= 0 ||
+      rank > lh::kLoraMaxRank || c_in < 0 || c_out < 0 || beyond_memory(n_rows, c_in) || beyond_memory(n_rows, c_out) ||
+      beyond_memory(n_rows, lh::kLoraMaxRank) || beyond_memory(n_adapters, lh::kLoraMaxRank, c_in) ||
+      beyond_memory(n_adapters, lh::kLoraMaxRank, c_out))
+    return 0;
+  return lh::lora_weight_ws_bytes(n_rows, n_segments, n_adapters, rank, c_in, c_out);
+}
+
+lh_status lh_lora_weight_grad(const void* x, int x_dtype, const uint8_t* x_scale, int64_t c_in, int64_t ld_x,
+                              const void* dy, int dy_dtype, int64_t c_out, int64_t ld_dy, const float* s,
+                              const float* ds, int64_t n_rows, const int64_t* row_offsets, const void* adapter_ids,
+                              int ids_type, int64_t n_segments, int64_t n_adapters, int64_t rank, const float* scale,
+                              float beta, void* da, void* db, int out_dtype, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  const char* fn = "lh_lora_weight_grad";
+  g_msg[0] = '\0';
+  if ((!valid_dtype(x_dtype) && x_dtype != LH_DTYPE_E4M3) || !valid_dtype(dy_dtype))
+    return fail(LH_ERR_DTYPE, "%s: x_dtype must be 0 (f32), 1 (bf16) or 2 (e4m3), dy_dtype 0 or 1", fn);
+  if (!valid_dtype(out_dtype)) return fail(LH_ERR_DTYPE, "%s: out_dtype must be 0 (f32) or 1 (bf16)", fn);
+  lh::LoraWeightArgs w{{{x, x_dtype, x_scale, c_in, ld_x, ds, da}, {dy, dy_dtype, nullptr, c_out, ld_dy, s, db}},
+                       n_rows, {row_offsets, adapter_ids, ids_type == LH_INDEX_I64, n_segments, n_adapters},
+                       rank, scale, beta, out_dtype, workspace, workspace_bytes};
+  const lh_status st = check_segments(fn, n_rows, w.seg, ids_type, rank);
+  if (st != LH_OK) return st;
+  if (c_in < 0 || c_out < 0) return fail(LH_ERR_SHAPE, "%s: negative size", fn);
+  if (n_adapters > lh::kLoraMaxAdapters) return fail(LH_ERR_SHAPE, "%s: n_adapters must be at most 1024", fn);
+  if (ld_x < c_in || ld_dy < c_out) return fail(LH_ERR_SHAPE, "%s: a leading dimension is smaller than its row", fn);
+  if (x_dtype == LH_DTYPE_E4M3 && ld_x != c_in && n_rows > 1)
+    return fail(LH_ERR_SHAPE, "%s: a checkpoint is dense (ld_x == c_in)", fn);
+  if (beyond_memory(n_rows, ld_x) || beyond_memory(n_rows, ld_dy) || beyond_memory(n_adapters, lh::kLoraMaxRank, c_in) ||
+      beyond_memory(n_adapters, lh::kLoraMaxRank, c_out))
+    return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
+  const bool any = n_adapters > 0 && rank > 0 && (c_in > 0 || c_out > 0);
+  if (any && da == nullptr && db == nullptr) return fail(LH_ERR_ARG, "%s: no output requested", fn);
+  const bool reads = any && n_rows > 0 && n_segments > 0;
+  if (reads && ((da && c_in > 0 && (x == nullptr || ds == nullptr || (x_dtype == LH_DTYPE_E4M3 && x_scale == nullptr))) ||
+                (db && c_out > 0 && (dy == nullptr || s == nullptr))))
+    return fail(LH_ERR_NULL, "%s: da needs x (with x_scale for a checkpoint) and ds, db needs dy and s", fn);
+  if (workspace == nullptr && workspace_bytes > 0) return fail(LH_ERR_NULL, "%s: workspace is NULL but workspace_bytes > 0", fn);
+  if ((x_dtype != LH_DTYPE_E4M3 && !aligned(x, elem_size(x_dtype))) || !aligned(dy, elem_size(dy_dtype)) ||
+      !aligned(s, 4) || !aligned(ds, 4) || !aligned(scale, 4) || !aligned(da, elem_size(out_dtype)) ||
+      !aligned(db, elem_size(out_dtype)) || !aligned(workspace, 256))
+    return fail(LH_ERR_ARG, "%s: misaligned pointer (workspace needs 256 bytes)", fn);
+  if (reads && workspace_bytes < lh::lora_weight_ws_bytes(n_rows, n_segments, n_adapters, rank, c_in, c_out))
+    return fail(LH_ERR_WORKSPACE, "%s: workspace smaller than lh_lora_weight_grad_workspace_bytes()", fn);
+  if (!any) return LH_OK;
+  if (!reads) w.rows = w.seg.n = 0;  // no rows: beta times what was there
+  const hipError_t e = lh::launch_lora_weight_grad(w, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks that packing and unpacking share.
+lh_status check_checkpoint(const char* fn, const void* x, int x_dtype, int64_t n_rows, int64_t cols, int64_t ld_x,
+                           const uint8_t* values, const uint8_t* scales) {
+  g_msg[0] = '\0';
+  if (!valid_dtype(x_dtype)) return fail(LH_ERR_DTYPE, "%s: x_dtype must be 0 (f32) or 1 (bf16)", fn);
+  if (n_rows < 0 || cols < 0) return fail(LH_ERR_SHAPE, "%s: negative size", fn);
+  if (ld_x < cols) return fail(LH_ERR_SHAPE, "%s: ld_x < cols", fn);
+  if (beyond_memory(n_rows, ld_x)) return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
+  if (n_rows > 0 && cols > 0 && (x == nullptr || values == nullptr || scales == nullptr))
+    return fail(LH_ERR_NULL, "%s: x, values and scales are required", fn);
+  if (!aligned(x, elem_size(x_dtype))) return fail(LH_ERR_ARG, "%s: x not aligned to its element size", fn);
+  return LH_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lh_status lh_checkpoint_pack(const void* x, int x_dtype, int64_t n_rows, int64_t cols, int64_t ld_x, uint8_t* values,
+                             uint8_t* scales, void* stream) {
+  const char* fn = "lh_checkpoint_pack";
+  const lh_status st = check_checkpoint(fn, x, x_dtype, n_rows, cols, ld_x, values, scales);
+  if (st != LH_OK || n_rows == 0 || cols == 0) return st;
+  lh::CheckpointArgs a{x, nullptr, x_dtype, n_rows, cols, ld_x, nullptr, nullptr, values, scales};
+  const hipError_t e = lh::launch_checkpoint_pack(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+lh_status lh_checkpoint_unpack(const uint8_t* values, const uint8_t* scales, int64_t n_rows, int64_t cols, void* x,
+                               int x_dtype, int64_t ld_x, void* stream) {
+  const char* fn = "lh_checkpoint_unpack";
+  const lh_status st = check_checkpoint(fn, x, x_dtype, n_rows, cols, ld_x, values, scales);
+  if (st != LH_OK || n_rows == 0 || cols == 0) return st;
+  lh::CheckpointArgs a{nullptr, x, x_dtype, n_rows, cols, ld_x, values, scales, nullptr, nullptr};
+  const hipError_t e = lh::launch_checkpoint_unpack(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LH_OK : hip_fail(e, fn);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
 // The whole path for callers that cannot allocate (code under graph capture,
 // tight serving loops, harnesses that forbid allocation).  The scratch that
 // lh_calibrate_nvfp4 takes as its workspace (skip certificates, the

@@ -269,4 +269,76 @@ hipError_t launch_moe_dispatch(const MoeRowsArgs& a, hipStream_t stream);
 hipError_t launch_moe_combine(const MoeRowsArgs& a, hipStream_t stream);
 hipError_t launch_moe_combine_grad(const MoeRowsArgs& a, hipStream_t stream);
 
+// Which rows take which adapter.
+struct SegmentArgs {
+  const int64_t* offsets;  // device [n + 1], or nullptr: n == n_rows (a row each) or n == 1 (all rows)
+  const void* ids;         // nullable: segment i takes adapter i
+  bool ids_i64;
+  int64_t n;
+  int64_t n_adapters;
+};
+
+// y = base + scale (x in^T) out, s = x in^T, with the factors [n_adapters]
+// [rank][.] of each row's adapter; the gradient exchanges the factors.
+struct LoraArgs {
+  const void* x;
+  int x_dtype;
+  int64_t rows, c_x, ld_x;
+  SegmentArgs seg;
+  const void* in;
+  const void* out;
+  int w_dtype;
+  int64_t rank;
+  const float* scale;      // nullable
+  const void* base;        // nullable, y_dtype
+  int64_t ld_base, c_y;
+  void* y;
+  int y_dtype;
+  int64_t ld_y;
+  float* s;                // nullable [rows][rank]
+  void* ws;
+  size_t ws_bytes;
+};
+size_t lora_ws_bytes(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, int64_t rank);
+hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
+
+constexpr int64_t kLoraMaxRank = 256;
+constexpr int64_t kLoraMaxAdapters = 1024;  // the gradient's LDS counters
+// One factor's gradient: out[g] = beta out[g] + scale[g] sum_t p[t]^T x[t].
+struct LoraFactor {
+  const void* x;
+  int dtype;               // 2: E4M3 with x_scale
+  const uint8_t* x_scale;
+  int64_t cols, ld;
+  const float* p;          // [rows][rank]
+  void* out;               // nullable: not asked for
+};
+struct LoraWeightArgs {
+  LoraFactor f[2];
+  int64_t rows;
+  SegmentArgs seg;
+  int64_t rank;
+  const float* scale;      // nullable
+  float beta;
+  int out_dtype;
+  void* ws;
+  size_t ws_bytes;
+};
+size_t lora_weight_ws_bytes(int64_t rows, int64_t segments, int64_t n_adapters, int64_t rank, int64_t c_in,
+                            int64_t c_out);
+hipError_t launch_lora_weight_grad(const LoraWeightArgs& a, hipStream_t stream);
+
+struct CheckpointArgs {
+  const void* x;           // pack: [rows][ld]
+  void* out;               // unpack: [rows][ld]
+  int dtype;
+  int64_t rows, cols, ld;
+  const uint8_t* values_in;
+  const uint8_t* scales_in;
+  uint8_t* values;
+  uint8_t* scales;
+};
+hipError_t launch_checkpoint_pack(const CheckpointArgs& a, hipStream_t stream);
+hipError_t launch_checkpoint_unpack(const CheckpointArgs& a, hipStream_t stream);
+
 }  // namespace lh

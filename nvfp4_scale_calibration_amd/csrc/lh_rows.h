@@ -1,6 +1,6 @@
 // lh_rows.h - row access of any alignment and the exact conversions shared by
 // the kernels that multiply, quantise and move rows (lh_linear.hip,
-// lh_moe.hip, lh_quant.hip).
+// lh_moe.hip, lh_quant.hip, lh_lora.hip, lh_checkpoint.hip).
 #pragma once
 
 #include <utility>
@@ -93,6 +93,11 @@ __device__ __forceinline__ uint16_t f32_to_bf16_bits(float v) { return __builtin
 template <int i>
 __device__ __forceinline__ float e4m3_to_f32(uint32_t v) {
   return __builtin_amdgcn_cvt_f32_fp8((int)v, i);
+}
+
+// E8M0 byte as fp32: 2^(byte - 127), 255 is NaN.
+__device__ __forceinline__ float e8m0_to_f32(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte == 0u ? 0x00400000u : byte << 23);
 }
 
 // Eight E2M1 nibbles (low nibble first) times c: exact, since r has 2

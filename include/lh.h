@@ -750,9 +750,10 @@ lh_status lh_moe_combine_grad(const void *dy, int dtype, int64_t n_tokens, int64
  *   row_offsets  device int64 [n_segments + 1], 8-byte aligned: segment i has
  *                the rows row_offsets[i] .. row_offsets[i+1]-1; expected
  *                non-decreasing within [0, n_rows].  No offset can lead outside
- *                a buffer; where segments overlap, the rows that they share get
- *                the adapter of one of them.  NULL: every row is a segment of its own
+ *                a buffer; where segments overlap, the first one has the rows
+ *                that they share.  NULL: every row is a segment of its own
  *                (n_segments == n_rows), or all rows are one (n_segments == 1).
+ *                n_segments and n_adapters are below 2^31.
  *   adapter_ids  ids_type (an lh_index) [n_segments], device; an id outside
  *                [0, n_adapters) means no adapter.  NULL: segment i takes
  *                adapter i (n_segments <= n_adapters; ids_type is ignored).

@@ -810,7 +810,7 @@ lh_status check_segments(const char* fn, int64_t n_rows, const lh::SegmentArgs& 
     return fail(LH_ERR_SHAPE, "%s: without row_offsets n_segments must be n_rows or 1", fn);
   if (g.ids == nullptr && g.n > g.n_adapters)
     return fail(LH_ERR_SHAPE, "%s: without adapter_ids there must be an adapter for every segment", fn);
-  if (beyond_memory(n_rows, lh::kLoraMaxRank) || beyond_memory(g.n, 1))
+  if (beyond_memory(n_rows, lh::kLoraMaxRank) || g.n > 0x7fffffff || g.n_adapters > 0x7fffffff)
     return fail(LH_ERR_SHAPE, "%s: sizes beyond any memory", fn);
   if (!aligned(g.offsets, 8) || !aligned(g.ids, ids_type == LH_INDEX_I64 ? 8 : 4))
     return fail(LH_ERR_ARG, "%s: row_offsets or adapter_ids not aligned to its element size", fn);

@@ -20,8 +20,8 @@ __device__ __forceinline__ int64_t adapter_of(const SegmentArgs& g, int64_t i) {
   return id >= 0 && id < g.n_adapters ? id : -1;
 }
 
-// Row t's adapter, -1 for none, -2 where t is in no segment.  All lanes of the
-// wave ask for the same row.
+// Row t's adapter, -1 for none, -2 where t is in no segment (the first one, where
+// segments overlap).  All lanes of the wave ask for the same row.
 __device__ __forceinline__ int64_t adapter_of_row(const SegmentArgs& g, int64_t t) {
   if (!g.offsets) return adapter_of(g, g.n == 1 ? 0 : t);
   const int lane = threadIdx.x & 63;
@@ -32,6 +32,32 @@ __device__ __forceinline__ int64_t adapter_of_row(const SegmentArgs& g, int64_t 
     if (hit) return uniform(adapter_of(g, i0 + __ffsll(hit) - 1));
   }
   return -2;
+}
+
+// The same for the rows t0 .. t0 + kRows - 1 of a tile, into LDS, by the whole
+// workgroup; rows past n_rows are in no segment.  Every thread looks at its
+// share of the segments; the smallest segment wins a row that several claim.
+template <int kRows>
+__device__ __forceinline__ void tile_adapters(const SegmentArgs& g, int64_t t0, int64_t n_rows, int (&of)[kRows]) {
+  __shared__ unsigned long long claim[kRows];
+  const int tid = threadIdx.x;
+  const int64_t t1 = min(t0 + kRows, n_rows);
+  if (!g.offsets) {
+    if (tid < kRows) of[tid] = t0 + tid < t1 ? (int)adapter_of(g, g.n == 1 ? 0 : t0 + tid) : -2;
+    __syncthreads();
+    return;
+  }
+  if (tid < kRows) claim[tid] = ~0ull;
+  __syncthreads();
+  for (int64_t i = tid; i < g.n; i += kThreads) {
+    const int64_t lo = max(g.offsets[i], t0), hi = min(g.offsets[i + 1], t1);
+    if (lo >= hi) continue;
+    const unsigned long long mine = ((unsigned long long)i << 32) | (uint32_t)(int)adapter_of(g, i);
+    for (int64_t t = lo; t < hi; ++t) atomicMin(&claim[t - t0], mine);
+  }
+  __syncthreads();
+  if (tid < kRows) of[tid] = claim[tid] == ~0ull ? -2 : (int)(uint32_t)claim[tid];
+  __syncthreads();
 }
 
 // Eight values of a row from p on as fp32, the first n of them inside it
@@ -143,6 +169,337 @@ __global__ __launch_bounds__(64) void lora_row_out_kernel(LoraArgs a, int64_t sp
 }
 
 // ---------------------------------------------------------------------------
+// The tile kernels: rows in tiles on the matrix cores, the rank in groups of 16.
+// bf16 inputs meet bf16 factors on v_mfma_f32_16x16x32_bf16 (exact products,
+// fp32 sums); where either is fp32 both are, on v_mfma_f32_16x16x4_f32.  The
+// adapters that a tile's rows take are gone through one after the other, each
+// over all of the tile; a row keeps its own adapter's result (rows and ranks of
+// a matrix product do not mix, so what belongs to others never has to be masked).
+// ---------------------------------------------------------------------------
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+// One lane's eight consecutive contraction elements of an operand.
+template <bool kBf>
+struct Frag;
+template <>
+struct Frag<true> {
+  uint4 v;
+};
+template <>
+struct Frag<false> {
+  float v[8];
+};
+__device__ __forceinline__ void load_frag(const uint16_t* p, Frag<true>& f) { f.v = load_u128(p); }
+template <typename T>
+__device__ __forceinline__ void load_frag(const T* p, Frag<false>& f) {
+  load8(p, 8, f.v);
+}
+__device__ __forceinline__ void load_frag(const uint16_t* p, int64_t n, Frag<true>& f) {
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  f.v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ void load_frag(const T* p, int64_t n, Frag<false>& f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f.v[i] = i < n ? load_as_f32<T>(p, i) : 0.0f;
+}
+__device__ __forceinline__ f32x4_t multiply(const Frag<true>& a, const Frag<true>& b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v), __builtin_bit_cast(bf16x8_t, b.v), c,
+                                                 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t multiply(const Frag<false>& a, const Frag<false>& b, f32x4_t c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+
+// Into the rank: a workgroup takes 32 rows and a share of the contraction, its
+// four waves a quarter of that each.  Operands come straight from global
+// memory, a lane eight consecutive elements of its row; the waves' sums are
+// joined through LDS, those of the shares by the kernel that reads them.
+constexpr int kInRows = 32;
+
+template <typename TX, typename TW, int kR16>
+__global__ __launch_bounds__(kThreads) void lora_tile_in_kernel(LoraArgs a, int splits, int64_t k_wave,
+                                                                float* __restrict__ part) {
+  constexpr bool kBf = sizeof(TX) == 2 && sizeof(TW) == 2;
+  constexpr int kSteps = kR16 <= 2 ? 4 : 2;  // contraction steps of 32 whose loads are in flight together
+  __shared__ int of[kInRows];
+  __shared__ __attribute__((aligned(16))) float red[kThreads / 64][kInRows][16];
+  const int64_t tile = block_id() / splits, split = block_id() - tile * splits, t0 = tile * kInRows;
+  if (t0 >= a.rows) return;
+  tile_adapters<kInRows>(a.seg, t0, a.rows, of);
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r16 = lane & 15, q = lane >> 4;
+  const int64_t k0 = min((split * 4 + wave) * k_wave, a.c_x), k1 = min(k0 + k_wave, a.c_x);
+  const int mine = of[lane & 31];
+  unsigned int left = (unsigned int)__ballot(mine >= 0);
+  const TX* x[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) x[h] = static_cast<const TX*>(a.x) + min(t0 + 16 * h + r16, a.rows - 1) * a.ld_x + 8 * q;
+  float* const dst = part + split * a.rows * a.rank;
+  while (left) {  // the same for the whole workgroup
+    const int g = __builtin_amdgcn_readlane(mine, __ffs(left) - 1);
+    left &= ~(unsigned int)__ballot(mine == g);
+    const TW* w[kR16];
+#pragma unroll
+    for (int i = 0; i < kR16; ++i)
+      w[i] = static_cast<const TW*>(a.in) + ((int64_t)g * a.rank + min((int64_t)(16 * i + r16), a.rank - 1)) * a.c_x + 8 * q;
+    f32x4_t acc[kR16][2];
+#pragma unroll
+    for (int i = 0; i < kR16; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) acc[i][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t k = k0;
+    for (; k + 32 * kSteps <= k1; k += 32 * kSteps) {
+      Frag<kBf> fx[kSteps][2], fw[kSteps][kR16];
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_frag(x[h] + k + 32 * u, fx[u][h]);
+#pragma unroll
+        for (int i = 0; i < kR16; ++i) load_frag(w[i] + k + 32 * u, fw[u][i]);
+      }
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+        for (int i = 0; i < kR16; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) acc[i][h] = multiply(fw[u][i], fx[u][h], acc[i][h]);
+    }
+    for (; k < k1; k += 32) {
+      Frag<kBf> fx[2];
+      const int64_t n = k1 - k - 8 * q;  // elements of this lane inside the row
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (n >= 8) load_frag(x[h] + k, fx[h]);
+        else load_frag(x[h] + k, n, fx[h]);
+      }
+#pragma unroll
+      for (int i = 0; i < kR16; ++i) {
+        Frag<kBf> fw;
+        if (n >= 8) load_frag(w[i] + k, fw);
+        else load_frag(w[i] + k, n, fw);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) acc[i][h] = multiply(fw, fx[h], acc[i][h]);
+      }
+    }
+    // lane: ranks 16 i + 4 q .. + 3 of the row 16 h + r16
+#pragma unroll
+    for (int i = 0; i < kR16; ++i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4_t*>(&red[wave][16 * h + r16][4 * q]) = acc[i][h];
+      __syncthreads();
+#pragma unroll
+      for (int e = tid; e < kInRows * 16; e += kThreads) {
+        const int t = e >> 4, r = e & 15;
+        if (of[t] == g && 16 * i + r < a.rank) {
+          float v = red[0][t][r];
+#pragma unroll
+          for (int u = 1; u < kThreads / 64; ++u) v += red[u][t][r];
+          dst[(t0 + t) * a.rank + 16 * i + r] = v;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  for (int64_t e = tid; e < kInRows * a.rank; e += kThreads) {
+    const int64_t t = e / a.rank;
+    if (of[t] == -1) dst[t0 * a.rank + e] = 0.0f;
+  }
+}
+
+// kN consecutive values of a row as fp32, the first n of them inside it.
+template <int kN, typename T>
+__device__ __forceinline__ void load_run(const T* p, int64_t n, float (&v)[kN]) {
+  T raw[kN];
+  if (n >= kN) {
+    __builtin_memcpy(raw, p, sizeof raw);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) raw[i] = i < n ? p[i] : T(0);
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = load_as_f32<T>(raw, i);
+}
+template <int kN>
+__device__ __forceinline__ void store_run(float* p, int64_t n, const float (&v)[kN]) {
+  if (n >= kN) {
+    __builtin_memcpy(p, v, sizeof v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+template <int kN>
+__device__ __forceinline__ void store_run(uint16_t* p, int64_t n, const float (&v)[kN]) {
+  uint32_t w[kN / 2];
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  if (n >= kN) {
+    __builtin_memcpy(p, w, sizeof w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+// Out of the rank: a workgroup takes up to 64 rows and 64 kOut outputs, each
+// wave 16 kOut of them, a lane kOut consecutive ones (those of one MFMA tile
+// are kOut apart, so that a row's outputs are read and written 16 bytes at a
+// lane).  A wave's part of the factor stays in its registers, as operands, for
+// all rows.  Factors are stored with the rank first, and an operand wants four
+// ranks of one output: bf16 ones are paired across two ranks' rows by byte
+// permutation.  s comes through LDS; bf16 factors meet it in kPlanes bf16
+// values that add up to it, to 16 bits (two, bf16 y) or exactly (three).
+constexpr int kOutRows = 64;
+
+template <typename TW, typename TY>
+constexpr int out_planes = sizeof(TW) == 4 ? 0 : sizeof(TY) == 2 ? 2 : 3;
+
+template <typename TW, typename TY, int kR16, int kOut>
+__global__ __launch_bounds__(kThreads) void lora_tile_out_kernel(LoraArgs a, const float* __restrict__ part, int splits,
+                                                                 int row_tile, int64_t col_tiles) {
+  constexpr int kPlanes = out_planes<TW, TY>;
+  constexpr int kPitch = 16 * kR16 + (kPlanes ? 8 : 4);  // elements of a row in LDS
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // kPlanes x [row_tile][kPitch] bf16, or [row_tile][kPitch] fp32
+  __shared__ int of[kOutRows];
+  const int64_t tile = block_id() / col_tiles, ct = block_id() - tile * col_tiles, t0 = tile * row_tile;
+  if (t0 >= a.rows) return;
+  tile_adapters<kOutRows>(a.seg, t0, min(t0 + row_tile, a.rows), of);
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, j16 = lane & 15, q = lane >> 4;
+  const int64_t rank = a.rank;
+  // s of the tile's rows: the sum of the contraction's shares, in their order
+  for (int e = tid; e < row_tile * 8 * kR16; e += kThreads) {
+    const int t = e / (8 * kR16), r = 2 * (e % (8 * kR16));
+    float v[2] = {};
+    if (of[t] >= -1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (r + h >= rank) continue;
+        const int64_t at = (t0 + t) * rank + r + h;
+        v[h] = sum_slices(part + at, a.rows * rank, splits);
+        if (a.s && ct == 0 && a.s != part) a.s[at] = v[h];
+      }
+    }
+    if constexpr (kPlanes == 0) {
+      *reinterpret_cast<float2*>(lds + (t * kPitch + r) * 4) = make_float2(v[0], v[1]);
+    } else {
+      uint32_t p[3];
+      split3(v[0], v[1], p);
+      if constexpr (kPlanes == 2) {  // the second part rounded, and no third
+        const float h0 = __uint_as_float(p[0] << 16), h1 = __uint_as_float(p[0] & 0xffff0000u);
+        p[1] = pack_bf16(isinf(v[0]) ? 0.0f : v[0] - h0, isinf(v[1]) ? 0.0f : v[1] - h1);
+      }
+#pragma unroll
+      for (int i = 0; i < kPlanes; ++i)
+        *reinterpret_cast<uint32_t*>(lds + ((i * row_tile + t) * kPitch + r) * 2) = p[i];
+    }
+  }
+  __syncthreads();
+  const int64_t c0 = (ct * 64 + 16 * wave) * kOut + kOut * j16, n = a.c_y - c0;
+  TY* const y = static_cast<TY*>(a.y) + t0 * a.ld_y + c0;
+  const TY* const base = a.base ? static_cast<const TY*>(a.base) + t0 * a.ld_base + c0 : nullptr;
+  const int mine = of[lane];
+  unsigned long long left = __ballot(mine >= 0);
+  while (left) {
+    const int g = __builtin_amdgcn_readlane(mine, __ffsll(left) - 1);
+    const unsigned long long rows = __ballot(mine == g);
+    left &= ~rows;
+    const float scale = a.scale ? a.scale[g] : 1.0f;
+    // ranks 16 i + 4 q + 0..3 of this lane's outputs
+    s16x4_t wb[kPlanes ? kR16 : 1][kOut];
+    float wf[kPlanes ? 1 : kR16][4][kOut];
+#pragma unroll
+    for (int i = 0; i < kR16; ++i) {
+      const TW* w = static_cast<const TW*>(a.out) + (int64_t)g * rank * a.c_y + c0;
+      TW raw[4][kOut];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t r = 16 * i + 4 * q + c;
+        const TW* p = w + r * a.c_y;
+        if (r < rank && n >= kOut) {
+          __builtin_memcpy(raw[c], p, sizeof raw[c]);
+        } else {
+#pragma unroll
+          for (int o = 0; o < kOut; ++o) raw[c][o] = r < rank && o < n ? p[o] : TW(0);
+        }
+      }
+      if constexpr (kPlanes == 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int o = 0; o < kOut; ++o) wf[i][c][o] = raw[c][o];
+      } else {
+        uint32_t d[4][kOut / 2];
+        __builtin_memcpy(d, raw, sizeof d);
+#pragma unroll
+        for (int o = 0; o < kOut / 2; ++o) {
+          const uint32_t lo[2] = {__builtin_amdgcn_perm(d[1][o], d[0][o], 0x05040100u), __builtin_amdgcn_perm(d[3][o], d[2][o], 0x05040100u)};
+          const uint32_t hi[2] = {__builtin_amdgcn_perm(d[1][o], d[0][o], 0x07060302u), __builtin_amdgcn_perm(d[3][o], d[2][o], 0x07060302u)};
+          __builtin_memcpy(&wb[i][2 * o], lo, 8);
+          __builtin_memcpy(&wb[i][2 * o + 1], hi, 8);
+        }
+      }
+    }
+    for (int t = 0; t < row_tile; t += 16) {
+      if (((rows >> t) & 0xffffull) == 0) continue;
+      float b[4][kOut];
+      bool live[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {  // the lane's rows t + 4 q + v
+        live[v] = ((rows >> (t + 4 * q + v)) & 1) && n > 0;
+#pragma unroll
+        for (int o = 0; o < kOut; ++o) b[v][o] = 0.0f;
+        if (live[v] && base) load_run<kOut>(base + (t + 4 * q + v) * a.ld_base, n, b[v]);
+      }
+      f32x4_t acc[kOut];
+#pragma unroll
+      for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kR16; ++i) {
+        if constexpr (kPlanes == 0) {
+          const float4 f = *reinterpret_cast<const float4*>(lds + ((t + j16) * kPitch + 16 * i + 4 * q) * 4);
+          const float sv[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x4f32(sv[c], wf[i][c][o], acc[o], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int p = kPlanes - 1; p >= 0; --p) {  // the smallest part first
+            const s16x4_t sv = *reinterpret_cast<const s16x4_t*>(lds + ((p * row_tile + t + j16) * kPitch + 16 * i + 4 * q) * 2);
+#pragma unroll
+            for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(sv, wb[i][o], acc[o], 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (!live[v]) continue;
+        float out[kOut];
+#pragma unroll
+        for (int o = 0; o < kOut; ++o) out[o] = __builtin_fmaf(scale, acc[o][v], b[v][o]);
+        store_run<kOut>(y + (t + 4 * q + v) * a.ld_y, n, out);
+      }
+    }
+  }
+  // rows without an adapter
+  if (n > 0 && a.base != a.y) {
+    for (int t = q; t < row_tile; t += 4) {
+      if (of[t] != -1) continue;
+      float b[kOut] = {};
+      if (base) load_run<kOut>(base + t * a.ld_base, n, b);
+      store_run<kOut>(y + t * a.ld_y, n, b);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Gradients to the factors: a thread per column, eight ranks at a time.
 // ---------------------------------------------------------------------------
 constexpr int kGradRanks = 8;
@@ -199,18 +556,46 @@ hipError_t by_type(int dtype, F&& f) {
 
 }  // namespace
 
-size_t lora_ws_bytes(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, int64_t rank) {
-  (void)segments;
-  (void)c_x;
-  (void)c_y;
-  return (size_t)rows * (size_t)rank * sizeof(float);
+namespace {
+
+// How the work is split, from sizes alone.
+struct LoraPlan {
+  bool rows;        // the row kernels
+  int splits;       // workgroups along the contraction
+  int64_t k_wave;   // tile kernels: elements of the contraction a wave takes
+};
+LoraPlan lora_plan(int64_t rows, int64_t segments, int64_t c_x) {
+  LoraPlan p{rows < 16 || rows < 4 * segments, 1, 0};
+  if (p.rows) return p;
+  const int64_t tiles = (rows + kInRows - 1) / kInRows, steps = (c_x + 31) / 32;
+  int64_t splits = (2048 / 4 + tiles - 1) / tiles;         // some eight waves a CU
+  const int64_t most = (steps + 15) / 16;                  // and four steps a wave at least
+  splits = splits < most ? splits : most;
+  splits = splits < 1 ? 1 : splits > 16 ? 16 : splits;
+  const int64_t per = (steps + 4 * splits - 1) / (4 * splits);
+  p.k_wave = 32 * (per > 0 ? per : 1);
+  p.splits = (int)((c_x + 4 * p.k_wave - 1) / (4 * p.k_wave));
+  if (p.splits < 1) p.splits = 1;
+  return p;
 }
 
-hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
-  const bool adds = a.rank > 0;
-  float* s = a.s ? a.s : static_cast<float*>(a.ws);
+template <typename F>
+hipError_t by_rank(int64_t rank, F&& f) {
+  const int64_t g = (rank + 15) / 16;
+  if (g <= 1) return f(std::integral_constant<int, 1>{});
+  if (g <= 2) return f(std::integral_constant<int, 2>{});
+  if (g <= 4) return f(std::integral_constant<int, 4>{});
+  if (g <= 8) return f(std::integral_constant<int, 8>{});
+  return f(std::integral_constant<int, 16>{});
+}
+
+// Outputs a lane, so that a wave's part of the factor takes 128 registers at most.
+template <typename TW, int kR16>
+constexpr int out_run = sizeof(TW) == 2 ? (kR16 <= 4 ? 8 : kR16 <= 8 ? 4 : 2) : (kR16 <= 8 ? 4 : 2);
+
+hipError_t launch_rows(const LoraArgs& a, float* s, hipStream_t stream) {
   hipError_t e = hipSuccess;
-  if (adds) {
+  if (a.rank > 0) {
     const int64_t groups = (a.rank + kRowRanks - 1) / kRowRanks;
     e = by_type(a.x_dtype, [&](auto x) {
       return by_type(a.w_dtype, [&](auto w) {
@@ -228,6 +613,55 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
       return hipGetLastError();
     });
   });
+}
+
+hipError_t launch_tiles(const LoraArgs& a, const LoraPlan& p, float* part, hipStream_t stream) {
+  const int64_t tiles = (a.rows + kInRows - 1) / kInRows;
+  const hipError_t e = by_type(a.x_dtype, [&](auto x) {
+    return by_type(a.w_dtype, [&](auto w) {
+      return by_rank(a.rank, [&](auto r) {
+        lora_tile_in_kernel<decltype(x), decltype(w), r><<<grid_of(tiles * p.splits), dim3(kThreads), 0, stream>>>(
+            a, p.splits, p.k_wave, part);
+        return hipGetLastError();
+      });
+    });
+  });
+  if (e != hipSuccess) return e;
+  return by_type(a.w_dtype, [&](auto w) {
+    return by_type(a.y_dtype, [&](auto y) {
+      return by_rank(a.rank, [&](auto r) {
+        using TW = decltype(w);
+        using TY = decltype(y);
+        constexpr int kOut = out_run<TW, r>, kPlanes = out_planes<TW, TY>;
+        const int64_t col_tiles = a.c_y > 64 * kOut ? (a.c_y + 64 * kOut - 1) / (64 * kOut) : 1;
+        // bytes of a row in LDS: below 26 KiB for 16 rows of any rank
+        constexpr size_t kRowBytes = kPlanes ? kPlanes * (16 * r + 8) * 2 : (16 * r + 4) * 4;
+        int row_tile = kOutRows;
+        while (row_tile > 16 &&
+               ((a.rows + row_tile - 1) / row_tile * col_tiles < 512 || row_tile * kRowBytes > 56 * 1024))
+          row_tile /= 2;
+        const size_t lds = row_tile * kRowBytes;
+        lora_tile_out_kernel<TW, TY, r, kOut>
+            <<<grid_of((a.rows + row_tile - 1) / row_tile * col_tiles), dim3(kThreads), lds, stream>>>(
+                a, part, p.splits, row_tile, col_tiles);
+        return hipGetLastError();
+      });
+    });
+  });
+}
+
+}  // namespace
+
+size_t lora_ws_bytes(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, int64_t rank) {
+  (void)c_y;
+  return (size_t)lora_plan(rows, segments, c_x).splits * (size_t)rows * (size_t)rank * sizeof(float);
+}
+
+hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
+  const LoraPlan p = lora_plan(a.rows, a.seg.n, a.c_x);
+  float* ws = static_cast<float*>(a.ws);
+  if (p.rows || a.rank == 0) return launch_rows(a, a.s ? a.s : ws, stream);
+  return launch_tiles(a, p, p.splits == 1 && a.s ? a.s : ws, stream);
 }
 
 size_t lora_weight_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }

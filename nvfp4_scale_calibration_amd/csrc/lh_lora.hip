@@ -7,6 +7,8 @@
 // first, so the gradient to the input (dy for x, b for in, a for out) is the
 // same two kernels.  The gradients to the factors are sums over an adapter's
 // rows, out[g][r][c] = scale[g] sum_t p[t][r] x[t][c].
+#include <type_traits>
+
 #include "lh_internal.h"
 #include "lh_rows.h"
 
@@ -500,53 +502,313 @@ __global__ __launch_bounds__(kThreads) void lora_tile_out_kernel(LoraArgs a, con
 }
 
 // ---------------------------------------------------------------------------
-// Gradients to the factors: a thread per column, eight ranks at a time.
+// Gradients to the factors, out[g][r][c] = scale[g] sum_t p[t][r] x[t][c]: a
+// product whose contraction runs over an adapter's rows.  The rows of adapter g
+// are those of all its segments, one after the other; a workgroup takes `chunk`
+// of them (a slot) and 16 kOut columns, its waves every fourth step of 32 rows.
+// A lane loads kOut consecutive columns of the eight rows 8 q .. 8 q + 7 of a
+// step and pairs rows by byte permutation, so that tile i of the product has the
+// columns kOut j + i; p meets them in three bf16 values that add up to it
+// exactly.  (fp32 rows: both as they are, v_mfma_f32_16x16x4_f32.)  Checkpoints
+// in 8 bits are decoded straight into that pairing, in bf16, which holds them.
+// Adapters of one slot are finished here; the sums of the others' slots are
+// added by lora_weight_sum_kernel in order: no atomics on data.
 // ---------------------------------------------------------------------------
-constexpr int kGradRanks = 8;
+// Where slot `s` works: adapter g, its rows k chunk .. in their order, and how
+// many there are; `parts` counts the slots of adapters with several before it.
+struct Slot {
+  int g;
+  int64_t row0, row1;  // of the adapter's rows
+  int64_t slots;       // the adapter's
+  int64_t part;        // the adapter's first place among the parts
+};
 
-template <int kDtype>
-__device__ __forceinline__ float value_at(const LoraFactor& f, int64_t t, int64_t c) {
-  if constexpr (kDtype == 0) return static_cast<const float*>(f.x)[t * f.ld + c];
-  if constexpr (kDtype == 1) return bf16_bits_to_f32(static_cast<const uint16_t*>(f.x)[t * f.ld + c]);
-  const uint32_t v = static_cast<const uint8_t*>(f.x)[t * f.cols + c];
-  return e4m3_to_f32<0>(v) * e8m0_to_f32(f.x_scale[t * ((f.cols + 31) / 32) + c / 32]);
+// cnt[g] = rows of adapter g, by the whole workgroup.
+__device__ __forceinline__ void segment_rows(const SegmentArgs& g, int64_t n_rows, int64_t i, int64_t& lo, int64_t& hi) {
+  if (g.offsets) {
+    lo = min(max(g.offsets[i], (int64_t)0), n_rows);
+    hi = min(max(g.offsets[i + 1], (int64_t)0), n_rows);
+  } else {
+    lo = g.n == 1 ? 0 : i;
+    hi = g.n == 1 ? n_rows : i + 1;
+  }
+  hi = max(lo, hi);
+}
+__device__ __forceinline__ void count_rows(const SegmentArgs& g, int64_t n_rows, unsigned long long* cnt) {
+  for (int i = threadIdx.x; i < (int)g.n_adapters; i += kThreads) cnt[i] = 0;
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < g.n; i += kThreads) {
+    const int64_t id = adapter_of(g, i);
+    int64_t lo, hi;
+    segment_rows(g, n_rows, i, lo, hi);
+    if (id >= 0 && hi > lo) atomicAdd(&cnt[id], (unsigned long long)(hi - lo));
+  }
+  __syncthreads();
+}
+// The slot `want` (kByAdapter: the first slot of adapter `want`), every wave for itself.
+template <bool kByAdapter>
+__device__ __forceinline__ bool find_slot(const unsigned long long* cnt, int64_t n_adapters, int64_t chunk, int64_t want,
+                                          Slot& s) {
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0, parts = 0;
+  for (int64_t g0 = 0; g0 < n_adapters; g0 += 64) {
+    const bool in = g0 + lane < n_adapters;
+    const int64_t rows = in ? (int64_t)cnt[g0 + lane] : 0;
+    const int64_t slots = in ? max((int64_t)1, (rows + chunk - 1) / chunk) : 0;
+    int64_t incl = slots, pin = slots > 1 ? slots : 0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t u = __shfl_up(incl, off), v = __shfl_up(pin, off);
+      if (lane >= off) incl += u, pin += v;
+    }
+    const unsigned long long hit = kByAdapter ? __ballot(g0 + lane == want) : __ballot(before + incl > want);
+    if (hit) {
+      const int l = __ffsll(hit) - 1;
+      const int64_t k = kByAdapter ? 0 : want - uniform(before + __shfl(incl - slots, l));
+      const int64_t all = uniform(__shfl(rows, l));
+      s.g = (int)(g0 + l);
+      s.slots = uniform(__shfl(slots, l));
+      s.part = parts + uniform(__shfl(pin, l)) - (s.slots > 1 ? s.slots : 0);
+      s.row0 = k * chunk;
+      s.row1 = min(s.row0 + chunk, all);
+      return true;
+    }
+    before += uniform(__shfl(incl, 63));
+    parts += uniform(__shfl(pin, 63));
+  }
+  return false;
 }
 
-template <int kDtype, typename TO>
-__global__ __launch_bounds__(kThreads) void lora_weight_kernel(LoraWeightArgs a, LoraFactor f, int64_t col_tiles,
-                                                               int64_t rank_tiles) {
-  const int64_t unit = block_id(), per = col_tiles * rank_tiles, g = unit / per, in = unit - g * per;
-  if (g >= a.seg.n_adapters) return;
-  const int64_t r0 = in / col_tiles * kGradRanks, c = in % col_tiles * kThreads + threadIdx.x;
-  if (c >= f.cols) return;
-  float acc[kGradRanks] = {};
-  for (int64_t i = 0; i < a.seg.n; ++i) {
-    if (adapter_of(a.seg, i) != g) continue;
-    int64_t t0, t1;
-    if (a.seg.offsets) {
-      t0 = min(max(a.seg.offsets[i], (int64_t)0), a.rows);
-      t1 = min(max(a.seg.offsets[i + 1], (int64_t)0), a.rows);
+constexpr int kMostChunk = 2048;  // rows of a slot, which are listed in LDS
+
+// list[0 .. row1 - row0): the buffer's rows, by the whole workgroup; the caller
+// waits before it reads them.
+__device__ __forceinline__ void list_rows(const SegmentArgs& g, int64_t n_rows, const Slot& s, int* list) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  int64_t at = 0;  // the adapter's rows before this group of segments
+  for (int64_t i0 = 0; i0 < g.n && at < s.row1; i0 += 64) {
+    int64_t lo = 0, hi = 0;
+    if (i0 + lane < g.n && adapter_of(g, i0 + lane) == s.g) segment_rows(g, n_rows, i0 + lane, lo, hi);
+    const int64_t len = hi - lo;
+    int64_t incl = len;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t u = __shfl_up(incl, off);
+      if (lane >= off) incl += u;
+    }
+    const int64_t first = at + incl - len;
+    const int64_t f0 = max(first, s.row0), f1 = min(first + len, s.row1);  // the part of the segment that is wanted
+    if (f1 > f0 && len <= 4 && tid < 64)
+      for (int64_t f = f0; f < f1; ++f) list[f - s.row0] = (int)(lo + f - first);
+    unsigned long long more = __ballot(f1 > f0 && len > 4);
+    while (more) {
+      const int l = __ffsll(more) - 1;
+      more &= more - 1;
+      const int64_t a0 = __shfl(f0, l), a1 = __shfl(f1, l), from = __shfl(lo - first, l);
+      for (int64_t f = a0 + tid; f < a1; f += kThreads) list[f - s.row0] = (int)(from + f);
+    }
+    at += uniform(__shfl(incl, 63));
+  }
+}
+
+// kOut consecutive columns of one row, the first n of them inside it: bf16 pairs (dtypes 1, 2) or fp32.
+template <int kDtype, int kOut>
+struct Cols {
+  uint32_t w[kDtype == 0 ? kOut : kOut / 2];
+};
+template <int kDtype, int kOut, bool kWhole>
+__device__ __forceinline__ Cols<kDtype, kOut> load_cols(const LoraFactor& f, int64_t row, int64_t c, int64_t n) {
+  Cols<kDtype, kOut> r;
+  if constexpr (kDtype == 2) {
+    uint8_t b[kOut];
+    const uint8_t* p = static_cast<const uint8_t*>(f.x) + row * f.cols + c;
+    if (kWhole || n >= kOut) {
+      __builtin_memcpy(b, p, sizeof b);
     } else {
-      t0 = a.seg.n == 1 ? 0 : i;
-      t1 = a.seg.n == 1 ? a.rows : i + 1;
-    }
-    for (int64_t t = t0; t < t1; ++t) {
-      const float v = value_at<kDtype>(f, t, c);
 #pragma unroll
-      for (int r = 0; r < kGradRanks; ++r)
-        if (r0 + r < a.rank) acc[r] = __builtin_fmaf(f.p[t * a.rank + r0 + r], v, acc[r]);
+      for (int o = 0; o < kOut; ++o) b[o] = o < n ? p[o] : 0;
+    }
+    const float up = kWhole || n > 0 ? e8m0_to_f32(f.x_scale[row * ((f.cols + 31) / 32) + c / 32]) : 1.0f;
+    static_for<kOut / 2>([&](auto o) {
+      const uint32_t two = (uint32_t)b[2 * o] | (uint32_t)b[2 * o + 1] << 8;
+      r.w[o] = pack_bf16(e4m3_to_f32<0>(two) * up, e4m3_to_f32<1>(two) * up);
+    });
+  } else {
+    using T = std::conditional_t<kDtype == 0, float, uint16_t>;
+    const T* p = static_cast<const T*>(f.x) + row * f.ld + c;
+    if (kWhole || n >= kOut) {
+      __builtin_memcpy(r.w, p, sizeof r.w);
+    } else {
+      T raw[kOut];
+#pragma unroll
+      for (int o = 0; o < kOut; ++o) raw[o] = o < n ? p[o] : T(0);
+      __builtin_memcpy(r.w, raw, sizeof r.w);
     }
   }
-  const float scale = a.scale ? a.scale[g] : 1.0f;
-  TO* out = static_cast<TO*>(f.out) + (g * a.rank + r0) * f.cols + c;
+  return r;
+}
+
+// Steps of 32 rows of the list, `steps` of them from row i on, every fourth.
+// kWhole: rows and columns all inside.
+template <int kDtype, int kR16, int kOut, bool kWhole>
+__device__ __forceinline__ void weight_step(const LoraFactor& f, int64_t rank, const int* list, int at, int count, int64_t c,
+                                            int64_t n, f32x4_t (&acc)[kR16][kOut]) {
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+  int row[8];
+  bool in[8];
+  Cols<kDtype, kOut> x[8];
 #pragma unroll
-  for (int r = 0; r < kGradRanks; ++r) {
-    if (r0 + r >= a.rank) break;
-    float v = scale * acc[r];
-    if (a.beta != 0.0f) v = __builtin_fmaf(a.beta, load_as_f32<TO>(out, r * f.cols), v);
-    if constexpr (sizeof(TO) == 2) out[r * f.cols] = f32_to_bf16_bits(v);
-    else out[r * f.cols] = v;
+  for (int j = 0; j < 8; ++j) {
+    const int i = at + 8 * q + j;
+    in[j] = kWhole || i < count;
+    row[j] = list[in[j] ? i : 0];
+    if (in[j]) x[j] = load_cols<kDtype, kOut, kWhole>(f, row[j], c, n);
+    else x[j] = Cols<kDtype, kOut>{};
   }
+  if constexpr (kDtype == 0) {
+#pragma unroll
+    for (int i = 0; i < kR16; ++i) {
+      const int64_t r = min((int64_t)(16 * i + r16), rank - 1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = in[j] ? f.p[row[j] * rank + r] : 0.0f;
+#pragma unroll
+        for (int o = 0; o < kOut; ++o)
+          acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, __uint_as_float(x[j].w[o]), acc[i][o], 0, 0, 0);
+      }
+    }
+  } else {
+    uint32_t b[kOut][4];  // operands: rows 8 q + 2 j, + 1 of one column
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int o = 0; o < kOut / 2; ++o) {
+        b[2 * o][j] = __builtin_amdgcn_perm(x[2 * j + 1].w[o], x[2 * j].w[o], 0x05040100u);
+        b[2 * o + 1][j] = __builtin_amdgcn_perm(x[2 * j + 1].w[o], x[2 * j].w[o], 0x07060302u);
+      }
+#pragma unroll
+    for (int i = 0; i < kR16; ++i) {
+      const int64_t r = min((int64_t)(16 * i + r16), rank - 1);
+      float p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[j] = in[j] ? f.p[row[j] * rank + r] : 0.0f;
+      uint32_t a[4][3];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split3(p[2 * j], p[2 * j + 1], a[j]);
+#pragma unroll
+      for (int u = 2; u >= 0; --u) {  // the smallest part first
+        const bf16x8_t fa = __builtin_bit_cast(bf16x8_t, make_uint4(a[0][u], a[1][u], a[2][u], a[3][u]));
+#pragma unroll
+        for (int o = 0; o < kOut; ++o)
+          acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              fa, __builtin_bit_cast(bf16x8_t, make_uint4(b[o][0], b[o][1], b[o][2], b[o][3])), acc[i][o], 0, 0, 0);
+      }
+    }
+  }
+}
+
+// scale v + beta out, kN consecutive elements, the first n of them inside the row.
+template <int kN>
+__device__ __forceinline__ void finish(const LoraWeightArgs& a, const LoraFactor& f, float scale, int64_t at, int64_t n,
+                                       const float (&v)[kN]) {
+  float w[kN], old[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) w[i] = scale * v[i];
+  if (a.out_dtype == 1) {
+    uint16_t* p = static_cast<uint16_t*>(f.out) + at;
+    if (a.beta != 0.0f) {
+      load_run<kN>(p, n, old);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) w[i] = __builtin_fmaf(a.beta, old[i], w[i]);
+    }
+    store_run<kN>(p, n, w);
+  } else {
+    float* p = static_cast<float*>(f.out) + at;
+    if (a.beta != 0.0f) {
+      load_run<kN>(p, n, old);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) w[i] = __builtin_fmaf(a.beta, old[i], w[i]);
+    }
+    store_run<kN>(p, n, w);
+  }
+}
+
+template <int kDtype, int kR16, int kOut>
+__global__ __launch_bounds__(kThreads) void lora_weight_kernel(LoraWeightArgs a, LoraFactor f, int64_t chunk,
+                                                               int64_t col_tiles, float* __restrict__ part,
+                                                               int64_t parts) {
+  __shared__ unsigned long long cnt[kLoraMaxAdapters];
+  __shared__ int list[kMostChunk];
+  __shared__ __attribute__((aligned(16))) float red[kThreads / 64][16][16 * kOut];
+  const int64_t want = block_id() / col_tiles, ct = block_id() - want * col_tiles;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, j16 = lane & 15, q = lane >> 4;
+  count_rows(a.seg, a.rows, cnt);
+  Slot s;
+  if (!find_slot<false>(cnt, a.seg.n_adapters, chunk, want, s)) return;  // the whole workgroup
+  list_rows(a.seg, a.rows, s, list);
+  __syncthreads();
+  const int count = (int)(s.row1 - s.row0);
+  const int64_t c_tile = ct * 16 * kOut, c = c_tile + kOut * j16, n = f.cols - c;
+  f32x4_t acc[kR16][kOut];
+#pragma unroll
+  for (int i = 0; i < kR16; ++i)
+#pragma unroll
+    for (int o = 0; o < kOut; ++o) acc[i][o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const bool whole = c_tile + 16 * kOut <= f.cols;
+  int at = 32 * wave;
+  if (whole)
+    for (; at + 32 <= count; at += 128) weight_step<kDtype, kR16, kOut, true>(f, a.rank, list, at, count, c, n, acc);
+  for (; at < count; at += 128) weight_step<kDtype, kR16, kOut, false>(f, a.rank, list, at, count, c, n, acc);
+  // the waves' sums, 16 ranks at a time; a thread has kOut columns of one rank
+  const float scale = a.scale ? a.scale[s.g] : 1.0f;
+  const int r = tid >> 4;
+#pragma unroll
+  for (int i = 0; i < kR16; ++i) {
+    if (i > 0) __syncthreads();
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int o = 0; o < kOut; ++o) red[wave][4 * q + v][kOut * j16 + o] = acc[i][o][v];
+    __syncthreads();
+    float sum[kOut];
+#pragma unroll
+    for (int o = 0; o < kOut; ++o) {
+      sum[o] = red[0][r][kOut * j16 + o];
+#pragma unroll
+      for (int w = 1; w < kThreads / 64; ++w) sum[o] += red[w][r][kOut * j16 + o];
+    }
+    if (16 * i + r < a.rank && n > 0) {
+      const int64_t k = s.slots > 1 ? s.part + s.row0 / chunk : s.g;
+      const int64_t to = (k * a.rank + 16 * i + r) * f.cols + c;
+      // (rows that overlapping segments claim twice can make more parts than there is room for)
+      if (s.slots == 1) finish<kOut>(a, f, scale, to, n, sum);
+      else if (k < parts) store_run<kOut>(part + to, n, sum);
+    }
+  }
+}
+
+// The sums of an adapter's slots, if it has several.
+constexpr int kSumRun = 4;
+__global__ __launch_bounds__(kThreads) void lora_weight_sum_kernel(LoraWeightArgs a, LoraFactor f, int64_t chunk,
+                                                                   int64_t spans, const float* __restrict__ part,
+                                                                   int64_t parts) {
+  __shared__ unsigned long long cnt[kLoraMaxAdapters];
+  const int64_t g = block_id() / spans, span = block_id() - g * spans;
+  if (g >= a.seg.n_adapters) return;
+  count_rows(a.seg, a.rows, cnt);
+  Slot s;
+  if (!find_slot<true>(cnt, a.seg.n_adapters, chunk, g, s) || s.slots < 2) return;
+  const int64_t all = a.rank * f.cols, e = (span * kThreads + threadIdx.x) * kSumRun, n = all - e;
+  if (n <= 0) return;
+  const float* p = part + s.part * all + e;
+  const int64_t slots = min(s.slots, parts - s.part);
+  float v[kSumRun] = {}, w[kSumRun];
+  for (int64_t k = 0; k < slots; ++k) {
+    load_run<kSumRun>(p + k * all, n, w);
+#pragma unroll
+    for (int i = 0; i < kSumRun; ++i) v[i] += w[i];
+  }
+  finish<kSumRun>(a, f, a.scale ? a.scale[g] : 1.0f, g * all + e, n, v);
 }
 
 template <typename F>
@@ -664,20 +926,60 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
   return launch_tiles(a, p, p.splits == 1 && a.s ? a.s : ws, stream);
 }
 
-size_t lora_weight_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+namespace {
+
+// Columns a lane takes, so that the sums of a wave take 128 registers.
+constexpr int weight_run(int r16, int dtype) { return r16 <= 4 ? (dtype == 0 ? 4 : 8) : r16 <= 8 ? 4 : 2; }
+int rank_groups(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : rank <= 128 ? 8 : 16; }
+
+// Rows of a slot: 256 to 2048, so that some 512 workgroups have work.
+int64_t weight_chunk(int64_t rows, int64_t rank, int64_t cols) {
+  const int64_t tile = 16 * weight_run(rank_groups(rank), 1), tiles = (cols + tile - 1) / tile;
+  int64_t chunk = kMostChunk;
+  while (chunk > 256 && (rows + chunk - 1) / chunk * tiles < 512) chunk /= 2;
+  return chunk;
+}
+// Parts: the slots of adapters that have several, at most two for every chunk of rows.
+int64_t weight_parts(int64_t rows, int64_t chunk) { return rows > chunk ? 2 * (rows / chunk) : 0; }
+
+}  // namespace
+
+size_t lora_weight_ws_bytes(int64_t rows, int64_t segments, int64_t n_adapters, int64_t rank, int64_t c_in,
+                            int64_t c_out) {
+  (void)segments;
+  (void)n_adapters;
+  size_t most = 0;
+  for (const int64_t cols : {c_in, c_out}) {
+    const size_t b = (size_t)weight_parts(rows, weight_chunk(rows, rank, cols)) * (size_t)rank * (size_t)cols * sizeof(float);
+    most = b > most ? b : most;
+  }
+  return most;
+}
 
 hipError_t launch_lora_weight_grad(const LoraWeightArgs& a, hipStream_t stream) {
+  float* part = static_cast<float*>(a.ws);
   for (const LoraFactor& f : a.f) {
     if (!f.out || f.cols == 0) continue;
-    const int64_t cols = (f.cols + kThreads - 1) / kThreads, ranks = (a.rank + kGradRanks - 1) / kGradRanks;
-    const dim3 grid = grid_of(a.seg.n_adapters * cols * ranks);
-    const hipError_t e = by_type(a.out_dtype, [&](auto o) {
-      using TO = decltype(o);
-      if (f.dtype == 0) lora_weight_kernel<0, TO><<<grid, dim3(kThreads), 0, stream>>>(a, f, cols, ranks);
-      else if (f.dtype == 1) lora_weight_kernel<1, TO><<<grid, dim3(kThreads), 0, stream>>>(a, f, cols, ranks);
-      else lora_weight_kernel<2, TO><<<grid, dim3(kThreads), 0, stream>>>(a, f, cols, ranks);
-      return hipGetLastError();
+    const int64_t chunk = weight_chunk(a.rows, a.rank, f.cols), slots = a.seg.n_adapters + a.rows / chunk;
+    const int64_t parts = weight_parts(a.rows, chunk);
+    hipError_t e = by_rank(a.rank, [&](auto r) {
+      const auto launch = [&](auto d) {
+        constexpr int kOut = weight_run(r, d);
+        const int64_t tiles = (f.cols + 16 * kOut - 1) / (16 * kOut);
+        lora_weight_kernel<d, r, kOut><<<grid_of(slots * tiles), dim3(kThreads), 0, stream>>>(a, f, chunk, tiles, part,
+                                                                                                   parts);
+        return hipGetLastError();
+      };
+      if (f.dtype == 0) return launch(std::integral_constant<int, 0>{});
+      if (f.dtype == 1) return launch(std::integral_constant<int, 1>{});
+      return launch(std::integral_constant<int, 2>{});
     });
+    if (e != hipSuccess) return e;
+    if (parts == 0) continue;
+    const int64_t spans = (a.rank * f.cols + kThreads * kSumRun - 1) / (kThreads * kSumRun);
+    lora_weight_sum_kernel<<<grid_of(a.seg.n_adapters * spans), dim3(kThreads), 0, stream>>>(a, f, chunk, spans, part,
+                                                                                             parts);
+    e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

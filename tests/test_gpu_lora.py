@@ -251,6 +251,15 @@ def test_bad_offsets_stay_inside(lh):
         lh.lh_lora(x, a, b, offsets=off, y=wide[10:30])
         lh.lh_lora_weight_grad(x, wide[10:30], torch.ones(20, 8, device=DEV), torch.ones(20, 8, device=DEV), 3, offsets=off)
         assert (wide[:10] == 9).all() and (wide[30:] == 9).all()
+    # every segment claims all rows: more rows than there are, in more slots than there is room for
+    rows = 1500
+    off = torch.tensor([0, rows] * 20 + [0], device=DEV)
+    x, p = rand(rng, (rows, 64), BF16).to(DEV), torch.ones(rows, 8, device=DEV)
+    nbytes = lh.lh_lora_weight_grad_workspace_bytes(rows, 40, 40, 8, 64, 64)
+    ws = torch.full((nbytes + 4096,), 3, dtype=torch.uint8, device=DEV)
+    da, db = lh.lh_lora_weight_grad(x, x, p, p, 40, offsets=off, workspace=ws[:nbytes])
+    torch.cuda.synchronize()
+    assert (ws[nbytes:] == 3).all() and da.shape == (40, 8, 64)
 
 
 def test_far_adapters(lh):

@@ -53,7 +53,6 @@ __device__ __forceinline__ void tile_adapters(const SegmentArgs& g, int64_t t0, 
   __syncthreads();
   for (int64_t i = tid; i < g.n; i += kThreads) {
     const int64_t lo = max(g.offsets[i], t0), hi = min(g.offsets[i + 1], t1);
-    if (lo >= hi) continue;
     const unsigned long long mine = ((unsigned long long)i << 32) | (uint32_t)(int)adapter_of(g, i);
     for (int64_t t = lo; t < hi; ++t) atomicMin(&claim[t - t0], mine);
   }
@@ -220,28 +219,43 @@ __device__ __forceinline__ f32x4_t multiply(const Frag<false>& a, const Frag<fal
 
 // Into the rank: a workgroup takes 32 rows and a share of the contraction, its
 // four waves a quarter of that each.  Operands come straight from global
-// memory, a lane eight consecutive elements of its row; the waves' sums are
-// joined through LDS, those of the shares by the kernel that reads them.
+// memory, a lane eight consecutive elements of its row, the next steps' while
+// the matrix cores work on these; the waves' sums are joined through LDS, those
+// of the shares by the kernel that reads them.
 constexpr int kInRows = 32;
 
 template <typename TX, typename TW, int kR16>
 __global__ __launch_bounds__(kThreads) void lora_tile_in_kernel(LoraArgs a, int splits, int64_t k_wave,
                                                                 float* __restrict__ part) {
   constexpr bool kBf = sizeof(TX) == 2 && sizeof(TW) == 2;
-  constexpr int kSteps = kR16 <= 2 ? 4 : 2;  // contraction steps of 32 whose loads are in flight together
+  // contraction steps of 32 that are loaded together: two such loads are in flight, in at most 160 registers
+  constexpr int kSteps = kBf ? (kR16 <= 2 ? 4 : kR16 <= 4 ? 2 : 1) : (kR16 <= 2 ? 2 : 1);
   __shared__ int of[kInRows];
   __shared__ __attribute__((aligned(16))) float red[kThreads / 64][kInRows][16];
   const int64_t tile = block_id() / splits, split = block_id() - tile * splits, t0 = tile * kInRows;
   if (t0 >= a.rows) return;
-  tile_adapters<kInRows>(a.seg, t0, a.rows, of);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r16 = lane & 15, q = lane >> 4;
   const int64_t k0 = min((split * 4 + wave) * k_wave, a.c_x), k1 = min(k0 + k_wave, a.c_x);
-  const int mine = of[lane & 31];
-  unsigned int left = (unsigned int)__ballot(mine >= 0);
+  const int64_t stages = (k1 - k0) / (32 * kSteps);
   const TX* x[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) x[h] = static_cast<const TX*>(a.x) + min(t0 + 16 * h + r16, a.rows - 1) * a.ld_x + 8 * q;
+  struct Stage {
+    Frag<kBf> x[kSteps][2], w[kSteps][kR16];
+  };
+  const auto load_x = [&](Stage& f, int64_t k) {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_frag(x[h] + k + 32 * u, f.x[u][h]);
+  };
+  Stage f0, f1;
+  if (stages > 0) load_x(f0, k0);  // before it is known whose rows they are
+  tile_adapters<kInRows>(a.seg, t0, a.rows, of);
+  const int mine = of[lane & 31];
+  unsigned int left = (unsigned int)__ballot(mine >= 0);
   float* const dst = part + split * a.rows * a.rank;
+  bool again = false;
   while (left) {  // the same for the whole workgroup
     const int g = __builtin_amdgcn_readlane(mine, __ffs(left) - 1);
     left &= ~(unsigned int)__ballot(mine == g);
@@ -254,36 +268,55 @@ __global__ __launch_bounds__(kThreads) void lora_tile_in_kernel(LoraArgs a, int 
     for (int i = 0; i < kR16; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) acc[i][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    int64_t k = k0;
-    for (; k + 32 * kSteps <= k1; k += 32 * kSteps) {
-      Frag<kBf> fx[kSteps][2], fw[kSteps][kR16];
+    const auto load_w = [&](Stage& f, int64_t k) {
 #pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
+      for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) load_frag(x[h] + k + 32 * u, fx[u][h]);
-#pragma unroll
-        for (int i = 0; i < kR16; ++i) load_frag(w[i] + k + 32 * u, fw[u][i]);
-      }
+        for (int i = 0; i < kR16; ++i) load_frag(w[i] + k + 32 * u, f.w[u][i]);
+    };
+    const auto add = [&](const Stage& f) {
 #pragma unroll
       for (int u = 0; u < kSteps; ++u)
 #pragma unroll
         for (int i = 0; i < kR16; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) acc[i][h] = multiply(fw[u][i], fx[u][h], acc[i][h]);
+          for (int h = 0; h < 2; ++h) acc[i][h] = multiply(f.w[u][i], f.x[u][h], acc[i][h]);
+    };
+    int64_t k = k0, n = stages;
+    if (n > 0) {
+      if (again) load_x(f0, k);
+      load_w(f0, k);
     }
+    while (n >= 2) {
+      load_x(f1, k + 32 * kSteps);
+      load_w(f1, k + 32 * kSteps);
+      add(f0);
+      if (n > 2) {
+        load_x(f0, k + 64 * kSteps);
+        load_w(f0, k + 64 * kSteps);
+      }
+      add(f1);
+      k += 64 * kSteps;
+      n -= 2;
+    }
+    if (n > 0) {
+      add(f0);
+      k += 32 * kSteps;
+    }
+    again = true;
     for (; k < k1; k += 32) {
       Frag<kBf> fx[2];
-      const int64_t n = k1 - k - 8 * q;  // elements of this lane inside the row
+      const int64_t in = k1 - k - 8 * q;  // elements of this lane inside the row
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (n >= 8) load_frag(x[h] + k, fx[h]);
-        else load_frag(x[h] + k, n, fx[h]);
+        if (in >= 8) load_frag(x[h] + k, fx[h]);
+        else load_frag(x[h] + k, in, fx[h]);
       }
 #pragma unroll
       for (int i = 0; i < kR16; ++i) {
         Frag<kBf> fw;
-        if (n >= 8) load_frag(w[i] + k, fw);
-        else load_frag(w[i] + k, n, fw);
+        if (in >= 8) load_frag(w[i] + k, fw);
+        else load_frag(w[i] + k, in, fw);
 #pragma unroll
         for (int h = 0; h < 2; ++h) acc[i][h] = multiply(fw, fx[h], acc[i][h]);
       }
@@ -313,18 +346,39 @@ __global__ __launch_bounds__(kThreads) void lora_tile_in_kernel(LoraArgs a, int 
   }
 }
 
-// kN consecutive values of a row as fp32, the first n of them inside it.
+// kN consecutive values of a row as they are, the first n of them inside it (the
+// others are zero), in whole words.
 template <int kN, typename T>
-__device__ __forceinline__ void load_run(const T* p, int64_t n, float (&v)[kN]) {
-  T raw[kN];
+struct Run {
+  static constexpr int kWords = kN * sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    else return __uint_as_float(w[i]);
+  }
+};
+template <int kN, typename T>
+__device__ __forceinline__ Run<kN, T> load_raw(const T* p, int64_t n) {
+  Run<kN, T> r;
   if (n >= kN) {
-    __builtin_memcpy(raw, p, sizeof raw);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) raw[i] = i < n ? p[i] : T(0);
+    __builtin_memcpy(r.w, p, sizeof r.w);
+    return r;
   }
 #pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = load_as_f32<T>(raw, i);
+  for (int i = 0; i < Run<kN, T>::kWords; ++i) {
+    if constexpr (sizeof(T) == 2)
+      r.w[i] = (2 * i < n ? (uint32_t)p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    else
+      r.w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+  }
+  return r;
+}
+// The same as fp32.
+template <int kN, typename T>
+__device__ __forceinline__ void load_run(const T* p, int64_t n, float (&v)[kN]) {
+  const Run<kN, T> r = load_raw<kN>(p, n);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = r.at(i);
 }
 template <int kN>
 __device__ __forceinline__ void store_run(float* p, int64_t n, const float (&v)[kN]) {
@@ -350,62 +404,105 @@ __device__ __forceinline__ void store_run(uint16_t* p, int64_t n, const float (&
   }
 }
 
+// kN consecutive values but for the first `skip`.
+template <int kN, typename T>
+__device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[kN]) {
+  if (skip == 0) {
+    store_run<kN>(p, kN, v);
+  } else if (skip < kN) {
+#pragma unroll
+    for (int i = 1; i < kN; ++i)
+      if (i >= skip) {
+        if constexpr (sizeof(T) == 2) p[i] = f32_to_bf16_bits(v[i]);
+        else p[i] = v[i];
+      }
+  }
+}
+
 // Out of the rank: a workgroup takes up to 64 rows and 64 kOut outputs, each
 // wave 16 kOut of them, a lane kOut consecutive ones (those of one MFMA tile
 // are kOut apart, so that a row's outputs are read and written 16 bytes at a
-// lane).  A wave's part of the factor stays in its registers, as operands, for
-// all rows.  Factors are stored with the rank first, and an operand wants four
-// ranks of one output: bf16 ones are paired across two ranks' rows by byte
-// permutation.  s comes through LDS; bf16 factors meet it in kPlanes bf16
-// values that add up to it, to 16 bits (two, bf16 y) or exactly (three).
+// lane).  A wave's part of the factor stays in its registers, as operands, while
+// it goes through the rows 16 at a time, what base holds of the next ones being
+// loaded meanwhile.  Factors are stored with the rank first, and an operand wants
+// four ranks of one output: bf16 ones are paired across two ranks' rows by byte
+// permutation.  s comes through LDS; bf16 factors meet it in kPlanes bf16 values
+// that add up to it, to 16 bits (two, bf16 y) or exactly (three).
 constexpr int kOutRows = 64;
 
 template <typename TW, typename TY>
 constexpr int out_planes = sizeof(TW) == 4 ? 0 : sizeof(TY) == 2 ? 2 : 3;
 
-template <typename TW, typename TY, int kR16, int kOut>
-__global__ __launch_bounds__(kThreads) void lora_tile_out_kernel(LoraArgs a, const float* __restrict__ part, int splits,
+// Outputs a lane, so that a wave's part of the factor takes 128 registers at most.
+template <typename TW, int kR16>
+constexpr int out_run = sizeof(TW) == 2 ? (kR16 <= 4 ? 8 : kR16 <= 8 ? 4 : 2) : (kR16 <= 8 ? 4 : 2);
+
+// Waves per SIMD that the registers are held to: as many as go without spilling.
+template <typename TW, typename TY, int kR16>
+constexpr int out_waves = sizeof(TW) == 2 ? (kR16 == 1 && sizeof(TY) == 2 ? 3 : kR16 <= 2 || (kR16 <= 8 && sizeof(TY) == 2) ? 2 : 1)
+                                          : (kR16 <= 2 ? 3 : kR16 <= 4 ? 2 : 1);
+
+template <typename TW, typename TY, int kR16>
+__global__ __launch_bounds__(kThreads, out_waves<TW, TY, kR16>) void lora_tile_out_kernel(LoraArgs a, const float* __restrict__ part, int splits,
                                                                  int row_tile, int64_t col_tiles) {
-  constexpr int kPlanes = out_planes<TW, TY>;
+  constexpr int kPlanes = out_planes<TW, TY>, kOut = out_run<TW, kR16>;
   constexpr int kPitch = 16 * kR16 + (kPlanes ? 8 : 4);  // elements of a row in LDS
   extern __shared__ __attribute__((aligned(16))) char lds[];  // kPlanes x [row_tile][kPitch] bf16, or [row_tile][kPitch] fp32
   __shared__ int of[kOutRows];
   const int64_t tile = block_id() / col_tiles, ct = block_id() - tile * col_tiles, t0 = tile * row_tile;
   if (t0 >= a.rows) return;
-  tile_adapters<kOutRows>(a.seg, t0, min(t0 + row_tile, a.rows), of);
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, j16 = lane & 15, q = lane >> 4;
-  const int64_t rank = a.rank;
-  // s of the tile's rows: the sum of the contraction's shares, in their order
-  for (int e = tid; e < row_tile * 8 * kR16; e += kThreads) {
-    const int t = e / (8 * kR16), r = 2 * (e % (8 * kR16));
-    float v[2] = {};
-    if (of[t] >= -1) {
+  const int64_t rank = a.rank, t1 = min(t0 + row_tile, a.rows);
+  // The lane's outputs.  At the end of a row they are moved back, so that all of
+  // them can be loaded, and the `skip` first belong to another lane.
+  const int64_t c_own = (ct * 64 + 16 * wave) * kOut + kOut * j16, c0 = min(c_own, a.c_y - kOut);
+  const int skip = (int)min(c_own - c0, (int64_t)kOut);
+  const TY* const base = static_cast<const TY*>(a.base);
+  Run<kOut, TY> b[4], next[4];
+  const auto load_base = [&](int t, Run<kOut, TY> (&to)[4]) {  // the lane's rows t + 4 q + v
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (r + h >= rank) continue;
-        const int64_t at = (t0 + t) * rank + r + h;
-        v[h] = sum_slices(part + at, a.rows * rank, splits);
-        if (a.s && ct == 0 && a.s != part) a.s[at] = v[h];
+    for (int v = 0; v < 4; ++v) {
+      if (base) __builtin_memcpy(to[v].w, base + min(t0 + t + 4 * q + v, t1 - 1) * a.ld_base + c0, sizeof to[v].w);
+      else to[v] = Run<kOut, TY>{};
+    }
+  };
+  load_base(0, b);  // before it is known whose rows they are
+  tile_adapters<kOutRows>(a.seg, t0, t1, of);
+  // s of the tile's rows: the sum of the contraction's shares, in their order
+#pragma unroll 2
+  for (int e = tid; e < row_tile * 4 * kR16; e += kThreads) {
+    const int t = e / (4 * kR16), r = 4 * (e % (4 * kR16));
+    float v[4] = {};
+    if (of[t] >= -1 && r < rank) {
+      const int64_t at = (t0 + t) * rank + r, in = rank - r;
+      load_run<4>(part + at, in, v);
+      for (int u = 1; u < splits; ++u) {
+        float w[4];
+        load_run<4>(part + u * a.rows * rank + at, in, w);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) v[h] += w[h];
       }
+      if (a.s && ct == 0 && a.s != part) store_run<4>(a.s + at, in, v);
     }
     if constexpr (kPlanes == 0) {
-      *reinterpret_cast<float2*>(lds + (t * kPitch + r) * 4) = make_float2(v[0], v[1]);
+      *reinterpret_cast<float4*>(lds + (t * kPitch + r) * 4) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-      uint32_t p[3];
-      split3(v[0], v[1], p);
-      if constexpr (kPlanes == 2) {  // the second part rounded, and no third
-        const float h0 = __uint_as_float(p[0] << 16), h1 = __uint_as_float(p[0] & 0xffff0000u);
-        p[1] = pack_bf16(isinf(v[0]) ? 0.0f : v[0] - h0, isinf(v[1]) ? 0.0f : v[1] - h1);
+      uint32_t p[2][3];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        split3(v[2 * h], v[2 * h + 1], p[h]);
+        if constexpr (kPlanes == 2) {  // the second part rounded, and no third
+          const float h0 = __uint_as_float(p[h][0] << 16), h1 = __uint_as_float(p[h][0] & 0xffff0000u);
+          p[h][1] = pack_bf16(isinf(v[2 * h]) ? 0.0f : v[2 * h] - h0, isinf(v[2 * h + 1]) ? 0.0f : v[2 * h + 1] - h1);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kPlanes; ++i)
-        *reinterpret_cast<uint32_t*>(lds + ((i * row_tile + t) * kPitch + r) * 2) = p[i];
+        *reinterpret_cast<uint2*>(lds + ((i * row_tile + t) * kPitch + r) * 2) = make_uint2(p[0][i], p[1][i]);
     }
   }
   __syncthreads();
-  const int64_t c0 = (ct * 64 + 16 * wave) * kOut + kOut * j16, n = a.c_y - c0;
-  TY* const y = static_cast<TY*>(a.y) + t0 * a.ld_y + c0;
-  const TY* const base = a.base ? static_cast<const TY*>(a.base) + t0 * a.ld_base + c0 : nullptr;
+  TY* const y = static_cast<TY*>(a.y);
   const int mine = of[lane];
   unsigned long long left = __ballot(mine >= 0);
   while (left) {
@@ -419,84 +516,86 @@ __global__ __launch_bounds__(kThreads) void lora_tile_out_kernel(LoraArgs a, con
 #pragma unroll
     for (int i = 0; i < kR16; ++i) {
       const TW* w = static_cast<const TW*>(a.out) + (int64_t)g * rank * a.c_y + c0;
-      TW raw[4][kOut];
+      Run<kOut, TW> d[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int64_t r = 16 * i + 4 * q + c;
-        const TW* p = w + r * a.c_y;
-        if (r < rank && n >= kOut) {
-          __builtin_memcpy(raw[c], p, sizeof raw[c]);
-        } else {
+        __builtin_memcpy(d[c].w, w + min(r, rank - 1) * a.c_y, sizeof d[c].w);
 #pragma unroll
-          for (int o = 0; o < kOut; ++o) raw[c][o] = r < rank && o < n ? p[o] : TW(0);
-        }
+        for (int o = 0; o < Run<kOut, TW>::kWords; ++o) d[c].w[o] = r < rank ? d[c].w[o] : 0u;
       }
       if constexpr (kPlanes == 0) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int o = 0; o < kOut; ++o) wf[i][c][o] = raw[c][o];
+          for (int o = 0; o < kOut; ++o) wf[i][c][o] = d[c].at(o);
       } else {
-        uint32_t d[4][kOut / 2];
-        __builtin_memcpy(d, raw, sizeof d);
 #pragma unroll
         for (int o = 0; o < kOut / 2; ++o) {
-          const uint32_t lo[2] = {__builtin_amdgcn_perm(d[1][o], d[0][o], 0x05040100u), __builtin_amdgcn_perm(d[3][o], d[2][o], 0x05040100u)};
-          const uint32_t hi[2] = {__builtin_amdgcn_perm(d[1][o], d[0][o], 0x07060302u), __builtin_amdgcn_perm(d[3][o], d[2][o], 0x07060302u)};
+          const uint32_t lo[2] = {__builtin_amdgcn_perm(d[1].w[o], d[0].w[o], 0x05040100u),
+                                  __builtin_amdgcn_perm(d[3].w[o], d[2].w[o], 0x05040100u)};
+          const uint32_t hi[2] = {__builtin_amdgcn_perm(d[1].w[o], d[0].w[o], 0x07060302u),
+                                  __builtin_amdgcn_perm(d[3].w[o], d[2].w[o], 0x07060302u)};
           __builtin_memcpy(&wb[i][2 * o], lo, 8);
           __builtin_memcpy(&wb[i][2 * o + 1], hi, 8);
         }
       }
     }
+#pragma unroll 1
     for (int t = 0; t < row_tile; t += 16) {
-      if (((rows >> t) & 0xffffull) == 0) continue;
-      float b[4][kOut];
-      bool live[4];
+      if (t + 16 < row_tile) load_base(t + 16, next);
+      if ((rows >> t) & 0xffffull) {
+        f32x4_t acc[kOut];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {  // the lane's rows t + 4 q + v
-        live[v] = ((rows >> (t + 4 * q + v)) & 1) && n > 0;
+        for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int o = 0; o < kOut; ++o) b[v][o] = 0.0f;
-        if (live[v] && base) load_run<kOut>(base + (t + 4 * q + v) * a.ld_base, n, b[v]);
-      }
-      f32x4_t acc[kOut];
+        for (int i = 0; i < kR16; ++i) {
+          if constexpr (kPlanes == 0) {
+            const float4 f = *reinterpret_cast<const float4*>(lds + ((t + j16) * kPitch + 16 * i + 4 * q) * 4);
+            const float sv[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-      for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int i = 0; i < kR16; ++i) {
-        if constexpr (kPlanes == 0) {
-          const float4 f = *reinterpret_cast<const float4*>(lds + ((t + j16) * kPitch + 16 * i + 4 * q) * 4);
-          const float sv[4] = {f.x, f.y, f.z, f.w};
+              for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x4f32(sv[c], wf[i][c][o], acc[o], 0, 0, 0);
+          } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int p = kPlanes - 1; p >= 0; --p) {  // the smallest part first
+              const s16x4_t sv =
+                  *reinterpret_cast<const s16x4_t*>(lds + ((p * row_tile + t + j16) * kPitch + 16 * i + 4 * q) * 2);
 #pragma unroll
-            for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x4f32(sv[c], wf[i][c][o], acc[o], 0, 0, 0);
-        } else {
-#pragma unroll
-          for (int p = kPlanes - 1; p >= 0; --p) {  // the smallest part first
-            const s16x4_t sv = *reinterpret_cast<const s16x4_t*>(lds + ((p * row_tile + t + j16) * kPitch + 16 * i + 4 * q) * 2);
-#pragma unroll
-            for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(sv, wb[i][o], acc[o], 0, 0, 0);
+              for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(sv, wb[i][o], acc[o], 0, 0, 0);
+            }
           }
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t at = t + 4 * q + v;
+          if (((rows >> at) & 1) == 0) continue;
+          float out[kOut];
+#pragma unroll
+          for (int o = 0; o < kOut; ++o) out[o] = __builtin_fmaf(scale, acc[o][v], b[v].at(o));
+          store_own<kOut>(y + (t0 + at) * a.ld_y + c0, skip, out);
         }
       }
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (!live[v]) continue;
-        float out[kOut];
-#pragma unroll
-        for (int o = 0; o < kOut; ++o) out[o] = __builtin_fmaf(scale, acc[o][v], b[v][o]);
-        store_run<kOut>(y + (t + 4 * q + v) * a.ld_y, n, out);
-      }
+      for (int v = 0; v < 4; ++v) b[v] = next[v];
     }
+    if (left) load_base(0, b);
   }
   // rows without an adapter
-  if (n > 0 && a.base != a.y) {
-    for (int t = q; t < row_tile; t += 4) {
-      if (of[t] != -1) continue;
-      float b[kOut] = {};
-      if (base) load_run<kOut>(base + t * a.ld_base, n, b);
-      store_run<kOut>(y + t * a.ld_y, n, b);
+  const unsigned long long bare = __ballot(mine == -1);
+  if (bare == 0 || a.base == a.y) return;
+#pragma unroll 1
+  for (int t = 0; t < row_tile; t += 16) {
+    load_base(t, b);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int64_t at = t + 4 * q + v;
+      if (((bare >> at) & 1) == 0) continue;
+      float out[kOut];
+#pragma unroll
+      for (int o = 0; o < kOut; ++o) out[o] = b[v].at(o);
+      store_own<kOut>(y + (t0 + at) * a.ld_y + c0, skip, out);
     }
   }
 }
@@ -826,8 +925,8 @@ struct LoraPlan {
   int splits;       // workgroups along the contraction
   int64_t k_wave;   // tile kernels: elements of the contraction a wave takes
 };
-LoraPlan lora_plan(int64_t rows, int64_t segments, int64_t c_x) {
-  LoraPlan p{rows < 16 || rows < 4 * segments, 1, 0};
+LoraPlan lora_plan(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y) {
+  LoraPlan p{rows < 16 || rows < 4 * segments || c_y < 8, 1, 0};
   if (p.rows) return p;
   const int64_t tiles = (rows + kInRows - 1) / kInRows, steps = (c_x + 31) / 32;
   int64_t splits = (2048 / 4 + tiles - 1) / tiles;         // some eight waves a CU
@@ -850,10 +949,6 @@ hipError_t by_rank(int64_t rank, F&& f) {
   if (g <= 8) return f(std::integral_constant<int, 8>{});
   return f(std::integral_constant<int, 16>{});
 }
-
-// Outputs a lane, so that a wave's part of the factor takes 128 registers at most.
-template <typename TW, int kR16>
-constexpr int out_run = sizeof(TW) == 2 ? (kR16 <= 4 ? 8 : kR16 <= 8 ? 4 : 2) : (kR16 <= 8 ? 4 : 2);
 
 hipError_t launch_rows(const LoraArgs& a, float* s, hipStream_t stream) {
   hipError_t e = hipSuccess;
@@ -895,7 +990,7 @@ hipError_t launch_tiles(const LoraArgs& a, const LoraPlan& p, float* part, hipSt
         using TW = decltype(w);
         using TY = decltype(y);
         constexpr int kOut = out_run<TW, r>, kPlanes = out_planes<TW, TY>;
-        const int64_t col_tiles = a.c_y > 64 * kOut ? (a.c_y + 64 * kOut - 1) / (64 * kOut) : 1;
+        const int64_t col_tiles = (a.c_y + 64 * kOut - 1) / (64 * kOut);
         // bytes of a row in LDS: below 26 KiB for 16 rows of any rank
         constexpr size_t kRowBytes = kPlanes ? kPlanes * (16 * r + 8) * 2 : (16 * r + 4) * 4;
         int row_tile = kOutRows;
@@ -903,9 +998,8 @@ hipError_t launch_tiles(const LoraArgs& a, const LoraPlan& p, float* part, hipSt
                ((a.rows + row_tile - 1) / row_tile * col_tiles < 512 || row_tile * kRowBytes > 56 * 1024))
           row_tile /= 2;
         const size_t lds = row_tile * kRowBytes;
-        lora_tile_out_kernel<TW, TY, r, kOut>
-            <<<grid_of((a.rows + row_tile - 1) / row_tile * col_tiles), dim3(kThreads), lds, stream>>>(
-                a, part, p.splits, row_tile, col_tiles);
+        lora_tile_out_kernel<TW, TY, r><<<grid_of((a.rows + row_tile - 1) / row_tile * col_tiles), dim3(kThreads), lds,
+                                          stream>>>(a, part, p.splits, row_tile, col_tiles);
         return hipGetLastError();
       });
     });
@@ -915,12 +1009,11 @@ hipError_t launch_tiles(const LoraArgs& a, const LoraPlan& p, float* part, hipSt
 }  // namespace
 
 size_t lora_ws_bytes(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, int64_t rank) {
-  (void)c_y;
-  return (size_t)lora_plan(rows, segments, c_x).splits * (size_t)rows * (size_t)rank * sizeof(float);
+  return (size_t)lora_plan(rows, segments, c_x, c_y).splits * (size_t)rows * (size_t)rank * sizeof(float);
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
-  const LoraPlan p = lora_plan(a.rows, a.seg.n, a.c_x);
+  const LoraPlan p = lora_plan(a.rows, a.seg.n, a.c_x, a.c_y);
   float* ws = static_cast<float*>(a.ws);
   if (p.rows || a.rank == 0) return launch_rows(a, a.s ? a.s : ws, stream);
   return launch_tiles(a, p, p.splits == 1 && a.s ? a.s : ws, stream);

@@ -443,7 +443,7 @@ constexpr int out_waves = sizeof(TW) == 2 ? (kR16 == 1 && sizeof(TY) == 2 ? 3 : 
                                           : (kR16 <= 2 ? 3 : kR16 <= 4 ? 2 : 1);
 
 template <typename TW, typename TY, int kR16>
-__global__ __launch_bounds__(kThreads, out_waves<TW, TY, kR16>) void lora_tile_out_kernel(LoraArgs a, const float* __restrict__ part, int splits,
+__global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile_out_kernel(LoraArgs a, const float* __restrict__ part, int splits,
                                                                  int row_tile, int64_t col_tiles) {
   constexpr int kPlanes = out_planes<TW, TY>, kOut = out_run<TW, kR16>;
   constexpr int kPitch = 16 * kR16 + (kPlanes ? 8 : 4);  // elements of a row in LDS

@@ -51,7 +51,7 @@ __device__ __forceinline__ void tile_adapters(const SegmentArgs& g, int64_t t0, 
   }
   if (tid < kRows) claim[tid] = ~0ull;
   __syncthreads();
-  for (int64_t i = tid; i < g.n; i += kThreads) {
+  for (int64_t i = tid; i < g.n; i += blockDim.x) {
     const int64_t lo = max(g.offsets[i], t0), hi = min(g.offsets[i + 1], t1);
     const unsigned long long mine = ((unsigned long long)i << 32) | (uint32_t)(int)adapter_of(g, i);
     for (int64_t t = lo; t < hi; ++t) atomicMin(&claim[t - t0], mine);
@@ -179,6 +179,15 @@ __global__ __launch_bounds__(64) void lora_row_out_kernel(LoraArgs a, int64_t sp
 // ---------------------------------------------------------------------------
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
+template <typename T>
+__device__ __forceinline__ const T* at_byte(const T* p, uint32_t offset) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(p) + offset);
+}
+template <typename T>
+__device__ __forceinline__ T* at_byte(T* p, uint32_t offset) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(p) + offset);
+}
+
 // One lane's eight consecutive contraction elements of an operand.
 template <bool kBf>
 struct Frag;
@@ -217,62 +226,64 @@ __device__ __forceinline__ f32x4_t multiply(const Frag<false>& a, const Frag<fal
   return c;
 }
 
-// Into the rank: a workgroup takes 32 rows and a share of the contraction, its
-// four waves a quarter of that each.  Operands come straight from global
-// memory, a lane eight consecutive elements of its row, the next steps' while
-// the matrix cores work on these; the waves' sums are joined through LDS, those
-// of the shares by the kernel that reads them.
-constexpr int kInRows = 32;
+// Into the rank where the input or the factor is fp32: a workgroup takes 32 rows
+// and a share of the contraction, its four waves a quarter of that each.  Operands
+// come straight from global memory, a lane eight consecutive elements of its row,
+// the next steps' while the matrix cores work on these; the waves' sums are joined
+// through LDS, those of the shares by the kernel that reads them.
+constexpr int kInSub = 2, kInRows = 16 * kInSub, kInWaves = 4;
 
 template <typename TX, typename TW, int kR16>
-__global__ __launch_bounds__(kThreads) void lora_tile_in_kernel(LoraArgs a, int splits, int64_t k_wave,
-                                                                float* __restrict__ part) {
-  constexpr bool kBf = sizeof(TX) == 2 && sizeof(TW) == 2;
-  // contraction steps of 32 that are loaded together: two such loads are in flight, in at most 160 registers
-  constexpr int kSteps = kBf ? (kR16 <= 2 ? 4 : kR16 <= 4 ? 2 : 1) : (kR16 <= 2 ? 2 : 1);
+__global__ __launch_bounds__(64 * kInWaves) void lora_tile_in_kernel(LoraArgs a, int splits, int64_t k_wave,
+                                                                     float* __restrict__ part) {
+  constexpr bool kBf = false;
+  constexpr int kSub = kInSub, kWaves = kInWaves;
+  constexpr int kSteps = kR16 <= 2 ? 2 : 1;  // contraction steps of 32 that are loaded together (twice as many are in flight)
   __shared__ int of[kInRows];
-  __shared__ __attribute__((aligned(16))) float red[kThreads / 64][kInRows][16];
+  __shared__ __attribute__((aligned(16))) float red[kWaves][kInRows][16];
   const int64_t tile = block_id() / splits, split = block_id() - tile * splits, t0 = tile * kInRows;
   if (t0 >= a.rows) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r16 = lane & 15, q = lane >> 4;
-  const int64_t k0 = min((split * 4 + wave) * k_wave, a.c_x), k1 = min(k0 + k_wave, a.c_x);
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, r16 = lane & 15, q = lane >> 4;
+  const int64_t k0 = min((split * kWaves + wave) * k_wave, a.c_x), k1 = min(k0 + k_wave, a.c_x);
   const int64_t stages = (k1 - k0) / (32 * kSteps);
-  const TX* x[2];
+  // a uniform address and 32 bits of a lane's own: bytes of its rows
+  const TX* const xt = static_cast<const TX*>(a.x) + t0 * a.ld_x;
+  uint32_t x[kSub];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) x[h] = static_cast<const TX*>(a.x) + min(t0 + 16 * h + r16, a.rows - 1) * a.ld_x + 8 * q;
+  for (int h = 0; h < kSub; ++h) x[h] = ((uint32_t)(min((int64_t)(16 * h + r16), a.rows - 1 - t0) * a.ld_x) + 8 * q) * sizeof(TX);
   struct Stage {
-    Frag<kBf> x[kSteps][2], w[kSteps][kR16];
+    Frag<kBf> x[kSteps][kSub], w[kSteps][kR16];
   };
   const auto load_x = [&](Stage& f, int64_t k) {
 #pragma unroll
     for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) load_frag(x[h] + k + 32 * u, f.x[u][h]);
+      for (int h = 0; h < kSub; ++h) load_frag(at_byte(xt + k + 32 * u, x[h]), f.x[u][h]);
   };
   Stage f0, f1;
   if (stages > 0) load_x(f0, k0);  // before it is known whose rows they are
   tile_adapters<kInRows>(a.seg, t0, a.rows, of);
-  const int mine = of[lane & 31];
-  unsigned int left = (unsigned int)__ballot(mine >= 0);
+  const int mine = of[lane % kInRows];
+  unsigned long long left = __ballot(mine >= 0);
   float* const dst = part + split * a.rows * a.rank;
   bool again = false;
   while (left) {  // the same for the whole workgroup
-    const int g = __builtin_amdgcn_readlane(mine, __ffs(left) - 1);
-    left &= ~(unsigned int)__ballot(mine == g);
-    const TW* w[kR16];
+    const int g = __builtin_amdgcn_readlane(mine, __ffsll(left) - 1);
+    left &= ~__ballot(mine == g);
+    const TW* const wt = static_cast<const TW*>(a.in) + (int64_t)g * a.rank * a.c_x;
+    uint32_t w[kR16];
+#pragma unroll
+    for (int i = 0; i < kR16; ++i) w[i] = ((uint32_t)(min((int64_t)(16 * i + r16), a.rank - 1) * a.c_x) + 8 * q) * sizeof(TW);
+    f32x4_t acc[kR16][kSub];
 #pragma unroll
     for (int i = 0; i < kR16; ++i)
-      w[i] = static_cast<const TW*>(a.in) + ((int64_t)g * a.rank + min((int64_t)(16 * i + r16), a.rank - 1)) * a.c_x + 8 * q;
-    f32x4_t acc[kR16][2];
 #pragma unroll
-    for (int i = 0; i < kR16; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) acc[i][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int h = 0; h < kSub; ++h) acc[i][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const auto load_w = [&](Stage& f, int64_t k) {
 #pragma unroll
       for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-        for (int i = 0; i < kR16; ++i) load_frag(w[i] + k + 32 * u, f.w[u][i]);
+        for (int i = 0; i < kR16; ++i) load_frag(at_byte(wt + k + 32 * u, w[i]), f.w[u][i]);
     };
     const auto add = [&](const Stage& f) {
 #pragma unroll
@@ -280,7 +291,7 @@ __global__ __launch_bounds__(kThreads) void lora_tile_in_kernel(LoraArgs a, int 
 #pragma unroll
         for (int i = 0; i < kR16; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) acc[i][h] = multiply(f.w[u][i], f.x[u][h], acc[i][h]);
+          for (int h = 0; h < kSub; ++h) acc[i][h] = multiply(f.w[u][i], f.x[u][h], acc[i][h]);
     };
     int64_t k = k0, n = stages;
     if (n > 0) {
@@ -305,42 +316,42 @@ __global__ __launch_bounds__(kThreads) void lora_tile_in_kernel(LoraArgs a, int 
     }
     again = true;
     for (; k < k1; k += 32) {
-      Frag<kBf> fx[2];
+      Frag<kBf> fx[kSub];
       const int64_t in = k1 - k - 8 * q;  // elements of this lane inside the row
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (in >= 8) load_frag(x[h] + k, fx[h]);
-        else load_frag(x[h] + k, in, fx[h]);
+      for (int h = 0; h < kSub; ++h) {
+        if (in >= 8) load_frag(at_byte(xt + k, x[h]), fx[h]);
+        else load_frag(at_byte(xt + k, x[h]), in, fx[h]);
       }
 #pragma unroll
       for (int i = 0; i < kR16; ++i) {
         Frag<kBf> fw;
-        if (in >= 8) load_frag(w[i] + k, fw);
-        else load_frag(w[i] + k, in, fw);
+        if (in >= 8) load_frag(at_byte(wt + k, w[i]), fw);
+        else load_frag(at_byte(wt + k, w[i]), in, fw);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) acc[i][h] = multiply(fw, fx[h], acc[i][h]);
+        for (int h = 0; h < kSub; ++h) acc[i][h] = multiply(fw, fx[h], acc[i][h]);
       }
     }
     // lane: ranks 16 i + 4 q .. + 3 of the row 16 h + r16
 #pragma unroll
     for (int i = 0; i < kR16; ++i) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4_t*>(&red[wave][16 * h + r16][4 * q]) = acc[i][h];
+      for (int h = 0; h < kSub; ++h) *reinterpret_cast<f32x4_t*>(&red[wave][16 * h + r16][4 * q]) = acc[i][h];
       __syncthreads();
 #pragma unroll
-      for (int e = tid; e < kInRows * 16; e += kThreads) {
+      for (int e = tid; e < kInRows * 16; e += 64 * kWaves) {
         const int t = e >> 4, r = e & 15;
         if (of[t] == g && 16 * i + r < a.rank) {
           float v = red[0][t][r];
 #pragma unroll
-          for (int u = 1; u < kThreads / 64; ++u) v += red[u][t][r];
+          for (int u = 1; u < kWaves; ++u) v += red[u][t][r];
           dst[(t0 + t) * a.rank + 16 * i + r] = v;
         }
       }
       __syncthreads();
     }
   }
-  for (int64_t e = tid; e < kInRows * a.rank; e += kThreads) {
+  for (int64_t e = tid; e < kInRows * a.rank; e += 64 * kWaves) {
     const int64_t t = e / a.rank;
     if (of[t] == -1) dst[t0 * a.rank + e] = 0.0f;
   }
@@ -430,6 +441,32 @@ __device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[kN]) 
 // that add up to it, to 16 bits (two, bf16 y) or exactly (three).
 constexpr int kOutRows = 64;
 
+// Two pairs of fp32 values in kPlanes (2 or 3) bf16 values each that add up to them.
+template <int kPlanes>
+__device__ __forceinline__ void cut(const float (&v)[4], uint32_t (&p)[2][3]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    split3(v[2 * h], v[2 * h + 1], p[h]);
+    if constexpr (kPlanes == 2) {  // the second part rounded, and no third
+      const float h0 = __uint_as_float(p[h][0] << 16), h1 = __uint_as_float(p[h][0] & 0xffff0000u);
+      p[h][1] = pack_bf16(isinf(v[2 * h]) ? 0.0f : v[2 * h] - h0, isinf(v[2 * h + 1]) ? 0.0f : v[2 * h + 1] - h1);
+    }
+  }
+}
+// kOut outputs of four ranks to the four ranks of each output.
+template <int kOut>
+__device__ __forceinline__ void pair_ranks(const Run<kOut, uint16_t> (&d)[4], s16x4_t (&to)[kOut]) {
+#pragma unroll
+  for (int o = 0; o < kOut / 2; ++o) {
+    const uint32_t lo[2] = {__builtin_amdgcn_perm(d[1].w[o], d[0].w[o], 0x05040100u),
+                            __builtin_amdgcn_perm(d[3].w[o], d[2].w[o], 0x05040100u)};
+    const uint32_t hi[2] = {__builtin_amdgcn_perm(d[1].w[o], d[0].w[o], 0x07060302u),
+                            __builtin_amdgcn_perm(d[3].w[o], d[2].w[o], 0x07060302u)};
+    __builtin_memcpy(&to[2 * o], lo, 8);
+    __builtin_memcpy(&to[2 * o + 1], hi, 8);
+  }
+}
+
 template <typename TW, typename TY>
 constexpr int out_planes = sizeof(TW) == 4 ? 0 : sizeof(TY) == 2 ? 2 : 3;
 
@@ -451,7 +488,7 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
   __shared__ int of[kOutRows];
   const int64_t tile = block_id() / col_tiles, ct = block_id() - tile * col_tiles, t0 = tile * row_tile;
   if (t0 >= a.rows) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, j16 = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, j16 = lane & 15, q = lane >> 4;
   const int64_t rank = a.rank, t1 = min(t0 + row_tile, a.rows);
   // The lane's outputs.  At the end of a row they are moved back, so that all of
   // them can be loaded, and the `skip` first belong to another lane.
@@ -488,14 +525,7 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
       *reinterpret_cast<float4*>(lds + (t * kPitch + r) * 4) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
       uint32_t p[2][3];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        split3(v[2 * h], v[2 * h + 1], p[h]);
-        if constexpr (kPlanes == 2) {  // the second part rounded, and no third
-          const float h0 = __uint_as_float(p[h][0] << 16), h1 = __uint_as_float(p[h][0] & 0xffff0000u);
-          p[h][1] = pack_bf16(isinf(v[2 * h]) ? 0.0f : v[2 * h] - h0, isinf(v[2 * h + 1]) ? 0.0f : v[2 * h + 1] - h1);
-        }
-      }
+      cut<kPlanes>(v, p);
 #pragma unroll
       for (int i = 0; i < kPlanes; ++i)
         *reinterpret_cast<uint2*>(lds + ((i * row_tile + t) * kPitch + r) * 2) = make_uint2(p[0][i], p[1][i]);
@@ -530,15 +560,7 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
 #pragma unroll
           for (int o = 0; o < kOut; ++o) wf[i][c][o] = d[c].at(o);
       } else {
-#pragma unroll
-        for (int o = 0; o < kOut / 2; ++o) {
-          const uint32_t lo[2] = {__builtin_amdgcn_perm(d[1].w[o], d[0].w[o], 0x05040100u),
-                                  __builtin_amdgcn_perm(d[3].w[o], d[2].w[o], 0x05040100u)};
-          const uint32_t hi[2] = {__builtin_amdgcn_perm(d[1].w[o], d[0].w[o], 0x07060302u),
-                                  __builtin_amdgcn_perm(d[3].w[o], d[2].w[o], 0x07060302u)};
-          __builtin_memcpy(&wb[i][2 * o], lo, 8);
-          __builtin_memcpy(&wb[i][2 * o + 1], hi, 8);
-        }
+        pair_ranks<kOut>(d, wb[i]);
       }
     }
 #pragma unroll 1
@@ -597,6 +619,341 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
       for (int o = 0; o < kOut; ++o) out[o] = b[v].at(o);
       store_own<kOut>(y + (t0 + at) * a.ld_y + c0, skip, out);
     }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Into the rank for bf16 inputs and factors: the contraction goes in pieces of 64
+// elements, a piece of a row being one line of 128 bytes that eight lanes load.
+// (Operands straight from global memory take 64 bytes of 16 rows a load, at a
+// third of the rate: 201 MB of factors read by 128 workgroups 21 us, in lines
+// 6.5.)  The wave's own part of LDS turns lines into operands, without a barrier:
+// piece p of row r lies at p ^ (r / 2 % 8), where the 16 rows that are read
+// together meet all banks once.  kDeep pieces are in flight.
+// ---------------------------------------------------------------------------
+// Eight bf16 of a row from p on, the first n of them inside it.
+__device__ __forceinline__ uint4 load_piece(const uint16_t* p, int64_t n) {
+  if (n >= 8) return load_u128(p);
+  Frag<true> f;
+  load_frag(p, n, f);
+  return f.v;
+}
+
+constexpr int line_lds(int r16, int sub) { return (r16 + sub) * 16 * 128; }  // bytes a wave
+
+// The sums of a wave over the pieces at k_first, k_first + k_step, .. for the
+// rows t0 .. + 16 kSub - 1, adapter by adapter: done(g, acc), in which lanes hold
+// the ranks 16 i + 4 q .. + 3 of the row 16 h + j16 (rows of other adapters hold
+// what this adapter would give them).  Fills `of`; the whole workgroup calls it.
+template <int kR16, int kSub, int kDeep, typename F>
+__device__ __forceinline__ void into_rank(const LoraArgs& a, int64_t t0, int64_t k_first, int64_t k_step, char* wave_lds,
+                                          int (&of)[16 * kSub], F&& done) {
+  const int lane = threadIdx.x & 63, j16 = lane & 15, q = lane >> 4;
+  const int l8 = lane >> 3, p8 = lane & 7;  // loading: the row of eight and its piece of 16 bytes
+  const uint16_t* const xt = static_cast<const uint16_t*>(a.x) + t0 * a.ld_x;
+  uint32_t x_at[2 * kSub], w_at[2 * kR16];  // bytes
+#pragma unroll
+  for (int i = 0; i < 2 * kSub; ++i) x_at[i] = ((uint32_t)(min((int64_t)(8 * i + l8), a.rows - 1 - t0) * a.ld_x) + 8 * p8) * 2;
+#pragma unroll
+  for (int i = 0; i < 2 * kR16; ++i) w_at[i] = ((uint32_t)(min((int64_t)(8 * i + l8), a.rank - 1) * a.c_x) + 8 * p8) * 2;
+  struct Piece {
+    uint4 x[2 * kSub], w[2 * kR16];
+  } f[kDeep];
+  const auto load_x = [&](Piece& to, int64_t k) {
+    if (k + 64 <= a.c_x) {
+#pragma unroll
+      for (int i = 0; i < 2 * kSub; ++i) to.x[i] = load_u128(at_byte(xt + k, x_at[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * kSub; ++i) to.x[i] = load_piece(at_byte(xt + k, x_at[i]), a.c_x - k - 8 * p8);
+    }
+  };
+  // rows 8 i + l8 go in, operands (row j16 of 16, pieces q and 4 + q) come out
+  const uint32_t to_even = l8 * 128 + ((p8 ^ (l8 >> 1)) << 4), to_odd = l8 * 128 + ((p8 ^ ((l8 >> 1) + 4)) << 4);
+  const uint32_t from0 = j16 * 128 + ((q ^ (j16 >> 1)) << 4), from1 = j16 * 128 + (((q + 4) ^ (j16 >> 1)) << 4);
+  static_for<kDeep>([&](auto d) {  // before it is known whose rows they are
+    if (k_first + d * k_step < a.c_x) load_x(f[d], k_first + d * k_step);
+  });
+  tile_adapters<16 * kSub>(a.seg, t0, a.rows, of);
+  const int mine = of[lane % (16 * kSub)];
+  unsigned long long left = __ballot(mine >= 0);
+  bool again = false;
+  while (left) {  // the same for the whole workgroup
+    const int g = __builtin_amdgcn_readlane(mine, __ffsll(left) - 1);
+    left &= ~__ballot(mine == g);
+    const uint16_t* const wt = static_cast<const uint16_t*>(a.in) + (int64_t)g * a.rank * a.c_x;
+    const auto load_w = [&](Piece& to, int64_t k) {
+      if (k + 64 <= a.c_x) {
+#pragma unroll
+        for (int i = 0; i < 2 * kR16; ++i) to.w[i] = load_u128(at_byte(wt + k, w_at[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * kR16; ++i) to.w[i] = load_piece(at_byte(wt + k, w_at[i]), a.c_x - k - 8 * p8);
+      }
+    };
+    f32x4_t acc[kR16][kSub];
+#pragma unroll
+    for (int i = 0; i < kR16; ++i)
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) acc[i][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    static_for<kDeep>([&](auto d) {
+      const int64_t k = k_first + d * k_step;
+      if (k >= a.c_x) return;
+      if (again) load_x(f[d], k);
+      load_w(f[d], k);
+    });
+    again = true;
+#pragma unroll 1
+    for (int64_t k0 = k_first; k0 < a.c_x; k0 += kDeep * k_step) {
+      static_for<kDeep>([&](auto d) {
+        const int64_t k = k0 + d * k_step;
+        if (k >= a.c_x) return;
+#pragma unroll
+        for (int i = 0; i < 2 * kSub; ++i)
+          *reinterpret_cast<uint4*>(wave_lds + i * 1024 + (i & 1 ? to_odd : to_even)) = f[d].x[i];
+#pragma unroll
+        for (int i = 0; i < 2 * kR16; ++i)
+          *reinterpret_cast<uint4*>(wave_lds + (2 * kSub + i) * 1024 + (i & 1 ? to_odd : to_even)) = f[d].w[i];
+        if (k + kDeep * k_step < a.c_x) {
+          load_x(f[d], k + kDeep * k_step);
+          load_w(f[d], k + kDeep * k_step);
+        }
+        // a wave's own accesses to LDS are served in order; the fences keep the compiler to it
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          bf16x8_t x[kSub];
+#pragma unroll
+          for (int h = 0; h < kSub; ++h)
+            x[h] = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(wave_lds + h * 2048 + (u ? from1 : from0)));
+#pragma unroll
+          for (int i = 0; i < kR16; ++i) {
+            const bf16x8_t w =
+                __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const uint4*>(wave_lds + (kSub + i) * 2048 + (u ? from1 : from0)));
+#pragma unroll
+            for (int h = 0; h < kSub; ++h) acc[i][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[h], acc[i][h], 0, 0, 0);
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      });
+    }
+    done(g, acc);
+  }
+}
+
+// A workgroup takes 32 rows and a share of the pieces, its waves taking them in
+// turn.
+template <int kR16>
+struct LineShape {
+  static constexpr int kSub = 2, kRows = 16 * kSub, kWaves = kR16 <= 4 ? 8 : 4;
+  static constexpr int kDeep = kR16 == 1 ? 4 : kR16 <= 4 ? 2 : 1;
+};
+template <int kR16>
+__global__ __launch_bounds__((LineShape<kR16>::kWaves * 64)) void lora_line_in_kernel(LoraArgs a, int splits,
+                                                                                       float* __restrict__ part) {
+  using Shape = LineShape<kR16>;
+  constexpr int kSub = Shape::kSub, kRows = Shape::kRows, kWaves = Shape::kWaves;
+  constexpr int kLds = line_lds(kR16, kSub) * kWaves, kRed = kWaves * kRows * 16 * 4;
+  __shared__ __attribute__((aligned(16))) char lds[kLds > kRed ? kLds : kRed];
+  __shared__ int of[kRows];
+  const int64_t tile = block_id() / splits, split = block_id() - tile * splits, t0 = tile * kRows;
+  if (t0 >= a.rows) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, j16 = lane & 15, q = lane >> 4;
+  float* const dst = part + split * a.rows * a.rank;
+  into_rank<kR16, kSub, Shape::kDeep>(
+      a, t0, 64 * (split * kWaves + wave), (int64_t)64 * kWaves * splits, lds + wave * line_lds(kR16, kSub), of,
+      [&](int g, const f32x4_t (&acc)[kR16][kSub]) {
+        float* const red = reinterpret_cast<float*>(lds);  // [kWaves][kRows][16]
+#pragma unroll
+        for (int i = 0; i < kR16; ++i) {
+          __syncthreads();
+#pragma unroll
+          for (int h = 0; h < kSub; ++h)
+            *reinterpret_cast<f32x4_t*>(red + (wave * kRows + 16 * h + j16) * 16 + 4 * q) = acc[i][h];
+          __syncthreads();
+          for (int e = tid; e < kRows * 16; e += 64 * kWaves) {
+            const int t = e >> 4, r = e & 15;
+            if (of[t] == g && 16 * i + r < a.rank) {
+              float v = red[e];
+#pragma unroll
+              for (int u = 1; u < kWaves; ++u) v += red[u * kRows * 16 + e];
+              dst[(t0 + t) * a.rank + 16 * i + r] = v;
+            }
+          }
+        }
+        __syncthreads();
+      });
+  for (int e = tid; e < kRows * (int)a.rank; e += 64 * kWaves)
+    if (of[e / (int)a.rank] == -1) dst[t0 * a.rank + e] = 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Both ways in one launch, for bf16 inputs and factors, a rank up to 16 and many
+// rows: a workgroup of eight waves takes 16 rows through the whole contraction and
+// out to all outputs, so that s stays in LDS.  Some three launches of latency less
+// than the two kernels, but fewer bytes in flight on the way out: see both_ways.
+// ---------------------------------------------------------------------------
+constexpr int kBothWaves = 8;
+
+template <typename TY>
+__global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lora_both_kernel(LoraArgs a) {
+  constexpr int kR16 = 1, kSub = 1, kRows = 16, kOut = 4, kPlanes = out_planes<uint16_t, TY>;
+  constexpr int kPitch = 16 * kR16 + 8;  // elements of a row of a plane
+  __shared__ __attribute__((aligned(16))) char lds[kBothWaves * line_lds(kR16, kSub)];  // (the sums take a quarter of it)
+  __shared__ __attribute__((aligned(16))) uint16_t planes[kPlanes][kRows][kPitch];
+  __shared__ int of[kRows];
+  const int64_t t0 = block_id() * kRows;
+  if (t0 >= a.rows) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, j16 = lane & 15, q = lane >> 4;
+  const int64_t rank = a.rank, t1 = min(t0 + kRows, a.rows);
+  into_rank<kR16, kSub, 2>(a, t0, 64 * wave, 64 * kBothWaves, lds + wave * line_lds(kR16, kSub), of,
+                           [&](int g, const f32x4_t (&acc)[kR16][kSub]) {
+                             float* const red = reinterpret_cast<float*>(lds);  // [kBothWaves][kRows][16]
+                             __syncthreads();
+                             *reinterpret_cast<f32x4_t*>(red + (wave * kRows + j16) * 16 + 4 * q) = acc[0][0];
+                             __syncthreads();
+                             const int t = tid >> 2, r = 4 * (tid & 3);
+                             if (tid < 4 * kRows && of[t] == g) {
+                               float v[4] = {};
+#pragma unroll
+                               for (int u = 0; u < kBothWaves; ++u) {
+                                 const f32x4_t p = *reinterpret_cast<const f32x4_t*>(red + (u * kRows + t) * 16 + r);
+#pragma unroll
+                                 for (int i = 0; i < 4; ++i) v[i] += p[i];
+                               }
+#pragma unroll
+                               for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.0f;
+                               if (a.s && r < rank) store_run<4>(a.s + (t0 + t) * rank + r, rank - r, v);
+                               uint32_t p[2][3];
+                               cut<kPlanes>(v, p);
+#pragma unroll
+                               for (int i = 0; i < kPlanes; ++i)
+                                 *reinterpret_cast<uint2*>(&planes[i][t][r]) = make_uint2(p[0][i], p[1][i]);
+                             }
+                             __syncthreads();
+                           });
+  const int mine = of[j16];
+  const unsigned long long all = __ballot(mine >= 0) & 0xffffull, bare = __ballot(mine == -1) & 0xffffull;
+  unsigned long long left = all;
+  for (int e = tid; a.s && bare && e < kRows * (int)rank; e += 64 * kBothWaves)
+    if (of[e / (int)rank] == -1) a.s[t0 * rank + e] = 0.0f;
+
+  // out of the rank: a wave takes 16 kOut outputs in turn, a lane kOut
+  const TY* const base = static_cast<const TY*>(a.base);
+  TY* const y = static_cast<TY*>(a.y);
+  Run<kOut, TY> b[kSub][4], b_next[kSub][4];
+  Run<kOut, uint16_t> w_next[kR16][4];
+  // uniform addresses and bytes of the lane's own: its outputs of the rows 16 h + 4 q + v and of the ranks 16 i + 4 q + c
+  uint32_t b_at[kSub][4], y_at[kSub][4], f_at[kR16][4];
+#pragma unroll
+  for (int h = 0; h < kSub; ++h)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const uint32_t t = (uint32_t)min((int64_t)(16 * h + 4 * q + v), t1 - t0 - 1);
+      b_at[h][v] = (t * (uint32_t)a.ld_base + kOut * j16) * sizeof(TY);
+      y_at[h][v] = (t * (uint32_t)a.ld_y + kOut * j16) * sizeof(TY);
+    }
+#pragma unroll
+  for (int i = 0; i < kR16; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) f_at[i][c] = (min((uint32_t)(16 * i + 4 * q + c), (uint32_t)rank - 1) * (uint32_t)a.c_y + kOut * j16) * 2;
+  // At the end of a row a lane's outputs are moved back, so that all of them can
+  // be loaded, and the first ones belong to another lane.
+  const auto past = [&](int c_wave) { return max(c_wave + kOut * j16 + kOut - (int)a.c_y, 0); };
+  const TY* const base_t = base ? base + t0 * a.ld_base : nullptr;
+  const auto load_base = [&](int c_wave, Run<kOut, TY> (&to)[kSub][4]) {
+    const uint32_t c = (c_wave - past(c_wave)) * (int)sizeof(TY);
+#pragma unroll
+    for (int h = 0; h < kSub; ++h)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (base) __builtin_memcpy(to[h][v].w, at_byte(base_t, b_at[h][v] + c), sizeof to[h][v].w);
+        else to[h][v] = Run<kOut, TY>{};
+      }
+  };
+  const int c_first = wave * 16 * kOut, c_step = 16 * kOut * kBothWaves, c_end = (int)a.c_y;
+  left = all;
+  while (left) {
+    const int g = __builtin_amdgcn_readlane(mine, __ffsll(left) - 1);
+    const unsigned long long rows = __ballot(mine == g);
+    left &= ~rows;
+    const float scale = a.scale ? a.scale[g] : 1.0f;
+    const uint16_t* const wt = static_cast<const uint16_t*>(a.out) + (int64_t)g * rank * a.c_y;
+    const auto load_w = [&](int c_wave) {
+      const uint32_t at = (c_wave - past(c_wave)) * 2;
+#pragma unroll
+      for (int i = 0; i < kR16; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) __builtin_memcpy(w_next[i][c].w, at_byte(wt, f_at[i][c] + at), sizeof w_next[i][c].w);
+    };
+    if (c_first < c_end) {
+      load_w(c_first);
+      load_base(c_first, b_next);
+    }
+#pragma unroll 1
+    for (int c_wave = c_first; c_wave < c_end; c_wave += c_step) {
+      s16x4_t wb[kR16][kOut];
+#pragma unroll
+      for (int i = 0; i < kR16; ++i) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int o = 0; o < kOut / 2; ++o) w_next[i][c].w[o] = 16 * i + 4 * q + c < rank ? w_next[i][c].w[o] : 0u;
+        pair_ranks<kOut>(w_next[i], wb[i]);
+      }
+#pragma unroll
+      for (int h = 0; h < kSub; ++h)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) b[h][v] = b_next[h][v];
+      if (c_wave + c_step < c_end) {
+        load_w(c_wave + c_step);
+        load_base(c_wave + c_step, b_next);
+      }
+      const int skip = min(past(c_wave), kOut);
+      TY* const y_t = y + t0 * a.ld_y;
+      const uint32_t y_c = (c_wave - past(c_wave)) * (int)sizeof(TY);
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) {
+        if (((rows >> (16 * h)) & 0xffffull) == 0) continue;
+        f32x4_t acc[kOut];
+#pragma unroll
+        for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kR16; ++i)
+#pragma unroll
+          for (int p = kPlanes - 1; p >= 0; --p) {  // the smallest part first
+            const s16x4_t sv = *reinterpret_cast<const s16x4_t*>(&planes[p][16 * h + j16][16 * i + 4 * q]);
+#pragma unroll
+            for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(sv, wb[i][o], acc[o], 0, 0, 0);
+          }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (((rows >> (16 * h + 4 * q + v)) & 1) == 0) continue;
+          float out[kOut];
+#pragma unroll
+          for (int o = 0; o < kOut; ++o) out[o] = __builtin_fmaf(scale, acc[o][v], b[h][v].at(o));
+          store_own<kOut>(at_byte(y_t, y_at[h][v] + y_c), skip, out);
+        }
+      }
+    }
+  }
+  // rows without an adapter
+  if (bare == 0 || a.base == a.y) return;
+#pragma unroll 1
+  for (int c_wave = c_first; c_wave < c_end; c_wave += c_step) {
+    const int skip = min(past(c_wave), kOut);
+    const uint32_t y_c = (c_wave - past(c_wave)) * (int)sizeof(TY);
+    load_base(c_wave, b);
+#pragma unroll
+    for (int h = 0; h < kSub; ++h)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (((bare >> (16 * h + 4 * q + v)) & 1) == 0) continue;
+        float out[kOut];
+#pragma unroll
+        for (int o = 0; o < kOut; ++o) out[o] = b[h][v].at(o);
+        store_own<kOut>(at_byte(y + t0 * a.ld_y, y_at[h][v] + y_c), skip, out);
+      }
   }
 }
 
@@ -840,7 +1197,7 @@ __global__ __launch_bounds__(kThreads) void lora_weight_kernel(LoraWeightArgs a,
   __shared__ int list[kMostChunk];
   __shared__ __attribute__((aligned(16))) float red[kThreads / 64][16][16 * kOut];
   const int64_t want = block_id() / col_tiles, ct = block_id() - want * col_tiles;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, j16 = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, j16 = lane & 15, q = lane >> 4;
   count_rows(a.seg, a.rows, cnt);
   Slot s;
   if (!find_slot<false>(cnt, a.seg.n_adapters, chunk, want, s)) return;  // the whole workgroup
@@ -919,24 +1276,21 @@ hipError_t by_type(int dtype, F&& f) {
 
 namespace {
 
-// How the work is split, from sizes alone.
+// How the work is split, from sizes alone (the types change the tile, so that the
+// same shares may be of another length).
 struct LoraPlan {
-  bool rows;        // the row kernels
-  int splits;       // workgroups along the contraction
-  int64_t k_wave;   // tile kernels: elements of the contraction a wave takes
+  bool rows;   // the row kernels
+  int splits;  // workgroups along the contraction
 };
+constexpr int64_t kFar = int64_t(1) << 21;  // elements of a row with which a tile's byte offsets stay below 2^31
 LoraPlan lora_plan(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y) {
-  LoraPlan p{rows < 16 || rows < 4 * segments || c_y < 8, 1, 0};
+  LoraPlan p{rows < 16 || rows < 4 * segments || c_y < 8 || c_x >= kFar, 1};
   if (p.rows) return p;
-  const int64_t tiles = (rows + kInRows - 1) / kInRows, steps = (c_x + 31) / 32;
-  int64_t splits = (2048 / 4 + tiles - 1) / tiles;         // some eight waves a CU
-  const int64_t most = (steps + 15) / 16;                  // and four steps a wave at least
+  const int64_t tiles = (rows + 31) / 32, steps = (c_x + 31) / 32;
+  int64_t splits = (512 + tiles - 1) / tiles;  // some two workgroups a CU
+  const int64_t most = steps / 16;             // and 512 elements each at least
   splits = splits < most ? splits : most;
-  splits = splits < 1 ? 1 : splits > 16 ? 16 : splits;
-  const int64_t per = (steps + 4 * splits - 1) / (4 * splits);
-  p.k_wave = 32 * (per > 0 ? per : 1);
-  p.splits = (int)((c_x + 4 * p.k_wave - 1) / (4 * p.k_wave));
-  if (p.splits < 1) p.splits = 1;
+  p.splits = splits < 1 ? 1 : splits > 16 ? 16 : (int)splits;
   return p;
 }
 
@@ -972,13 +1326,20 @@ hipError_t launch_rows(const LoraArgs& a, float* s, hipStream_t stream) {
   });
 }
 
-hipError_t launch_tiles(const LoraArgs& a, const LoraPlan& p, float* part, hipStream_t stream) {
-  const int64_t tiles = (a.rows + kInRows - 1) / kInRows;
+hipError_t launch_tiles(const LoraArgs& a, int splits, float* part, hipStream_t stream) {
   const hipError_t e = by_type(a.x_dtype, [&](auto x) {
     return by_type(a.w_dtype, [&](auto w) {
       return by_rank(a.rank, [&](auto r) {
-        lora_tile_in_kernel<decltype(x), decltype(w), r><<<grid_of(tiles * p.splits), dim3(kThreads), 0, stream>>>(
-            a, p.splits, p.k_wave, part);
+        using TX = decltype(x);
+        using TW = decltype(w);
+        const dim3 grid = grid_of((a.rows + kInRows - 1) / kInRows * splits);
+        if constexpr (sizeof(TX) == 2 && sizeof(TW) == 2) {
+          static_assert(LineShape<r>::kRows == kInRows);
+          lora_line_in_kernel<r><<<grid, dim3(64 * LineShape<r>::kWaves), 0, stream>>>(a, splits, part);
+        } else {
+          const int64_t waves = (int64_t)kInWaves * splits, k_wave = ((a.c_x + 31) / 32 + waves - 1) / waves * 32;
+          lora_tile_in_kernel<TX, TW, r><<<grid, dim3(64 * kInWaves), 0, stream>>>(a, splits, k_wave, part);
+        }
         return hipGetLastError();
       });
     });
@@ -999,10 +1360,26 @@ hipError_t launch_tiles(const LoraArgs& a, const LoraPlan& p, float* part, hipSt
           row_tile /= 2;
         const size_t lds = row_tile * kRowBytes;
         lora_tile_out_kernel<TW, TY, r><<<grid_of((a.rows + row_tile - 1) / row_tile * col_tiles), dim3(kThreads), lds,
-                                          stream>>>(a, part, p.splits, row_tile, col_tiles);
+                                          stream>>>(a, part, splits, row_tile, col_tiles);
         return hipGetLastError();
       });
     });
+  });
+}
+
+// Whether one launch does it: for many rows, unless most of the work is the way
+// out (8192 rows, rank 16, 4096 -> 4096: 47 us, two launches 59; 12288 -> 4096: 73
+// and 86; 4096 -> 12288: 107 and 101; 32768 rows, 2048 -> 1024: 63 and 71; larger
+// ranks leave room for one workgroup a CU, 32768 rows of rank 32: 88 and 75).
+bool both_ways(const LoraArgs& a) {
+  return a.x_dtype == 1 && a.w_dtype == 1 && a.rank <= 16 && a.rows >= 2048 && a.c_y <= 2 * a.c_x && a.ld_base < kFar &&
+         a.ld_y < kFar && a.c_y < kFar;
+}
+
+hipError_t launch_both(const LoraArgs& a, hipStream_t stream) {
+  return by_type(a.y_dtype, [&](auto y) {
+    lora_both_kernel<decltype(y)><<<grid_of((a.rows + 15) / 16), dim3(64 * kBothWaves), 0, stream>>>(a);
+    return hipGetLastError();
   });
 }
 
@@ -1015,8 +1392,14 @@ size_t lora_ws_bytes(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, i
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
   const LoraPlan p = lora_plan(a.rows, a.seg.n, a.c_x, a.c_y);
   float* ws = static_cast<float*>(a.ws);
-  if (p.rows || a.rank == 0) return launch_rows(a, a.s ? a.s : ws, stream);
-  return launch_tiles(a, p, p.splits == 1 && a.s ? a.s : ws, stream);
+  if (p.rows || a.rank == 0 || a.ld_x >= kFar) return launch_rows(a, a.s ? a.s : ws, stream);
+  if (both_ways(a)) return launch_both(a, stream);
+  int splits = p.splits;
+  if (a.x_dtype == 1 && a.w_dtype == 1) {  // workgroups of eight waves, one a CU
+    const int64_t tiles = (a.rows + kInRows - 1) / kInRows, most = (256 + tiles - 1) / tiles;
+    splits = splits < most ? splits : (int)most;
+  }
+  return launch_tiles(a, splits, splits == 1 && a.s ? a.s : ws, stream);
 }
 
 namespace {

@@ -746,10 +746,10 @@ __device__ __forceinline__ void into_rank(const LoraArgs& a, int64_t t0, int64_t
 template <int kR16>
 struct LineShape {
   static constexpr int kSub = 2, kRows = 16 * kSub, kWaves = kR16 <= 4 ? 8 : 4;
-  static constexpr int kDeep = kR16 == 1 ? 4 : kR16 <= 4 ? 2 : 1;
+  static constexpr int kDeep = kR16 == 1 || kR16 == 4 ? 2 : 1;
 };
 template <int kR16>
-__global__ __launch_bounds__((LineShape<kR16>::kWaves * 64)) void lora_line_in_kernel(LoraArgs a, int splits,
+__global__ __launch_bounds__((LineShape<kR16>::kWaves * 64), (kR16 <= 2 ? 4 : kR16 <= 4 ? 2 : 1)) void lora_line_in_kernel(LoraArgs a, int splits,
                                                                                        float* __restrict__ part) {
   using Shape = LineShape<kR16>;
   constexpr int kSub = Shape::kSub, kRows = Shape::kRows, kWaves = Shape::kWaves;
@@ -1395,8 +1395,8 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
   if (p.rows || a.rank == 0 || a.ld_x >= kFar) return launch_rows(a, a.s ? a.s : ws, stream);
   if (both_ways(a)) return launch_both(a, stream);
   int splits = p.splits;
-  if (a.x_dtype == 1 && a.w_dtype == 1) {  // workgroups of eight waves, one a CU
-    const int64_t tiles = (a.rows + kInRows - 1) / kInRows, most = (256 + tiles - 1) / tiles;
+  if (a.x_dtype == 1 && a.w_dtype == 1) {  // workgroups of eight waves, two a CU or one
+    const int64_t tiles = (a.rows + kInRows - 1) / kInRows, most = ((a.rank <= 32 ? 512 : 256) + tiles - 1) / tiles;
     splits = splits < most ? splits : (int)most;
   }
   return launch_tiles(a, splits, splits == 1 && a.s ? a.s : ws, stream);

@@ -975,11 +975,11 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
 struct Slot {
   int g;
   int64_t row0, row1;  // of the adapter's rows
-  int64_t slots;       // the adapter's
-  int64_t part;        // the adapter's first place among the parts
+  int slots;           // the adapter's
+  int part;            // the adapter's first place among the parts
 };
 
-// cnt[g] = rows of adapter g, by the whole workgroup.
+// The rows of segment i, clamped into the buffer.
 __device__ __forceinline__ void segment_rows(const SegmentArgs& g, int64_t n_rows, int64_t i, int64_t& lo, int64_t& hi) {
   if (g.offsets) {
     lo = min(max(g.offsets[i], (int64_t)0), n_rows);
@@ -990,47 +990,64 @@ __device__ __forceinline__ void segment_rows(const SegmentArgs& g, int64_t n_row
   }
   hi = max(lo, hi);
 }
-__device__ __forceinline__ void count_rows(const SegmentArgs& g, int64_t n_rows, unsigned long long* cnt) {
-  for (int i = threadIdx.x; i < (int)g.n_adapters; i += kThreads) cnt[i] = 0;
+
+// The first segments as the workgroup has read them, for list_rows.
+constexpr int kKnown = 256;
+struct Segments {
+  unsigned long long cnt[kLoraMaxAdapters];
+  int lo[kKnown], len[kKnown], id[kKnown];
+};
+// cnt[g] = rows of adapter g, by the whole workgroup.
+__device__ __forceinline__ void count_rows(const SegmentArgs& g, int64_t n_rows, Segments& s) {
+  const int tid = threadIdx.x;
+  int64_t lo = 0, hi = 0, id = -1;
+  if (tid < g.n) {  // loaded while the counters are cleared
+    segment_rows(g, n_rows, tid, lo, hi);
+    id = adapter_of(g, tid);
+  }
+  for (int i = tid; i < (int)g.n_adapters; i += kThreads) s.cnt[i] = 0;
   __syncthreads();
-  for (int64_t i = threadIdx.x; i < g.n; i += kThreads) {
-    const int64_t id = adapter_of(g, i);
-    int64_t lo, hi;
+  s.lo[tid] = (int)lo;
+  s.len[tid] = (int)(hi - lo);
+  s.id[tid] = (int)id;
+  if (id >= 0 && hi > lo) atomicAdd(&s.cnt[id], (unsigned long long)(hi - lo));
+  for (int64_t i = tid + kThreads; i < g.n; i += kThreads) {
+    id = adapter_of(g, i);
     segment_rows(g, n_rows, i, lo, hi);
-    if (id >= 0 && hi > lo) atomicAdd(&cnt[id], (unsigned long long)(hi - lo));
+    if (id >= 0 && hi > lo) atomicAdd(&s.cnt[id], (unsigned long long)(hi - lo));
   }
   __syncthreads();
 }
+static_assert(kKnown == kThreads);
 // The slot `want` (kByAdapter: the first slot of adapter `want`), every wave for itself.
 template <bool kByAdapter>
-__device__ __forceinline__ bool find_slot(const unsigned long long* cnt, int64_t n_adapters, int64_t chunk, int64_t want,
-                                          Slot& s) {
+__device__ __forceinline__ bool find_slot(const unsigned long long* cnt, int n_adapters, int chunk, int64_t want, Slot& s) {
   const int lane = threadIdx.x & 63;
   int64_t before = 0, parts = 0;
-  for (int64_t g0 = 0; g0 < n_adapters; g0 += 64) {
+  for (int g0 = 0; g0 < n_adapters; g0 += 64) {
     const bool in = g0 + lane < n_adapters;
-    const int64_t rows = in ? (int64_t)cnt[g0 + lane] : 0;
-    const int64_t slots = in ? max((int64_t)1, (rows + chunk - 1) / chunk) : 0;
-    int64_t incl = slots, pin = slots > 1 ? slots : 0;
+    const unsigned long long rows = in ? cnt[g0 + lane] : 0;
+    // (overlapping segments can claim more rows than there are: no more slots than the buffer has)
+    const int slots = in ? max(1, (int)min((rows + chunk - 1) / (unsigned)chunk, 1ull << 20)) : 0;
+    int incl = slots, pin = slots > 1 ? slots : 0;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int64_t u = __shfl_up(incl, off), v = __shfl_up(pin, off);
+      const int u = __shfl_up(incl, off), v = __shfl_up(pin, off);
       if (lane >= off) incl += u, pin += v;
     }
     const unsigned long long hit = kByAdapter ? __ballot(g0 + lane == want) : __ballot(before + incl > want);
     if (hit) {
       const int l = __ffsll(hit) - 1;
-      const int64_t k = kByAdapter ? 0 : want - uniform(before + __shfl(incl - slots, l));
-      const int64_t all = uniform(__shfl(rows, l));
-      s.g = (int)(g0 + l);
-      s.slots = uniform(__shfl(slots, l));
-      s.part = parts + uniform(__shfl(pin, l)) - (s.slots > 1 ? s.slots : 0);
+      s.g = g0 + l;
+      s.slots = __builtin_amdgcn_readlane(slots, l);
+      s.part = (int)parts + __builtin_amdgcn_readlane(pin, l) - (s.slots > 1 ? s.slots : 0);
+      const int64_t k = kByAdapter ? 0 : want - before - (__builtin_amdgcn_readlane(incl, l) - s.slots);
       s.row0 = k * chunk;
-      s.row1 = min(s.row0 + chunk, all);
+      s.row1 = min(s.row0 + chunk, uniform((int64_t)cnt[s.g]));
       return true;
     }
-    before += uniform(__shfl(incl, 63));
-    parts += uniform(__shfl(pin, 63));
+    before += __builtin_amdgcn_readlane(incl, 63);
+    parts += __builtin_amdgcn_readlane(pin, 63);
   }
   return false;
 }
@@ -1039,17 +1056,24 @@ constexpr int kMostChunk = 2048;  // rows of a slot, which are listed in LDS
 
 // list[0 .. row1 - row0): the buffer's rows, by the whole workgroup; the caller
 // waits before it reads them.
-__device__ __forceinline__ void list_rows(const SegmentArgs& g, int64_t n_rows, const Slot& s, int* list) {
+__device__ __forceinline__ void list_rows(const SegmentArgs& g, int64_t n_rows, const Segments& known, const Slot& s,
+                                          int* list) {
   const int tid = threadIdx.x, lane = tid & 63;
   int64_t at = 0;  // the adapter's rows before this group of segments
   for (int64_t i0 = 0; i0 < g.n && at < s.row1; i0 += 64) {
     int64_t lo = 0, hi = 0;
-    if (i0 + lane < g.n && adapter_of(g, i0 + lane) == s.g) segment_rows(g, n_rows, i0 + lane, lo, hi);
+    const int64_t i = i0 + lane;
+    if (i0 < kKnown) {
+      lo = known.lo[i];
+      hi = known.id[i] == s.g ? lo + known.len[i] : lo;
+    } else if (i < g.n && adapter_of(g, i) == s.g) {
+      segment_rows(g, n_rows, i, lo, hi);
+    }
     const int64_t len = hi - lo;
-    int64_t incl = len;
+    uint32_t incl = (uint32_t)len;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const int64_t u = __shfl_up(incl, off);
+      const uint32_t u = (uint32_t)__shfl_up((int)incl, off);
       if (lane >= off) incl += u;
     }
     const int64_t first = at + incl - len;
@@ -1063,94 +1087,103 @@ __device__ __forceinline__ void list_rows(const SegmentArgs& g, int64_t n_rows, 
       const int64_t a0 = __shfl(f0, l), a1 = __shfl(f1, l), from = __shfl(lo - first, l);
       for (int64_t f = a0 + tid; f < a1; f += kThreads) list[f - s.row0] = (int)(from + f);
     }
-    at += uniform(__shfl(incl, 63));
+    at += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
   }
 }
 
-// kOut consecutive columns of one row, the first n of them inside it: bf16 pairs (dtypes 1, 2) or fp32.
+// kOut consecutive columns of one row, the first n of them inside it (kWhole: all
+// are): bf16 pairs (dtypes 1, 2) or fp32.  Checkpoints come as their bytes, and
+// their scale beside them.
 template <int kDtype, int kOut>
 struct Cols {
-  uint32_t w[kDtype == 0 ? kOut : kOut / 2];
+  uint32_t w[kDtype == 0 ? kOut : kDtype == 1 ? kOut / 2 : (kOut + 3) / 4];
+  uint32_t scale;
 };
 template <int kDtype, int kOut, bool kWhole>
-__device__ __forceinline__ Cols<kDtype, kOut> load_cols(const LoraFactor& f, int64_t row, int64_t c, int64_t n) {
-  Cols<kDtype, kOut> r;
-  if constexpr (kDtype == 2) {
-    uint8_t b[kOut];
-    const uint8_t* p = static_cast<const uint8_t*>(f.x) + row * f.cols + c;
-    if (kWhole || n >= kOut) {
-      __builtin_memcpy(b, p, sizeof b);
-    } else {
-#pragma unroll
-      for (int o = 0; o < kOut; ++o) b[o] = o < n ? p[o] : 0;
-    }
-    const float up = kWhole || n > 0 ? e8m0_to_f32(f.x_scale[row * ((f.cols + 31) / 32) + c / 32]) : 1.0f;
-    static_for<kOut / 2>([&](auto o) {
-      const uint32_t two = (uint32_t)b[2 * o] | (uint32_t)b[2 * o + 1] << 8;
-      r.w[o] = pack_bf16(e4m3_to_f32<0>(two) * up, e4m3_to_f32<1>(two) * up);
-    });
+__device__ __forceinline__ void load_cols(const LoraFactor& f, int64_t row, int64_t c, int64_t n, Cols<kDtype, kOut>& r) {
+  using T = std::conditional_t<kDtype == 0, float, std::conditional_t<kDtype == 1, uint16_t, uint8_t>>;
+  const T* p = static_cast<const T*>(f.x) + row * (kDtype == 2 ? f.cols : f.ld) + c;
+  if constexpr (kDtype == 2) r.scale = kWhole || n > 0 ? f.x_scale[row * ((f.cols + 31) / 32) + c / 32] : 127u;
+  if (kWhole || n >= kOut) {
+    __builtin_memcpy(r.w, p, kOut * sizeof(T));
   } else {
-    using T = std::conditional_t<kDtype == 0, float, uint16_t>;
-    const T* p = static_cast<const T*>(f.x) + row * f.ld + c;
-    if (kWhole || n >= kOut) {
-      __builtin_memcpy(r.w, p, sizeof r.w);
-    } else {
-      T raw[kOut];
+    constexpr int kPer = 4 / sizeof(T);
 #pragma unroll
-      for (int o = 0; o < kOut; ++o) raw[o] = o < n ? p[o] : T(0);
-      __builtin_memcpy(r.w, raw, sizeof r.w);
+    for (int i = 0; i < (int)(sizeof r.w / 4); ++i) {
+      r.w[i] = 0;
+#pragma unroll
+      for (int o = 0; o < kPer; ++o) {
+        T v = T(0);
+        if (kPer * i + o < n) v = p[kPer * i + o];
+        if constexpr (sizeof(T) == 4) r.w[i] = __float_as_uint(v);
+        else r.w[i] |= (uint32_t)v << (8 * (int)sizeof(T) * o);
+      }
     }
   }
-  return r;
+}
+// Pair o of them as bf16 (exact: E4M3 has 4 significant bits).
+template <int o, int kDtype, int kOut>
+__device__ __forceinline__ uint32_t pair_of(const Cols<kDtype, kOut>& r) {
+  if constexpr (kDtype == 1) {
+    return r.w[o];
+  } else {
+    const float up = e8m0_to_f32(r.scale);
+    return pack_bf16(e4m3_to_f32<(2 * o) % 4>(r.w[o / 2]) * up, e4m3_to_f32<(2 * o) % 4 + 1>(r.w[o / 2]) * up);
+  }
 }
 
-// Steps of 32 rows of the list, `steps` of them from row i on, every fourth.
-// kWhole: rows and columns all inside.
-template <int kDtype, int kR16, int kOut, bool kWhole>
-__device__ __forceinline__ void weight_step(const LoraFactor& f, int64_t rank, const int* list, int at, int count, int64_t c,
-                                            int64_t n, f32x4_t (&acc)[kR16][kOut]) {
-  const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
-  int row[8];
-  bool in[8];
+// A lane's share of a step of 32 rows of the list: the rows 8 q + j.  kWhole: rows
+// and columns are all inside; else those past `count` are zeros.
+template <int kDtype, int kR16, int kOut>
+struct Step {
   Cols<kDtype, kOut> x[8];
+  float p[kR16][8];
+};
+template <int kDtype, int kR16, int kOut, bool kWhole>
+__device__ __forceinline__ void load_step(const LoraFactor& f, int64_t rank, const int* list, int at, int count, int64_t c,
+                                          int64_t n, Step<kDtype, kR16, kOut>& s) {
+  const int r16 = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+  int row[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int i = at + 8 * q + j;
-    in[j] = kWhole || i < count;
-    row[j] = list[in[j] ? i : 0];
-    if (in[j]) x[j] = load_cols<kDtype, kOut, kWhole>(f, row[j], c, n);
-    else x[j] = Cols<kDtype, kOut>{};
+    row[j] = kWhole || i < count ? list[i] : -1;
+    if (kWhole || i < count) load_cols<kDtype, kOut, kWhole>(f, row[j], c, n, s.x[j]);
+    else s.x[j] = Cols<kDtype, kOut>{};
   }
+#pragma unroll
+  for (int i = 0; i < kR16; ++i) {
+    const int64_t r = min((int64_t)(16 * i + r16), rank - 1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s.p[i][j] = kWhole || row[j] >= 0 ? f.p[row[j] * rank + r] : 0.0f;
+  }
+}
+template <int kDtype, int kR16, int kOut>
+__device__ __forceinline__ void add_step(const Step<kDtype, kR16, kOut>& s, f32x4_t (&acc)[kR16][kOut]) {
+  const auto& p = s.p;
   if constexpr (kDtype == 0) {
 #pragma unroll
-    for (int i = 0; i < kR16; ++i) {
-      const int64_t r = min((int64_t)(16 * i + r16), rank - 1);
+    for (int i = 0; i < kR16; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float p = in[j] ? f.p[row[j] * rank + r] : 0.0f;
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int o = 0; o < kOut; ++o)
-          acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, __uint_as_float(x[j].w[o]), acc[i][o], 0, 0, 0);
-      }
-    }
+          acc[i][o] = __builtin_amdgcn_mfma_f32_16x16x4f32(p[i][j], __uint_as_float(s.x[j].w[o]), acc[i][o], 0, 0, 0);
   } else {
     uint32_t b[kOut][4];  // operands: rows 8 q + 2 j, + 1 of one column
+    static_for<kOut / 2>([&](auto o) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int o = 0; o < kOut / 2; ++o) {
-        b[2 * o][j] = __builtin_amdgcn_perm(x[2 * j + 1].w[o], x[2 * j].w[o], 0x05040100u);
-        b[2 * o + 1][j] = __builtin_amdgcn_perm(x[2 * j + 1].w[o], x[2 * j].w[o], 0x07060302u);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = pair_of<o>(s.x[2 * j]), hi = pair_of<o>(s.x[2 * j + 1]);
+        b[2 * o][j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+        b[2 * o + 1][j] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
       }
+    });
 #pragma unroll
     for (int i = 0; i < kR16; ++i) {
-      const int64_t r = min((int64_t)(16 * i + r16), rank - 1);
-      float p[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = in[j] ? f.p[row[j] * rank + r] : 0.0f;
       uint32_t a[4][3];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split3(p[2 * j], p[2 * j + 1], a[j]);
+      for (int j = 0; j < 4; ++j) split3(p[i][2 * j], p[i][2 * j + 1], a[j]);
 #pragma unroll
       for (int u = 2; u >= 0; --u) {  // the smallest part first
         const bf16x8_t fa = __builtin_bit_cast(bf16x8_t, make_uint4(a[0][u], a[1][u], a[2][u], a[3][u]));
@@ -1189,19 +1222,29 @@ __device__ __forceinline__ void finish(const LoraWeightArgs& a, const LoraFactor
   }
 }
 
-template <int kDtype, int kR16, int kOut>
-__global__ __launch_bounds__(kThreads) void lora_weight_kernel(LoraWeightArgs a, LoraFactor f, int64_t chunk,
-                                                               int64_t col_tiles, float* __restrict__ part,
-                                                               int64_t parts) {
-  __shared__ unsigned long long cnt[kLoraMaxAdapters];
-  __shared__ int list[kMostChunk];
-  __shared__ __attribute__((aligned(16))) float red[kThreads / 64][16][16 * kOut];
-  const int64_t want = block_id() / col_tiles, ct = block_id() - want * col_tiles;
+// Columns a lane takes, so that the sums of a wave take 128 registers at most.
+constexpr int weight_run(int r16, int dtype) { return r16 <= 2 ? (dtype == 0 ? 4 : 8) : r16 <= 8 ? 4 : 2; }
+
+template <int kOut>
+union WeightLds {  // the sums come last
+  struct {
+    Segments segments;
+    int list[kMostChunk];
+  };
+  float red[kThreads / 64 * 16 * 16 * kOut];
+};
+
+template <int kDtype, int kR16>
+__device__ __forceinline__ void weight_tile(const LoraWeightArgs& a, const LoraFactor& f, int64_t chunk, int64_t want,
+                                            int64_t ct, float* __restrict__ part, int64_t parts,
+                                            WeightLds<weight_run(kR16, kDtype)>& lds) {
+  constexpr int kOut = weight_run(kR16, kDtype);
+  float* const red = lds.red;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, j16 = lane & 15, q = lane >> 4;
-  count_rows(a.seg, a.rows, cnt);
+  count_rows(a.seg, a.rows, lds.segments);
   Slot s;
-  if (!find_slot<false>(cnt, a.seg.n_adapters, chunk, want, s)) return;  // the whole workgroup
-  list_rows(a.seg, a.rows, s, list);
+  if (!find_slot<false>(lds.segments.cnt, (int)a.seg.n_adapters, (int)chunk, want, s)) return;  // the whole workgroup
+  list_rows(a.seg, a.rows, lds.segments, s, lds.list);
   __syncthreads();
   const int count = (int)(s.row1 - s.row0);
   const int64_t c_tile = ct * 16 * kOut, c = c_tile + kOut * j16, n = f.cols - c;
@@ -1210,28 +1253,43 @@ __global__ __launch_bounds__(kThreads) void lora_weight_kernel(LoraWeightArgs a,
   for (int i = 0; i < kR16; ++i)
 #pragma unroll
     for (int o = 0; o < kOut; ++o) acc[i][o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const bool whole = c_tile + 16 * kOut <= f.cols;
   int at = 32 * wave;
-  if (whole)
-    for (; at + 32 <= count; at += 128) weight_step<kDtype, kR16, kOut, true>(f, a.rank, list, at, count, c, n, acc);
-  for (; at < count; at += 128) weight_step<kDtype, kR16, kOut, false>(f, a.rank, list, at, count, c, n, acc);
+  if (c_tile + 16 * kOut <= f.cols && at + 32 <= count) {  // the next step's loads are in flight while this one is added
+    Step<kDtype, kR16, kOut> s0, s1;
+    load_step<kDtype, kR16, kOut, true>(f, a.rank, lds.list, at, count, c, n, s0);
+#pragma unroll 1
+    for (;;) {
+      const bool more = at + 160 <= count;
+      if (more) load_step<kDtype, kR16, kOut, true>(f, a.rank, lds.list, at + 128, count, c, n, s1);
+      add_step(s0, acc);
+      at += 128;
+      if (!more) break;
+      s0 = s1;
+    }
+  }
+#pragma unroll 1
+  for (; at < count; at += 128) {
+    Step<kDtype, kR16, kOut> s0;
+    load_step<kDtype, kR16, kOut, false>(f, a.rank, lds.list, at, count, c, n, s0);
+    add_step(s0, acc);
+  }
   // the waves' sums, 16 ranks at a time; a thread has kOut columns of one rank
   const float scale = a.scale ? a.scale[s.g] : 1.0f;
   const int r = tid >> 4;
 #pragma unroll
   for (int i = 0; i < kR16; ++i) {
-    if (i > 0) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int v = 0; v < 4; ++v)
 #pragma unroll
-      for (int o = 0; o < kOut; ++o) red[wave][4 * q + v][kOut * j16 + o] = acc[i][o][v];
+      for (int o = 0; o < kOut; ++o) red[(wave * 16 + 4 * q + v) * 16 * kOut + kOut * j16 + o] = acc[i][o][v];
     __syncthreads();
     float sum[kOut];
 #pragma unroll
     for (int o = 0; o < kOut; ++o) {
-      sum[o] = red[0][r][kOut * j16 + o];
+      sum[o] = red[r * 16 * kOut + kOut * j16 + o];
 #pragma unroll
-      for (int w = 1; w < kThreads / 64; ++w) sum[o] += red[w][r][kOut * j16 + o];
+      for (int w = 1; w < kThreads / 64; ++w) sum[o] += red[(w * 16 + r) * 16 * kOut + kOut * j16 + o];
     }
     if (16 * i + r < a.rank && n > 0) {
       const int64_t k = s.slots > 1 ? s.part + s.row0 / chunk : s.g;
@@ -1243,26 +1301,53 @@ __global__ __launch_bounds__(kThreads) void lora_weight_kernel(LoraWeightArgs a,
   }
 }
 
+// Both factors' tiles, those of the first before those of the second; a factor
+// that is not asked for has none.
+struct WeightWork {
+  int64_t chunk, slots, parts;
+  int64_t tiles[2];  // of columns
+  float* part[2];
+};
+template <int kDx, int kDy, int kR16>
+__global__ __launch_bounds__(kThreads, (kR16 <= 4 ? 2 : 1)) void lora_weight_kernel(LoraWeightArgs a, WeightWork w) {
+  __shared__ __attribute__((aligned(16))) union Lds {
+    WeightLds<weight_run(kR16, kDx)> x;
+    WeightLds<weight_run(kR16, kDy)> y;
+  } lds;
+  int64_t b = block_id();
+  if (b < w.slots * w.tiles[0]) {
+    weight_tile<kDx, kR16>(a, a.f[0], w.chunk, b / w.tiles[0], b % w.tiles[0], w.part[0], w.parts, lds.x);
+    return;
+  }
+  b -= w.slots * w.tiles[0];
+  if (w.tiles[1] == 0) return;
+  weight_tile<kDy, kR16>(a, a.f[1], w.chunk, b / w.tiles[1], b % w.tiles[1], w.part[1], w.parts, lds.y);
+}
+
 // The sums of an adapter's slots, if it has several.
 constexpr int kSumRun = 4;
-__global__ __launch_bounds__(kThreads) void lora_weight_sum_kernel(LoraWeightArgs a, LoraFactor f, int64_t chunk,
-                                                                   int64_t spans, const float* __restrict__ part,
-                                                                   int64_t parts) {
-  __shared__ unsigned long long cnt[kLoraMaxAdapters];
-  const int64_t g = block_id() / spans, span = block_id() - g * spans;
+__global__ __launch_bounds__(kThreads) void lora_weight_sum_kernel(LoraWeightArgs a, WeightWork w, int64_t spans0,
+                                                                   int64_t spans) {
+  __shared__ Segments segments;
+  const int64_t g = block_id() / spans;
+  int64_t span = block_id() - g * spans;
   if (g >= a.seg.n_adapters) return;
-  count_rows(a.seg, a.rows, cnt);
+  const int which = span < spans0 ? 0 : 1;
+  if (which) span -= spans0;
+  const LoraFactor f = a.f[which];
+  count_rows(a.seg, a.rows, segments);
   Slot s;
-  if (!find_slot<true>(cnt, a.seg.n_adapters, chunk, g, s) || s.slots < 2) return;
+  if (!find_slot<true>(segments.cnt, (int)a.seg.n_adapters, (int)w.chunk, g, s) || s.slots < 2) return;
   const int64_t all = a.rank * f.cols, e = (span * kThreads + threadIdx.x) * kSumRun, n = all - e;
   if (n <= 0) return;
-  const float* p = part + s.part * all + e;
-  const int64_t slots = min(s.slots, parts - s.part);
-  float v[kSumRun] = {}, w[kSumRun];
+  const float* p = w.part[which] + s.part * all + e;
+  const int64_t slots = min((int64_t)s.slots, w.parts - s.part);
+  float v[kSumRun] = {}, t[kSumRun];
+#pragma unroll 4
   for (int64_t k = 0; k < slots; ++k) {
-    load_run<kSumRun>(p + k * all, n, w);
+    load_run<kSumRun>(p + k * all, n, t);
 #pragma unroll
-    for (int i = 0; i < kSumRun; ++i) v[i] += w[i];
+    for (int i = 0; i < kSumRun; ++i) v[i] += t[i];
   }
   finish<kSumRun>(a, f, a.scale ? a.scale[g] : 1.0f, g * all + e, n, v);
 }
@@ -1404,13 +1489,11 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
 
 namespace {
 
-// Columns a lane takes, so that the sums of a wave take 128 registers.
-constexpr int weight_run(int r16, int dtype) { return r16 <= 4 ? (dtype == 0 ? 4 : 8) : r16 <= 8 ? 4 : 2; }
 int rank_groups(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : rank <= 128 ? 8 : 16; }
 
 // Rows of a slot: 256 to 2048, so that some 512 workgroups have work.
-int64_t weight_chunk(int64_t rows, int64_t rank, int64_t cols) {
-  const int64_t tile = 16 * weight_run(rank_groups(rank), 1), tiles = (cols + tile - 1) / tile;
+int64_t weight_chunk(int64_t rows, int64_t rank, int64_t c_in, int64_t c_out) {
+  const int64_t tile = 16 * weight_run(rank_groups(rank), 1), tiles = (c_in + tile - 1) / tile + (c_out + tile - 1) / tile;
   int64_t chunk = kMostChunk;
   while (chunk > 256 && (rows + chunk - 1) / chunk * tiles < 512) chunk /= 2;
   return chunk;
@@ -1418,47 +1501,55 @@ int64_t weight_chunk(int64_t rows, int64_t rank, int64_t cols) {
 // Parts: the slots of adapters that have several, at most two for every chunk of rows.
 int64_t weight_parts(int64_t rows, int64_t chunk) { return rows > chunk ? 2 * (rows / chunk) : 0; }
 
+template <int kDx, int kDy>
+hipError_t launch_weights(const LoraWeightArgs& a, WeightWork w, hipStream_t stream) {
+  return by_rank(a.rank, [&](auto r) {
+    constexpr int kX = 16 * weight_run(r, kDx), kY = 16 * weight_run(r, kDy);
+    w.tiles[0] = a.f[0].out ? (a.f[0].cols + kX - 1) / kX : 0;
+    w.tiles[1] = a.f[1].out ? (a.f[1].cols + kY - 1) / kY : 0;
+    const int64_t blocks = w.slots * (w.tiles[0] + w.tiles[1]);
+    if (blocks == 0) return hipSuccess;
+    lora_weight_kernel<kDx, kDy, r><<<grid_of(blocks), dim3(kThreads), 0, stream>>>(a, w);
+    return hipGetLastError();
+  });
+}
+
 }  // namespace
 
 size_t lora_weight_ws_bytes(int64_t rows, int64_t segments, int64_t n_adapters, int64_t rank, int64_t c_in,
                             int64_t c_out) {
   (void)segments;
   (void)n_adapters;
-  size_t most = 0;
-  for (const int64_t cols : {c_in, c_out}) {
-    const size_t b = (size_t)weight_parts(rows, weight_chunk(rows, rank, cols)) * (size_t)rank * (size_t)cols * sizeof(float);
-    most = b > most ? b : most;
-  }
-  return most;
+  return (size_t)weight_parts(rows, weight_chunk(rows, rank, c_in, c_out)) * (size_t)rank * (size_t)(c_in + c_out) *
+         sizeof(float);
 }
 
 hipError_t launch_lora_weight_grad(const LoraWeightArgs& a, hipStream_t stream) {
-  float* part = static_cast<float*>(a.ws);
-  for (const LoraFactor& f : a.f) {
-    if (!f.out || f.cols == 0) continue;
-    const int64_t chunk = weight_chunk(a.rows, a.rank, f.cols), slots = a.seg.n_adapters + a.rows / chunk;
-    const int64_t parts = weight_parts(a.rows, chunk);
-    hipError_t e = by_rank(a.rank, [&](auto r) {
-      const auto launch = [&](auto d) {
-        constexpr int kOut = weight_run(r, d);
-        const int64_t tiles = (f.cols + 16 * kOut - 1) / (16 * kOut);
-        lora_weight_kernel<d, r, kOut><<<grid_of(slots * tiles), dim3(kThreads), 0, stream>>>(a, f, chunk, tiles, part,
-                                                                                                   parts);
-        return hipGetLastError();
-      };
-      if (f.dtype == 0) return launch(std::integral_constant<int, 0>{});
-      if (f.dtype == 1) return launch(std::integral_constant<int, 1>{});
-      return launch(std::integral_constant<int, 2>{});
-    });
+  WeightWork w{};
+  w.chunk = weight_chunk(a.rows, a.rank, a.f[0].cols, a.f[1].cols);
+  w.slots = a.seg.n_adapters + a.rows / w.chunk;
+  w.parts = weight_parts(a.rows, w.chunk);
+  w.part[0] = static_cast<float*>(a.ws);
+  w.part[1] = w.part[0] + w.parts * a.rank * a.f[0].cols;
+  const int dx = a.f[0].dtype, dy = a.f[1].dtype;
+  hipError_t e;
+  if (dx == dy) {
+    e = dx == 0 ? launch_weights<0, 0>(a, w, stream) : launch_weights<1, 1>(a, w, stream);
+  } else if (dx == 2 && dy == 1) {
+    e = launch_weights<2, 1>(a, w, stream);
+  } else {  // one after the other
+    LoraWeightArgs x = a, y = a;
+    x.f[1].out = y.f[0].out = nullptr;
+    e = dx == 0 ? launch_weights<0, 0>(x, w, stream) : dx == 1 ? launch_weights<1, 1>(x, w, stream) : launch_weights<2, 1>(x, w, stream);
     if (e != hipSuccess) return e;
-    if (parts == 0) continue;
-    const int64_t spans = (a.rank * f.cols + kThreads * kSumRun - 1) / (kThreads * kSumRun);
-    lora_weight_sum_kernel<<<grid_of(a.seg.n_adapters * spans), dim3(kThreads), 0, stream>>>(a, f, chunk, spans, part,
-                                                                                             parts);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    e = dy == 0 ? launch_weights<0, 0>(y, w, stream) : launch_weights<1, 1>(y, w, stream);
   }
-  return hipSuccess;
+  if (e != hipSuccess || w.parts == 0) return e;
+  const auto spans_of = [&](const LoraFactor& f) { return f.out ? (a.rank * f.cols + kThreads * kSumRun - 1) / (kThreads * kSumRun) : 0; };
+  const int64_t spans0 = spans_of(a.f[0]), spans = spans0 + spans_of(a.f[1]);
+  if (spans == 0) return e;
+  lora_weight_sum_kernel<<<grid_of(a.seg.n_adapters * spans), dim3(kThreads), 0, stream>>>(a, w, spans0, spans);
+  return hipGetLastError();
 }
 
 }  // namespace lh

@@ -840,7 +840,8 @@ size_t lh_lora_weight_grad_workspace_bytes(int64_t n_rows, int64_t n_segments, i
  *            [n_adapters][rank][c_out], dense.
  *   workspace  at least lh_lora_weight_grad_workspace_bytes() bytes, 256-byte
  *            aligned (may be NULL where that is 0).
- * n_adapters <= 1024, n_rows < 2^31.
+ * n_adapters <= 1024; n_rows and the leading dimensions below 2^31.  An infinity
+ * or NaN in x, dy, s or ds leaves infinities or NaN in its adapter's gradients.
  * Errors: LH_ERR_NULL, LH_ERR_SHAPE, LH_ERR_DTYPE, LH_ERR_WORKSPACE,
  * LH_ERR_ARG, LH_ERR_HIP.
  */

@@ -912,7 +912,8 @@ lh_status lh_lora_weight_grad(const void* x, int x_dtype, const uint8_t* x_scale
   if (st != LH_OK) return st;
   if (c_in < 0 || c_out < 0) return fail(LH_ERR_SHAPE, "%s: negative size", fn);
   if (n_adapters > lh::kLoraMaxAdapters) return fail(LH_ERR_SHAPE, "%s: n_adapters must be at most 1024", fn);
-  if (n_rows > 0x7fffffff) return fail(LH_ERR_SHAPE, "%s: n_rows must be below 2^31", fn);
+  if (n_rows > 0x7fffffff || ld_x > 0x7fffffff || ld_dy > 0x7fffffff)
+    return fail(LH_ERR_SHAPE, "%s: n_rows and the leading dimensions must be below 2^31", fn);
   if (ld_x < c_in || ld_dy < c_out) return fail(LH_ERR_SHAPE, "%s: a leading dimension is smaller than its row", fn);
   if (x_dtype == LH_DTYPE_E4M3 && ld_x != c_in && n_rows > 1)
     return fail(LH_ERR_SHAPE, "%s: a checkpoint is dense (ld_x == c_in)", fn);

@@ -1100,10 +1100,15 @@ struct Cols {
   uint32_t scale;
 };
 template <int kDtype, int kOut, bool kWhole>
-__device__ __forceinline__ void load_cols(const LoraFactor& f, int64_t row, int64_t c, int64_t n, Cols<kDtype, kOut>& r) {
+__device__ __forceinline__ void load_cols(const LoraFactor& f, int row, int64_t c, int64_t n, Cols<kDtype, kOut>& r) {
   using T = std::conditional_t<kDtype == 0, float, std::conditional_t<kDtype == 1, uint16_t, uint8_t>>;
-  const T* p = static_cast<const T*>(f.x) + row * (kDtype == 2 ? f.cols : f.ld) + c;
-  if constexpr (kDtype == 2) r.scale = kWhole || n > 0 ? f.x_scale[row * ((f.cols + 31) / 32) + c / 32] : 127u;
+  // (one 32 x 32 bit product each: no row is 2^31 elements long)
+  const uint32_t ld = (uint32_t)(kDtype == 2 ? f.cols : f.ld);
+  const T* p = static_cast<const T*>(f.x) + ((uint64_t)(uint32_t)row * ld + (uint64_t)c);
+  if constexpr (kDtype == 2) {
+    const uint32_t blocks = (ld + 31) / 32;
+    r.scale = kWhole || n > 0 ? f.x_scale[(uint64_t)(uint32_t)row * blocks + (uint64_t)(c >> 5)] : 127u;
+  }
   if (kWhole || n >= kOut) {
     __builtin_memcpy(r.w, p, kOut * sizeof(T));
   } else {
@@ -1127,9 +1132,19 @@ __device__ __forceinline__ uint32_t pair_of(const Cols<kDtype, kOut>& r) {
   if constexpr (kDtype == 1) {
     return r.w[o];
   } else {
-    const float up = e8m0_to_f32(r.scale);
-    return pack_bf16(e4m3_to_f32<(2 * o) % 4>(r.w[o / 2]) * up, e4m3_to_f32<(2 * o) % 4 + 1>(r.w[o / 2]) * up);
+    const bf16x2_t v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.w[o / 2], e8m0_to_f32(r.scale), o % 2 != 0);
+    return __builtin_bit_cast(uint32_t, v);
   }
+}
+
+// split3 without its care for infinities: they leave NaN in the second part.
+__device__ __forceinline__ void split3_finite(float a, float b, uint32_t (&p)[3]) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  const uint32_t ra = __float_as_uint(a - __uint_as_float(ua & 0xffff0000u)), rb = __float_as_uint(b - __uint_as_float(ub & 0xffff0000u));
+  const float la = __uint_as_float(ra) - __uint_as_float(ra & 0xffff0000u), lb = __uint_as_float(rb) - __uint_as_float(rb & 0xffff0000u);
+  p[0] = __builtin_amdgcn_perm(ub, ua, 0x07060302u);
+  p[1] = __builtin_amdgcn_perm(rb, ra, 0x07060302u);
+  p[2] = __builtin_amdgcn_perm(__float_as_uint(lb), __float_as_uint(la), 0x07060302u);
 }
 
 // A lane's share of a step of 32 rows of the list: the rows 8 q + j.  kWhole: rows
@@ -1151,11 +1166,14 @@ __device__ __forceinline__ void load_step(const LoraFactor& f, int64_t rank, con
     if (kWhole || i < count) load_cols<kDtype, kOut, kWhole>(f, row[j], c, n, s.x[j]);
     else s.x[j] = Cols<kDtype, kOut>{};
   }
+  int r[kR16];
 #pragma unroll
-  for (int i = 0; i < kR16; ++i) {
-    const int64_t r = min((int64_t)(16 * i + r16), rank - 1);
+  for (int i = 0; i < kR16; ++i) r[i] = min(16 * i + r16, (int)rank - 1);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s.p[i][j] = kWhole || row[j] >= 0 ? f.p[row[j] * rank + r] : 0.0f;
+  for (int j = 0; j < 8; ++j) {
+    const float* p = f.p + (uint64_t)(uint32_t)row[j] * (uint32_t)rank;
+#pragma unroll
+    for (int i = 0; i < kR16; ++i) s.p[i][j] = kWhole || row[j] >= 0 ? p[r[i]] : 0.0f;
   }
 }
 template <int kDtype, int kR16, int kOut>
@@ -1183,7 +1201,7 @@ __device__ __forceinline__ void add_step(const Step<kDtype, kR16, kOut>& s, f32x
     for (int i = 0; i < kR16; ++i) {
       uint32_t a[4][3];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split3(p[i][2 * j], p[i][2 * j + 1], a[j]);
+      for (int j = 0; j < 4; ++j) split3_finite(p[i][2 * j], p[i][2 * j + 1], a[j]);
 #pragma unroll
       for (int u = 2; u >= 0; --u) {  // the smallest part first
         const bf16x8_t fa = __builtin_bit_cast(bf16x8_t, make_uint4(a[0][u], a[1][u], a[2][u], a[3][u]));

@@ -503,7 +503,7 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
       else to[v] = Run<kOut, TY>{};
     }
   };
-  load_base(0, b);  // before it is known whose rows they are
+  load_base(0, next);  // before it is known whose rows they are
   tile_adapters<kOutRows>(a.seg, t0, t1, of);
   // s of the tile's rows: the sum of the contraction's shares, in their order
 #pragma unroll 2
@@ -565,6 +565,8 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
     }
 #pragma unroll 1
     for (int t = 0; t < row_tile; t += 16) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) b[v] = next[v];
       if (t + 16 < row_tile) load_base(t + 16, next);
       if ((rows >> t) & 0xffffull) {
         f32x4_t acc[kOut];
@@ -599,10 +601,8 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
           store_own<kOut>(y + (t0 + at) * a.ld_y + c0, skip, out);
         }
       }
-#pragma unroll
-      for (int v = 0; v < 4; ++v) b[v] = next[v];
     }
-    if (left) load_base(0, b);
+    if (left) load_base(0, next);
   }
   // rows without an adapter
   const unsigned long long bare = __ballot(mine == -1);
@@ -1273,16 +1273,13 @@ __device__ __forceinline__ void weight_tile(const LoraWeightArgs& a, const LoraF
     for (int o = 0; o < kOut; ++o) acc[i][o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   int at = 32 * wave;
   if (c_tile + 16 * kOut <= f.cols && at + 32 <= count) {  // the next step's loads are in flight while this one is added
-    Step<kDtype, kR16, kOut> s0, s1;
-    load_step<kDtype, kR16, kOut, true>(f, a.rank, lds.list, at, count, c, n, s0);
+    Step<kDtype, kR16, kOut> next;
+    load_step<kDtype, kR16, kOut, true>(f, a.rank, lds.list, at, count, c, n, next);
 #pragma unroll 1
-    for (;;) {
-      const bool more = at + 160 <= count;
-      if (more) load_step<kDtype, kR16, kOut, true>(f, a.rank, lds.list, at + 128, count, c, n, s1);
+    for (; at + 32 <= count; at += 128) {
+      const Step<kDtype, kR16, kOut> s0 = next;
+      if (at + 160 <= count) load_step<kDtype, kR16, kOut, true>(f, a.rank, lds.list, at + 128, count, c, n, next);
       add_step(s0, acc);
-      at += 128;
-      if (!more) break;
-      s0 = s1;
     }
   }
 #pragma unroll 1
@@ -1327,7 +1324,7 @@ struct WeightWork {
   float* part[2];
 };
 template <int kDx, int kDy, int kR16>
-__global__ __launch_bounds__(kThreads, (kR16 <= 4 ? 2 : 1)) void lora_weight_kernel(LoraWeightArgs a, WeightWork w) {
+__global__ __launch_bounds__(kThreads, (kR16 <= 1 ? 3 : kR16 <= 4 ? 2 : 1)) void lora_weight_kernel(LoraWeightArgs a, WeightWork w) {
   __shared__ __attribute__((aligned(16))) union Lds {
     WeightLds<weight_run(kR16, kDx)> x;
     WeightLds<weight_run(kR16, kDy)> y;

@@ -109,64 +109,152 @@ __device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8])
 }
 
 // ---------------------------------------------------------------------------
-// The row kernels: a wave per row and group of ranks, a thread per row and
-// eight outputs.
+// The row kernels, for few rows and for segments of a row or so: no matrix cores,
+// every row with its own adapter.  Latency is what counts, so all loads that do not
+// wait for an adapter's number are issued before it, and a workgroup's four waves
+// share the sum that its outputs need.
 // ---------------------------------------------------------------------------
 constexpr int kRowRanks = 4;
 
+// Into the rank: a workgroup takes a row, four ranks and a span of the contraction
+// (a multiple of 512), its waves 512 elements in turn.
 template <typename TX, typename TW>
-__global__ __launch_bounds__(64) void lora_row_in_kernel(LoraArgs a, int64_t groups, float* __restrict__ s) {
-  const int64_t unit = block_id(), t = unit / groups, r0 = (unit - t * groups) * kRowRanks;
+__global__ __launch_bounds__(kThreads) void lora_row_in_kernel(LoraArgs a, int64_t groups, int splits, int64_t span,
+                                                               float* __restrict__ part) {
+  __shared__ float red[kThreads / 64][kRowRanks];
+  const int64_t unit = block_id(), t = unit / (groups * splits);
   if (t >= a.rows) return;
-  const int lane = threadIdx.x & 63;
+  const int64_t rest = unit - t * (groups * splits), split = rest / groups, r0 = (rest - split * groups) * kRowRanks;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int64_t c0 = split * span + 512 * wave, end = min(split * span + span, a.c_x);
+  const TX* const x = static_cast<const TX*>(a.x) + t * a.ld_x + lane * 8;
+  float first[8] = {};
+  if (c0 + 512 <= end) load8(x + c0, 8, first);
   const int64_t g = adapter_of_row(a.seg, t);
-  if (g == -2) return;
+  if (g == -2) return;  // the whole workgroup
   float acc[kRowRanks] = {};
   if (g >= 0) {
-    const TX* x = static_cast<const TX*>(a.x) + t * a.ld_x;
-    const TW* w = static_cast<const TW*>(a.in) + (g * a.rank + r0) * a.c_x;
-    for (int64_t c = lane * 8; c < a.c_x; c += 512) {
-      float xv[8];
-      load8(x + c, a.c_x - c, xv);
+    const TW* w[kRowRanks];
+#pragma unroll
+    for (int r = 0; r < kRowRanks; ++r)
+      w[r] = static_cast<const TW*>(a.in) + (g * a.rank + min(r0 + r, a.rank - 1)) * a.c_x + lane * 8;
+    int64_t c = c0;
+    if (c + 512 <= end) {
+      float wv[kRowRanks][8];
+#pragma unroll
+      for (int r = 0; r < kRowRanks; ++r) load8(w[r] + c, 8, wv[r]);
+#pragma unroll
+      for (int r = 0; r < kRowRanks; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[r] = __builtin_fmaf(first[i], wv[r][i], acc[r]);
+      c += 512 * (kThreads / 64);
+    }
+#pragma unroll 2
+    for (; c + 512 <= end; c += 512 * (kThreads / 64)) {
+      float xv[8], wv[kRowRanks][8];
+      load8(x + c, 8, xv);
+#pragma unroll
+      for (int r = 0; r < kRowRanks; ++r) load8(w[r] + c, 8, wv[r]);
+#pragma unroll
+      for (int r = 0; r < kRowRanks; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[r] = __builtin_fmaf(xv[i], wv[r][i], acc[r]);
+    }
+    if (c + lane * 8 < end) {  // the row's last elements
+      const int64_t n = end - c - lane * 8;
+      float xv[8], wv[8];
+      load8(x + c, n, xv);
 #pragma unroll
       for (int r = 0; r < kRowRanks; ++r) {
-        if (r0 + r >= a.rank) break;
-        float wv[8];
-        load8(w + r * a.c_x + c, a.c_x - c, wv);
+        load8(w[r] + c, n, wv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[r] = __builtin_fmaf(xv[i], wv[i], acc[r]);
       }
     }
   }
   const float v = wave_sums(acc);
-  const int r = lane / (64 / kRowRanks);
-  if (lane % (64 / kRowRanks) == 0 && r0 + r < a.rank) s[t * a.rank + r0 + r] = v;
+  if (lane % (64 / kRowRanks) == 0) red[wave][lane / (64 / kRowRanks)] = v;
+  __syncthreads();
+  if (tid < kRowRanks && r0 + tid < a.rank) {
+    float sum = red[0][tid];
+#pragma unroll
+    for (int u = 1; u < kThreads / 64; ++u) sum += red[u][tid];
+    part[(split * a.rows + t) * a.rank + r0 + tid] = sum;
+  }
 }
 
+// Out of the rank: a workgroup takes a row and 512 outputs, its waves every fourth
+// rank, a lane eight outputs.
 template <typename TW, typename TY>
-__global__ __launch_bounds__(64) void lora_row_out_kernel(LoraArgs a, int64_t spans, const float* __restrict__ s) {
-  const int64_t unit = block_id(), t = unit / spans;
+__global__ __launch_bounds__(kThreads) void lora_row_out_kernel(LoraArgs a, int64_t spans, const float* __restrict__ part,
+                                                                int splits) {
+  constexpr int kWaves = kThreads / 64, kAhead = 4;
+  __shared__ float s[kLoraMaxRank];
+  __shared__ __attribute__((aligned(16))) float red[kWaves][512];
+  const int64_t unit = block_id(), t = unit / spans, c_tile = (unit - t * spans) * 512;
   if (t >= a.rows) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, rank = (int)a.rank;
+  const int64_t c = c_tile + lane * 8, n = a.c_y - c, o = c_tile + 2 * tid, left = a.c_y - o;  // o: the two outputs it stores
+  TY* const y = static_cast<TY*>(a.y) + t * a.ld_y + o;
+  float b[2] = {};
+  if (a.base) {
+    const TY* p = static_cast<const TY*>(a.base) + t * a.ld_base + o;
+    if (left > 0) b[0] = load_as_f32<TY>(p, 0);
+    if (left > 1) b[1] = load_as_f32<TY>(p, 1);
+  }
   const int64_t g = adapter_of_row(a.seg, t);
-  const int64_t c = (unit - t * spans) * 512 + threadIdx.x * 8;
-  if (g == -2 || c >= a.c_y) return;
-  const int64_t n = a.c_y - c;
-  TY* y = static_cast<TY*>(a.y) + t * a.ld_y + c;
-  float acc[8] = {}, v[8] = {};
-  if (a.base) load8(static_cast<const TY*>(a.base) + t * a.ld_base + c, n, v);
-  if (g >= 0) {
-    const TW* w = static_cast<const TW*>(a.out) + g * a.rank * a.c_y + c;
-    for (int64_t r = 0; r < a.rank; ++r) {
+  if (g == -2) return;  // the whole workgroup
+  if (g >= 0 && rank > 0) {
+    const TW* const w = static_cast<const TW*>(a.out) + g * a.rank * a.c_y + c;
+    float first[kAhead][8];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load8(w + min(wave + kWaves * u, rank - 1) * a.c_y, n, first[u]);
+    if (tid < rank) {
+      const int64_t at = t * a.rank + tid;
+      const float v = sum_slices(part + at, a.rows * a.rank, splits);
+      s[tid] = v;
+      if (a.s && a.s != part && c_tile == 0) a.s[at] = v;
+    }
+    __syncthreads();
+    float acc[8] = {};
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (wave + kWaves * u < rank) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(s[wave + kWaves * u], first[u][i], acc[i]);
+      }
+#pragma unroll 4
+    for (int r = wave + kWaves * kAhead; r < rank; r += kWaves) {
       float wv[8];
       load8(w + r * a.c_y, n, wv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(s[t * a.rank + r], wv[i], acc[i]);
+      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(s[r], wv[i], acc[i]);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[wave][8 * lane + i] = acc[i];
+    __syncthreads();
     const float scale = a.scale ? a.scale[g] : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(scale, acc[i], v[i]);
+    for (int h = 0; h < 2; ++h) {
+      float v = red[0][2 * tid + h];
+#pragma unroll
+      for (int u = 1; u < kWaves; ++u) v += red[u][2 * tid + h];
+      b[h] = __builtin_fmaf(scale, v, b[h]);
+    }
+  } else if (a.s && a.s != part && c_tile == 0 && tid < rank) {
+    a.s[t * a.rank + tid] = 0.0f;
   }
-  store8(y, n, v);
+  if (left > 1) {
+    if constexpr (sizeof(TY) == 2) {
+      const uint32_t v = pack_bf16(b[0], b[1]);
+      __builtin_memcpy(y, &v, 4);
+    } else {
+      __builtin_memcpy(y, b, 8);
+    }
+  } else if (left > 0) {
+    if constexpr (sizeof(TY) == 2) y[0] = f32_to_bf16_bits(b[0]);
+    else y[0] = b[0];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -1383,9 +1471,15 @@ struct LoraPlan {
   int splits;  // workgroups along the contraction
 };
 constexpr int64_t kFar = int64_t(1) << 21;  // elements of a row with which a tile's byte offsets stay below 2^31
-LoraPlan lora_plan(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y) {
+LoraPlan lora_plan(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, int64_t rank) {
   LoraPlan p{rows < 16 || rows < 4 * segments || c_y < 8 || c_x >= kFar, 1};
-  if (p.rows) return p;
+  if (p.rows) {  // two pieces of 512 elements a wave while the card is not full
+    const int64_t units = rows * ((rank + kRowRanks - 1) / kRowRanks), most = (c_x + 4095) / 4096;
+    const int64_t splits = units > 0 ? 512 / units : 1;
+    p.splits = (int)(splits < 1 ? 1 : splits < most ? splits : most < 1 ? 1 : most);
+    if (p.splits > 16) p.splits = 16;
+    return p;
+  }
   const int64_t tiles = (rows + 31) / 32, steps = (c_x + 31) / 32;
   int64_t splits = (512 + tiles - 1) / tiles;  // some two workgroups a CU
   const int64_t most = steps / 16;             // and 512 elements each at least
@@ -1404,23 +1498,24 @@ hipError_t by_rank(int64_t rank, F&& f) {
   return f(std::integral_constant<int, 16>{});
 }
 
-hipError_t launch_rows(const LoraArgs& a, float* s, hipStream_t stream) {
+hipError_t launch_rows(const LoraArgs& a, int splits, float* part, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (a.rank > 0) {
-    const int64_t groups = (a.rank + kRowRanks - 1) / kRowRanks;
+    const int64_t groups = (a.rank + kRowRanks - 1) / kRowRanks, span = ((a.c_x + 511) / 512 + splits - 1) / splits * 512;
     e = by_type(a.x_dtype, [&](auto x) {
       return by_type(a.w_dtype, [&](auto w) {
-        lora_row_in_kernel<decltype(x), decltype(w)><<<grid_of(a.rows * groups), dim3(64), 0, stream>>>(a, groups, s);
+        lora_row_in_kernel<decltype(x), decltype(w)>
+            <<<grid_of(a.rows * groups * splits), dim3(kThreads), 0, stream>>>(a, groups, splits, span, part);
         return hipGetLastError();
       });
     });
     if (e != hipSuccess) return e;
   }
-  if (a.c_y == 0) return e;
-  const int64_t spans = (a.c_y + 511) / 512;
+  const int64_t spans = a.c_y > 512 ? (a.c_y + 511) / 512 : 1;  // (without outputs: for s)
   return by_type(a.w_dtype, [&](auto w) {
     return by_type(a.y_dtype, [&](auto y) {
-      lora_row_out_kernel<decltype(w), decltype(y)><<<grid_of(a.rows * spans), dim3(64), 0, stream>>>(a, spans, s);
+      lora_row_out_kernel<decltype(w), decltype(y)>
+          <<<grid_of(a.rows * spans), dim3(kThreads), 0, stream>>>(a, spans, part, splits);
       return hipGetLastError();
     });
   });
@@ -1486,13 +1581,16 @@ hipError_t launch_both(const LoraArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t lora_ws_bytes(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, int64_t rank) {
-  return (size_t)lora_plan(rows, segments, c_x, c_y).splits * (size_t)rows * (size_t)rank * sizeof(float);
+  return (size_t)lora_plan(rows, segments, c_x, c_y, rank).splits * (size_t)rows * (size_t)rank * sizeof(float);
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream) {
-  const LoraPlan p = lora_plan(a.rows, a.seg.n, a.c_x, a.c_y);
+  const LoraPlan p = lora_plan(a.rows, a.seg.n, a.c_x, a.c_y, a.rank);
   float* ws = static_cast<float*>(a.ws);
-  if (p.rows || a.rank == 0 || a.ld_x >= kFar) return launch_rows(a, a.s ? a.s : ws, stream);
+  if (p.rows || a.rank == 0 || a.ld_x >= kFar || a.ld_base >= kFar || a.ld_y >= kFar || a.c_y >= kFar) {
+    const int splits = p.rows ? p.splits : 1;
+    return launch_rows(a, splits, splits == 1 && a.s ? a.s : ws, stream);
+  }
   if (both_ways(a)) return launch_both(a, stream);
   int splits = p.splits;
   if (a.x_dtype == 1 && a.w_dtype == 1) {  // workgroups of eight waves, two a CU or one

@@ -1,6 +1,6 @@
 """An MoE layer from calibration to a training step, through the library's calls.
 
-    python3 examples/moe_layer.py [--tokens 4096] [--experts 64] [--top-k 8] [--c-in 2048] [--c-out 1024]
+    python3 examples/moe_layer.py [--tokens 4096] [--experts 64] [--top-k 8] [--c-in 2048] [--c-out 1024] [--rank 16]
 
 1. Route tokens, sort them by expert (lh_moe_sort) and send their rows to the
    experts (lh_moe_dispatch).
@@ -12,6 +12,9 @@
 4. Its gradients: to the routing weights and the experts' outputs
    (lh_moe_combine_grad), through the experts (lh_linear_nvfp4_ragged_grad) and
    back to the tokens (lh_moe_combine).
+5. With --rank: a low-rank adapter for every expert beside its frozen weights
+   (lh_lora, lh_lora_grad), trained from the experts' rows kept in 8 bits
+   (lh_checkpoint_pack, lh_lora_weight_grad).
 
 Random weights and activations stand in for a model's.
 """
@@ -43,8 +46,8 @@ def build_layer(lh, w, x, ids):
                 amax_x=lh.lh_absmax(x))
 
 
-def forward(lh, layer, x, ids, weights, quantize_x=False):
-    """y [tokens, c_out] and what the backward pass needs."""
+def forward(lh, layer, x, ids, weights, quantize_x=False, adapters=None):
+    """y [tokens, c_out] and what the backward pass needs.  adapters: (a, b, scale), one for every expert."""
     experts = layer["packed"].shape[0]
     plan = lh.lh_moe_sort(ids, experts, order=False)
     x_scale = None
@@ -55,16 +58,26 @@ def forward(lh, layer, x, ids, weights, quantize_x=False):
     ys = lh.lh_linear_nvfp4_ragged(xs, plan["offsets"], layer["packed"], layer["scale_e4m3"], layer["global_scale"],
                                    x_scale=x_scale)
     # (rows of assignments without an expert are not written; nothing reads them)
-    return lh.lh_moe_combine(ys, plan["position"], weights), (plan, ys)
+    saved = (plan, ys)
+    if adapters is not None:  # added in place; the rows are kept in 8 bits for the adapters' gradients
+        ys, s = lh.lh_lora(xs, *adapters, offsets=plan["offsets"], base=ys, y=ys, s=True)
+        saved = (plan, ys, s, lh.lh_checkpoint_pack(xs))
+    return lh.lh_moe_combine(ys, plan["position"], weights), saved
 
 
-def backward(lh, layer, saved, weights, dy):
-    """Gradients to the tokens and to the routing weights."""
-    plan, ys = saved
+def backward(lh, layer, saved, weights, dy, adapters=None):
+    """Gradients to the tokens, to the routing weights and, with adapters, to both factors of each."""
+    plan, ys = saved[:2]
     dys, dweights = lh.lh_moe_combine_grad(dy, ys, plan["position"], weights)
     dxs = lh.lh_linear_nvfp4_ragged_grad(dys, plan["offsets"], layer["packed"], layer["scale_e4m3"],
                                          layer["global_scale"])
-    return lh.lh_moe_combine(dxs, plan["position"]), dweights
+    if adapters is None:
+        return lh.lh_moe_combine(dxs, plan["position"]), dweights
+    s, (values, scales) = saved[2:]
+    dxs, ds = lh.lh_lora_grad(dys, *adapters, offsets=plan["offsets"], base=dxs, dx=dxs, ds=True)
+    da, db = lh.lh_lora_weight_grad(values, dys, s, ds, adapters[0].shape[0], adapters[2], offsets=plan["offsets"],
+                                    x_scale=scales)
+    return lh.lh_moe_combine(dxs, plan["position"]), dweights, da, db
 
 
 def make(tokens, experts, top_k, c_in, c_out, seed=0, device="cuda:0"):
@@ -79,6 +92,14 @@ def make(tokens, experts, top_k, c_in, c_out, seed=0, device="cuda:0"):
     return w, x, ids, torch.softmax(top, dim=1), rand(tokens, c_out).to(torch.bfloat16)
 
 
+def make_adapters(experts, rank, c_in, c_out, seed=1, device="cuda:0"):
+    """(a, b, scale) as training finds them some steps on: neither factor is zero any more."""
+    gen = torch.Generator(device=device).manual_seed(seed)
+    a = torch.randn((experts, rank, c_in), generator=gen, device=device) * c_in ** -0.5
+    b = torch.randn((experts, rank, c_out), generator=gen, device=device) * 0.02
+    return a.to(torch.bfloat16), b.to(torch.bfloat16), torch.full((experts,), 2.0, device=device)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, default=4096)
@@ -86,6 +107,7 @@ def main(argv=None):
     ap.add_argument("--top-k", type=int, default=8)
     ap.add_argument("--c-in", type=int, default=2048)
     ap.add_argument("--c-out", type=int, default=1024)
+    ap.add_argument("--rank", type=int, default=16, help="rank of the experts' adapters (0: none)")
     a = ap.parse_args(argv)
     import nvfp4_scale_calibration_amd as lh
 
@@ -120,6 +142,12 @@ def main(argv=None):
           % (timed(lambda: forward(lh, layer, x, ids, weights)),
              timed(lambda: backward(lh, layer, forward(lh, layer, x, ids, weights)[1], weights, dy)), rows, a.experts,
              a.c_out, a.c_in))
+    if a.rank > 0:
+        ad = make_adapters(a.experts, a.rank, a.c_in, a.c_out)
+        _, _, da, db = backward(lh, layer, forward(lh, layer, x, ids, weights, adapters=ad)[1], weights, dy, ad)
+        print("adapters of rank %d: gradients %s and %s, forward and backward with them %.0f us"
+              % (a.rank, tuple(da.shape), tuple(db.shape),
+                 timed(lambda: backward(lh, layer, forward(lh, layer, x, ids, weights, adapters=ad)[1], weights, dy, ad))))
 
 
 if __name__ == "__main__":

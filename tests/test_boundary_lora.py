@@ -150,3 +150,38 @@ def test_binding_refuses_host_tensors(lib):
                  lambda: m.lh_checkpoint_unpack(torch.zeros(4, 8, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8))):
         with pytest.raises(ValueError, match="device tensors"):
             call()
+
+
+def test_calls_run_with_their_tensors_device_current(lib, monkeypatch):
+    """On another device than the current one the call is made with the tensors' as current."""
+    import nvfp4_scale_calibration_amd as m
+
+    class On:
+        def get_device(self):
+            return 3
+
+    state = dict(current=0)
+
+    class Guard:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.old, state["current"] = state["current"], self.d
+
+        def __exit__(self, *_):
+            state["current"] = self.old
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["current"])
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(m, "_stream", lambda t: 17)
+    seen = []
+
+    def call(*args):
+        seen.append((state["current"], args))
+        return 0
+
+    m._launch(On(), call, 1, 2)
+    state["current"] = 3
+    m._launch(On(), call, 4)
+    assert seen == [(3, (1, 2, 17)), (3, (4, 17))]

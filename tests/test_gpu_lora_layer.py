@@ -188,3 +188,21 @@ def test_experts_adapters(lh, layer_example, tokens, experts, top_k, c_in, c_out
     # in single terms; sums are fp32 (2^-16 of their mass covers 8 sqrt(n) 2^-24 for n < 1024, twice)
     assert ((da.double().cpu() - rda).abs() <= tda * 2.0 ** -7 + 1e-30).all()
     assert ((db.double().cpu() - rdb).abs() <= tdb * 2.0 ** -7 + 1e-30).all()
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("power", [-126, -120, -100, 0, 60])
+def test_checkpoints_of_any_magnitude(lh, dt, power):
+    """The gradient takes a checkpoint's blocks at every exponent, the lowest among
+    them (e = -127): against the values that come back in bf16, in 64 bits."""
+    rng = np.random.default_rng(power + 200)
+    rows, cols, rank = 70, 100, 8
+    x = rng.uniform(1, 2, (rows, cols)) * 2.0 ** power * rng.choice([-1, 1], (rows, cols))
+    x = torch.from_numpy(x.astype(np.float32)).to(dt).to(DEV)
+    values, scales = lh.lh_checkpoint_pack(x)
+    assert power > -119 or (scales == 0).all()
+    ds = rand(rng, rows, rank, dtype=F32, scale=2.0 ** (-power / 2))
+    da, _ = lh.lh_lora_weight_grad(values, x, None, ds, 1, x_scale=scales, db=False)
+    kept, p = lh.lh_checkpoint_unpack(values, scales).double().cpu(), ds.double().cpu()
+    want, mass = p.t() @ kept, p.abs().t() @ kept.abs()
+    assert ((da[0].double().cpu() - want).abs() <= (8 * rows ** 0.5 + 6) * 2.0 ** -24 * mass).all()

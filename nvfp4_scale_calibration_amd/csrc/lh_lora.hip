@@ -89,27 +89,6 @@ __device__ __forceinline__ void load8(const float* p, int64_t n, float (&v)[8]) 
     for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
   }
 }
-__device__ __forceinline__ void store8(uint16_t* p, int64_t n, const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  if (n >= 8) {
-    __builtin_memcpy(p, w, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-  }
-}
-__device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8]) {
-  if (n >= 8) {
-    __builtin_memcpy(p, v, 32);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = v[i];
-  }
-}
 
 // ---------------------------------------------------------------------------
 // The row kernels, for few rows and for segments of a row or so: no matrix cores,
@@ -281,38 +260,19 @@ __device__ __forceinline__ T* at_byte(T* p, uint32_t offset) {
 }
 
 // One lane's eight consecutive contraction elements of an operand.
-template <bool kBf>
-struct Frag;
-template <>
-struct Frag<true> {
-  uint4 v;
-};
-template <>
-struct Frag<false> {
+struct Frag {
   float v[8];
 };
-__device__ __forceinline__ void load_frag(const uint16_t* p, Frag<true>& f) { f.v = load_u128(p); }
 template <typename T>
-__device__ __forceinline__ void load_frag(const T* p, Frag<false>& f) {
+__device__ __forceinline__ void load_frag(const T* p, Frag& f) {
   load8(p, 8, f.v);
 }
-__device__ __forceinline__ void load_frag(const uint16_t* p, int64_t n, Frag<true>& f) {
-  uint32_t w[4] = {};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-  f.v = make_uint4(w[0], w[1], w[2], w[3]);
-}
 template <typename T>
-__device__ __forceinline__ void load_frag(const T* p, int64_t n, Frag<false>& f) {
+__device__ __forceinline__ void load_frag(const T* p, int64_t n, Frag& f) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f.v[i] = i < n ? load_as_f32<T>(p, i) : 0.0f;
 }
-__device__ __forceinline__ f32x4_t multiply(const Frag<true>& a, const Frag<true>& b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v), __builtin_bit_cast(bf16x8_t, b.v), c,
-                                                 0, 0, 0);
-}
-__device__ __forceinline__ f32x4_t multiply(const Frag<false>& a, const Frag<false>& b, f32x4_t c) {
+__device__ __forceinline__ f32x4_t multiply(const Frag& a, const Frag& b, f32x4_t c) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
   return c;
@@ -328,7 +288,6 @@ constexpr int kInSub = 2, kInRows = 16 * kInSub, kInWaves = 4;
 template <typename TX, typename TW, int kR16>
 __global__ __launch_bounds__(64 * kInWaves) void lora_tile_in_kernel(LoraArgs a, int splits, int64_t k_wave,
                                                                      float* __restrict__ part) {
-  constexpr bool kBf = false;
   constexpr int kSub = kInSub, kWaves = kInWaves;
   constexpr int kSteps = kR16 <= 2 ? 2 : 1;  // contraction steps of 32 that are loaded together (twice as many are in flight)
   __shared__ int of[kInRows];
@@ -344,7 +303,7 @@ __global__ __launch_bounds__(64 * kInWaves) void lora_tile_in_kernel(LoraArgs a,
 #pragma unroll
   for (int h = 0; h < kSub; ++h) x[h] = ((uint32_t)(min((int64_t)(16 * h + r16), a.rows - 1 - t0) * a.ld_x) + 8 * q) * sizeof(TX);
   struct Stage {
-    Frag<kBf> x[kSteps][kSub], w[kSteps][kR16];
+    Frag x[kSteps][kSub], w[kSteps][kR16];
   };
   const auto load_x = [&](Stage& f, int64_t k) {
 #pragma unroll
@@ -408,7 +367,7 @@ __global__ __launch_bounds__(64 * kInWaves) void lora_tile_in_kernel(LoraArgs a,
     }
     again = true;
     for (; k < k1; k += 32) {
-      Frag<kBf> fx[kSub];
+      Frag fx[kSub];
       const int64_t in = k1 - k - 8 * q;  // elements of this lane inside the row
 #pragma unroll
       for (int h = 0; h < kSub; ++h) {
@@ -417,7 +376,7 @@ __global__ __launch_bounds__(64 * kInWaves) void lora_tile_in_kernel(LoraArgs a,
       }
 #pragma unroll
       for (int i = 0; i < kR16; ++i) {
-        Frag<kBf> fw;
+        Frag fw;
         if (in >= 8) load_frag(at_byte(wt + k, w[i]), fw);
         else load_frag(at_byte(wt + k, w[i]), in, fw);
 #pragma unroll
@@ -728,9 +687,11 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
 // Eight bf16 of a row from p on, the first n of them inside it.
 __device__ __forceinline__ uint4 load_piece(const uint16_t* p, int64_t n) {
   if (n >= 8) return load_u128(p);
-  Frag<true> f;
-  load_frag(p, n, f);
-  return f.v;
+  uint32_t w[4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 constexpr int line_lds(int r16, int sub) { return (r16 + sub) * 16 * 128; }  // bytes a wave

@@ -777,9 +777,8 @@ size_t lh_lora_workspace_bytes(int grad, int64_t n_rows, int64_t n_segments, int
  *   y[t][o] = base[t][o] + scale[g] * sum_r s[t][r] b[g][r][o]
  * Rows of a segment without an adapter get y = base and s = 0; rows of no
  * segment are not written.  Sums are fp32 in an order that depends on the
- * sizes alone, products exact or rounded to fp32; where bf16 factors meet s on
- * the matrix cores, s is cut into two bf16 values for a bf16 y (2^-16 of s is
- * lost, 2^-8 below y's own rounding) and into three for an fp32 y (nothing).
+ * sizes alone, products exact or rounded to fp32; s keeps its 24 bits on the
+ * way out, whatever the types.
  * One rounding to y_dtype at the end.  Infinities and NaN follow the formula,
  * in their own row only.
  *   x      fp32 or bf16 [n_rows][ld_x], ld_x >= c_in.

@@ -488,24 +488,12 @@ __device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[kN]) 
 // it goes through the rows 16 at a time, what base holds of the next ones being
 // loaded meanwhile.  Factors are stored with the rank first, and an operand wants
 // four ranks of one output: bf16 ones are paired across two ranks' rows by byte
-// permutation.  s comes through LDS; bf16 factors meet it in kPlanes bf16 values
-// that add up to it, to 16 bits (two, bf16 y) or exactly (three).  8192 rows, 4096
-// -> 12288, rank 16: 78 us, 5.1 TB/s, as a copy; rank 64 (4096 x 4096) 23 us, 2.9, at
+// permutation.  s comes through LDS; bf16 factors meet it in three bf16 values that
+// add up to it exactly.  8192 rows, 4096
+// -> 12288, rank 16: 79 us, 5.1 TB/s, as a copy; rank 64 (4096 x 4096) 27 us, 2.5, at
 // two waves a SIMD.  128 or 256 rows a workgroup: 99 -> 105 to 111 us with both kernels.
 constexpr int kOutRows = 64;
 
-// Two pairs of fp32 values in kPlanes (2 or 3) bf16 values each that add up to them.
-template <int kPlanes>
-__device__ __forceinline__ void cut(const float (&v)[4], uint32_t (&p)[2][3]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    split3(v[2 * h], v[2 * h + 1], p[h]);
-    if constexpr (kPlanes == 2) {  // the second part rounded, and no third
-      const float h0 = __uint_as_float(p[h][0] << 16), h1 = __uint_as_float(p[h][0] & 0xffff0000u);
-      p[h][1] = pack_bf16(isinf(v[2 * h]) ? 0.0f : v[2 * h] - h0, isinf(v[2 * h + 1]) ? 0.0f : v[2 * h + 1] - h1);
-    }
-  }
-}
 // kOut outputs of four ranks to the four ranks of each output.
 template <int kOut>
 __device__ __forceinline__ void pair_ranks(const Run<kOut, uint16_t> (&d)[4], s16x4_t (&to)[kOut]) {
@@ -520,8 +508,9 @@ __device__ __forceinline__ void pair_ranks(const Run<kOut, uint16_t> (&d)[4], s1
   }
 }
 
-template <typename TW, typename TY>
-constexpr int out_planes = sizeof(TW) == 4 ? 0 : sizeof(TY) == 2 ? 2 : 3;
+// The bf16 parts of s that bf16 factors meet (0: fp32 factors meet s itself).
+template <typename TW>
+constexpr int out_planes = sizeof(TW) == 4 ? 0 : 3;
 
 // Outputs a lane, so that a wave's part of the factor takes 128 registers at most.
 template <typename TW, int kR16>
@@ -535,7 +524,7 @@ constexpr int out_waves = sizeof(TW) == 2 ? (kR16 == 1 && sizeof(TY) == 2 ? 3 : 
 template <typename TW, typename TY, int kR16>
 __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile_out_kernel(LoraArgs a, const float* __restrict__ part, int splits,
                                                                  int row_tile, int64_t col_tiles) {
-  constexpr int kPlanes = out_planes<TW, TY>, kOut = out_run<TW, kR16>;
+  constexpr int kPlanes = out_planes<TW>, kOut = out_run<TW, kR16>;
   constexpr int kPitch = 16 * kR16 + (kPlanes ? 8 : 4);  // elements of a row in LDS
   extern __shared__ __attribute__((aligned(16))) char lds[];  // kPlanes x [row_tile][kPitch] bf16, or [row_tile][kPitch] fp32
   __shared__ int of[kOutRows];
@@ -578,7 +567,8 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
       *reinterpret_cast<float4*>(lds + (t * kPitch + r) * 4) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
       uint32_t p[2][3];
-      cut<kPlanes>(v, p);
+      split3(v[0], v[1], p[0]);
+      split3(v[2], v[3], p[1]);
 #pragma unroll
       for (int i = 0; i < kPlanes; ++i)
         *reinterpret_cast<uint2*>(lds + ((i * row_tile + t) * kPitch + r) * 2) = make_uint2(p[0][i], p[1][i]);
@@ -852,7 +842,7 @@ constexpr int kBothWaves = 8;
 
 template <typename TY>
 __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lora_both_kernel(LoraArgs a) {
-  constexpr int kR16 = 1, kSub = 1, kRows = 16, kOut = 4, kPlanes = out_planes<uint16_t, TY>;
+  constexpr int kR16 = 1, kSub = 1, kRows = 16, kOut = 4, kPlanes = out_planes<uint16_t>;
   constexpr int kPitch = 16 * kR16 + 8;  // elements of a row of a plane
   __shared__ __attribute__((aligned(16))) char lds[kBothWaves * line_lds(kR16, kSub)];  // (the sums take a quarter of it)
   __shared__ __attribute__((aligned(16))) uint16_t planes[kPlanes][kRows][kPitch];
@@ -880,7 +870,8 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
                                for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.0f;
                                if (a.s && r < rank) store_run<4>(a.s + (t0 + t) * rank + r, rank - r, v);
                                uint32_t p[2][3];
-                               cut<kPlanes>(v, p);
+                               split3(v[0], v[1], p[0]);
+                               split3(v[2], v[3], p[1]);
 #pragma unroll
                                for (int i = 0; i < kPlanes; ++i)
                                  *reinterpret_cast<uint2*>(&planes[i][t][r]) = make_uint2(p[0][i], p[1][i]);
@@ -1520,7 +1511,7 @@ hipError_t launch_tiles(const LoraArgs& a, int splits, float* part, hipStream_t 
       return by_rank(a.rank, [&](auto r) {
         using TW = decltype(w);
         using TY = decltype(y);
-        constexpr int kOut = out_run<TW, r>, kPlanes = out_planes<TW, TY>;
+        constexpr int kOut = out_run<TW, r>, kPlanes = out_planes<TW>;
         const int64_t col_tiles = (a.c_y + 64 * kOut - 1) / (64 * kOut);
         // bytes of a row in LDS: below 26 KiB for 16 rows of any rank
         constexpr size_t kRowBytes = kPlanes ? kPlanes * (16 * r + 8) * 2 : (16 * r + 4) * 4;

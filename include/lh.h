@@ -824,7 +824,8 @@ size_t lh_lora_weight_grad_workspace_bytes(int64_t n_rows, int64_t n_segments, i
  * (ds) left:
  *   da[g][r][c] = beta * da[g][r][c] + scale[g] * sum_t ds[t][r] x[t][c]
  *   db[g][r][o] = beta * db[g][r][o] + scale[g] * sum_t s[t][r] dy[t][o]
- * over the rows t of all segments with adapter g.  Either output may be NULL,
+ * over the rows t of all segments with adapter g, each row once (overlapping
+ * segments as in the product).  Either output may be NULL,
  * not both (where they have any elements), and so may what only it needs.
  * beta == 0 never reads the outputs; an adapter without rows gets beta times
  * what it had.  fp32 sums in an order that depends on sizes and offsets alone.

@@ -1029,8 +1029,8 @@ struct Slot {
   int part;            // the adapter's first place among the parts
 };
 
-// The rows of segment i, clamped into the buffer.
-__device__ __forceinline__ void segment_rows(const SegmentArgs& g, int64_t n_rows, int64_t i, int64_t& lo, int64_t& hi) {
+// The rows of segment i, clamped into the buffer; whether its end lies before its beginning.
+__device__ __forceinline__ bool segment_rows(const SegmentArgs& g, int64_t n_rows, int64_t i, int64_t& lo, int64_t& hi) {
   if (g.offsets) {
     lo = min(max(g.offsets[i], (int64_t)0), n_rows);
     hi = min(max(g.offsets[i + 1], (int64_t)0), n_rows);
@@ -1038,7 +1038,54 @@ __device__ __forceinline__ void segment_rows(const SegmentArgs& g, int64_t n_row
     lo = g.n == 1 ? 0 : i;
     hi = g.n == 1 ? n_rows : i + 1;
   }
+  const bool falls = hi < lo;
   hi = max(lo, hi);
+  return falls;
+}
+
+// Segments overlap only where offsets decrease.  A row is then the first segment's
+// that has it: the runs of rows that are a segment's own, f(i, lo, hi), for the
+// segments that are wanted, in order, by a whole wave.  (Not a path for speed: a run
+// looks at all earlier segments, unless they are known to have the whole segment.)
+template <typename W, typename F>
+__device__ __forceinline__ void own_runs(const SegmentArgs& g, int64_t n_rows, W&& wanted, F&& f) {
+  const int lane = threadIdx.x & 63;
+  int64_t c0 = 0, c1 = 0;  // rows that earlier segments have without a gap
+  for (int64_t i0 = 0; i0 < g.n; i0 += 64) {
+    int64_t lo = 0, hi = 0;
+    if (i0 + lane < g.n) segment_rows(g, n_rows, i0 + lane, lo, hi);
+    unsigned long long left = __ballot(lo < hi);
+    while (left) {
+      const int l = __ffsll(left) - 1;
+      left &= left - 1;
+      const int64_t i = i0 + l, from = __shfl(lo, l), to = __shfl(hi, l);
+      if (c0 <= from && to <= c1) continue;
+      if (wanted(i))
+        for (int64_t at = from; at < to;) {
+          int64_t past = at, next = to;  // where those that have row `at` end, and where another begins
+          for (int64_t j = lane; j < i; j += 64) {
+            int64_t a, b;
+            segment_rows(g, n_rows, j, a, b);
+            if (a <= at) past = max(past, b);
+            else if (a < b) next = min(next, a);
+          }
+#pragma unroll
+          for (int off = 1; off < 64; off <<= 1) {
+            past = max(past, (int64_t)__shfl_xor(past, off));
+            next = min(next, (int64_t)__shfl_xor(next, off));
+          }
+          if (past == at) f(i, at, next);
+          at = past == at ? next : past;
+        }
+      if (from <= c1 && c0 <= to) {
+        c0 = min(c0, from);
+        c1 = max(c1, to);
+      } else if (to - from > c1 - c0) {
+        c0 = from;
+        c1 = to;
+      }
+    }
+  }
 }
 
 // The first segments as the workgroup has read them, for list_rows.
@@ -1046,16 +1093,19 @@ constexpr int kKnown = 256;
 struct Segments {
   unsigned long long cnt[kLoraMaxAdapters];
   int lo[kKnown], len[kKnown], id[kKnown];
+  int falls;  // whether offsets decrease anywhere
 };
-// cnt[g] = rows of adapter g, by the whole workgroup.
+// cnt[g] = rows of adapter g, by the whole workgroup; n_rows at most over all adapters.
 __device__ __forceinline__ void count_rows(const SegmentArgs& g, int64_t n_rows, Segments& s) {
   const int tid = threadIdx.x;
   int64_t lo = 0, hi = 0, id = -1;
+  bool falls = false;
   if (tid < g.n) {  // loaded while the counters are cleared
-    segment_rows(g, n_rows, tid, lo, hi);
+    falls = segment_rows(g, n_rows, tid, lo, hi);
     id = adapter_of(g, tid);
   }
   for (int i = tid; i < (int)g.n_adapters; i += kThreads) s.cnt[i] = 0;
+  if (tid == 0) s.falls = 0;
   __syncthreads();
   s.lo[tid] = (int)lo;
   s.len[tid] = (int)(hi - lo);
@@ -1063,9 +1113,18 @@ __device__ __forceinline__ void count_rows(const SegmentArgs& g, int64_t n_rows,
   if (id >= 0 && hi > lo) atomicAdd(&s.cnt[id], (unsigned long long)(hi - lo));
   for (int64_t i = tid + kThreads; i < g.n; i += kThreads) {
     id = adapter_of(g, i);
-    segment_rows(g, n_rows, i, lo, hi);
+    falls |= segment_rows(g, n_rows, i, lo, hi);
     if (id >= 0 && hi > lo) atomicAdd(&s.cnt[id], (unsigned long long)(hi - lo));
   }
+  if (falls) s.falls = 1;
+  __syncthreads();
+  if (s.falls == 0) return;
+  for (int i = tid; i < (int)g.n_adapters; i += kThreads) s.cnt[i] = 0;
+  __syncthreads();
+  if (tid < 64)
+    own_runs(g, n_rows, [&](int64_t i) { return adapter_of(g, i) >= 0; }, [&](int64_t i, int64_t a, int64_t b) {
+      if (tid == 0) s.cnt[adapter_of(g, i)] += (unsigned long long)(b - a);
+    });
   __syncthreads();
 }
 static_assert(kKnown == kThreads);
@@ -1077,8 +1136,7 @@ __device__ __forceinline__ bool find_slot(const unsigned long long* cnt, int n_a
   for (int g0 = 0; g0 < n_adapters; g0 += 64) {
     const bool in = g0 + lane < n_adapters;
     const unsigned long long rows = in ? cnt[g0 + lane] : 0;
-    // (overlapping segments can claim more rows than there are: no more slots than the buffer has)
-    const int slots = in ? max(1, (int)min((rows + chunk - 1) / (unsigned)chunk, 1ull << 20)) : 0;
+    const int slots = in ? max(1, (int)((rows + chunk - 1) / (unsigned)chunk)) : 0;
     int incl = slots, pin = slots > 1 ? slots : 0;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -1110,6 +1168,14 @@ __device__ __forceinline__ void list_rows(const SegmentArgs& g, int64_t n_rows, 
                                           int* list) {
   const int tid = threadIdx.x, lane = tid & 63;
   int64_t at = 0;  // the adapter's rows before this group of segments
+  if (known.falls) {  // every wave goes through the runs and lists its threads' share
+    own_runs(g, n_rows, [&](int64_t i) { return at < s.row1 && adapter_of(g, i) == s.g; }, [&](int64_t, int64_t a, int64_t b) {
+      const int64_t f1 = min(at + b - a, s.row1);
+      for (int64_t f = max(at, s.row0) + tid; f < f1; f += kThreads) list[f - s.row0] = (int)(a + f - at);
+      at += b - a;
+    });
+    return;
+  }
   for (int64_t i0 = 0; i0 < g.n && at < s.row1; i0 += 64) {
     int64_t lo = 0, hi = 0;
     const int64_t i = i0 + lane;
@@ -1304,7 +1370,7 @@ union WeightLds {  // the sums come last
 
 template <int kDtype, int kR16>
 __device__ __forceinline__ void weight_tile(const LoraWeightArgs& a, const LoraFactor& f, int64_t chunk, int64_t want,
-                                            int64_t ct, float* __restrict__ part, int64_t parts,
+                                            int64_t ct, float* __restrict__ part,
                                             WeightLds<weight_run(kR16, kDtype)>& lds) {
   constexpr int kOut = weight_run(kR16, kDtype);
   float* const red = lds.red;
@@ -1359,9 +1425,8 @@ __device__ __forceinline__ void weight_tile(const LoraWeightArgs& a, const LoraF
     if (16 * i + r < a.rank && n > 0) {
       const int64_t k = s.slots > 1 ? s.part + s.row0 / chunk : s.g;
       const int64_t to = (k * a.rank + 16 * i + r) * f.cols + c;
-      // (rows that overlapping segments claim twice can make more parts than there is room for)
       if (s.slots == 1) finish<kOut>(a, f, scale, to, n, sum);
-      else if (k < parts) store_run<kOut>(part + to, n, sum);
+      else store_run<kOut>(part + to, n, sum);
     }
   }
 }
@@ -1369,7 +1434,7 @@ __device__ __forceinline__ void weight_tile(const LoraWeightArgs& a, const LoraF
 // Both factors' tiles, those of the first before those of the second; a factor
 // that is not asked for has none.
 struct WeightWork {
-  int64_t chunk, slots, parts;
+  int64_t chunk, slots;
   int64_t tiles[2];  // of columns
   float* part[2];
 };
@@ -1381,12 +1446,12 @@ __global__ __launch_bounds__(kThreads, (kR16 <= 1 ? 3 : kR16 <= 4 ? 2 : 1)) void
   } lds;
   int64_t b = block_id();
   if (b < w.slots * w.tiles[0]) {
-    weight_tile<kDx, kR16>(a, a.f[0], w.chunk, b / w.tiles[0], b % w.tiles[0], w.part[0], w.parts, lds.x);
+    weight_tile<kDx, kR16>(a, a.f[0], w.chunk, b / w.tiles[0], b % w.tiles[0], w.part[0], lds.x);
     return;
   }
   b -= w.slots * w.tiles[0];
   if (w.tiles[1] == 0) return;
-  weight_tile<kDy, kR16>(a, a.f[1], w.chunk, b / w.tiles[1], b % w.tiles[1], w.part[1], w.parts, lds.y);
+  weight_tile<kDy, kR16>(a, a.f[1], w.chunk, b / w.tiles[1], b % w.tiles[1], w.part[1], lds.y);
 }
 
 // The sums of an adapter's slots, if it has several.
@@ -1406,10 +1471,9 @@ __global__ __launch_bounds__(kThreads) void lora_weight_sum_kernel(LoraWeightArg
   const int64_t all = a.rank * f.cols, e = (span * kThreads + threadIdx.x) * kSumRun, n = all - e;
   if (n <= 0) return;
   const float* p = w.part[which] + s.part * all + e;
-  const int64_t slots = min((int64_t)s.slots, w.parts - s.part);
   float v[kSumRun] = {}, t[kSumRun];
 #pragma unroll 4
-  for (int64_t k = 0; k < slots; ++k) {
+  for (int k = 0; k < s.slots; ++k) {
     load_run<kSumRun>(p + k * all, n, t);
 #pragma unroll
     for (int i = 0; i < kSumRun; ++i) v[i] += t[i];
@@ -1576,7 +1640,8 @@ int64_t weight_chunk(int64_t rows, int64_t rank, int64_t c_in, int64_t c_out) {
   while (chunk > 256 && (rows + chunk - 1) / chunk * tiles < 512) chunk /= 2;
   return chunk;
 }
-// Parts: the slots of adapters that have several, at most two for every chunk of rows.
+// Parts: the slots of adapters that have several, at most two for every chunk of rows (no row
+// is counted twice, and k full chunks and a rest are k + 1 <= 2 k slots).
 int64_t weight_parts(int64_t rows, int64_t chunk) { return rows > chunk ? 2 * (rows / chunk) : 0; }
 
 template <int kDx, int kDy>
@@ -1606,9 +1671,9 @@ hipError_t launch_lora_weight_grad(const LoraWeightArgs& a, hipStream_t stream) 
   WeightWork w{};
   w.chunk = weight_chunk(a.rows, a.rank, a.f[0].cols, a.f[1].cols);
   w.slots = a.seg.n_adapters + a.rows / w.chunk;
-  w.parts = weight_parts(a.rows, w.chunk);
+  const int64_t parts = weight_parts(a.rows, w.chunk);
   w.part[0] = static_cast<float*>(a.ws);
-  w.part[1] = w.part[0] + w.parts * a.rank * a.f[0].cols;
+  w.part[1] = w.part[0] + parts * a.rank * a.f[0].cols;
   const int dx = a.f[0].dtype, dy = a.f[1].dtype;
   hipError_t e;
   if (dx == dy) {
@@ -1622,7 +1687,7 @@ hipError_t launch_lora_weight_grad(const LoraWeightArgs& a, hipStream_t stream) 
     if (e != hipSuccess) return e;
     e = dy == 0 ? launch_weights<0, 0>(y, w, stream) : launch_weights<1, 1>(y, w, stream);
   }
-  if (e != hipSuccess || w.parts == 0) return e;
+  if (e != hipSuccess || parts == 0) return e;
   const auto spans_of = [&](const LoraFactor& f) { return f.out ? (a.rank * f.cols + kThreads * kSumRun - 1) / (kThreads * kSumRun) : 0; };
   const int64_t spans0 = spans_of(a.f[0]), spans = spans0 + spans_of(a.f[1]);
   if (spans == 0) return e;

@@ -780,7 +780,8 @@ size_t lh_lora_workspace_bytes(int grad, int64_t n_rows, int64_t n_segments, int
  * sizes alone, products exact or rounded to fp32; s keeps its 24 bits on the
  * way out, whatever the types.
  * One rounding to y_dtype at the end.  Infinities and NaN follow the formula,
- * in their own row only.
+ * in their own row only, those of the factors too (but that an s below 2^-133
+ * may count as zero where a bf16 factor is infinite).
  *   x      fp32 or bf16 [n_rows][ld_x], ld_x >= c_in.
  *   base   y_dtype [n_rows][ld_base], ld_base >= c_out, or NULL (0).  It may be
  *          y itself (with ld_base == ld_y): the projection's output is then

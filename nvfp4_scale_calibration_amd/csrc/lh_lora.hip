@@ -490,7 +490,7 @@ __device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[kN]) 
 // four ranks of one output: bf16 ones are paired across two ranks' rows by byte
 // permutation.  s comes through LDS; bf16 factors meet it in three bf16 values that
 // add up to it exactly.  8192 rows, 4096
-// -> 12288, rank 16: 79 us, 5.1 TB/s, as a copy; rank 64 (4096 x 4096) 27 us, 2.5, at
+// -> 12288, rank 16: 80 us, 5.0 TB/s, as a copy; rank 64 (4096 x 4096) 27 us, 2.5, at
 // two waves a SIMD.  128 or 256 rows a workgroup: 99 -> 105 to 111 us with both kernels.
 constexpr int kOutRows = 64;
 
@@ -511,6 +511,50 @@ __device__ __forceinline__ void pair_ranks(const Run<kOut, uint16_t> (&d)[4], s1
 // The bf16 parts of s that bf16 factors meet (0: fp32 factors meet s itself).
 template <typename TW>
 constexpr int out_planes = sizeof(TW) == 4 ? 0 : 3;
+
+// Four bf16 values, zeros in the place of infinities and NaN.
+__device__ __forceinline__ s16x4_t finite_or_zero(s16x4_t v) {
+  asm volatile("" : "+v"(v));  // computed where it is used: all of a wave's factors at once would spill
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (v[i] & 0x7f80) == 0x7f80 ? (short)0 : v[i];
+  return v;
+}
+
+// acc[o] = the sums over all ranks of s, whose parts are part(p, i) for the ranks 16 i on,
+// and bf16 factors.  A factor that is infinite or NaN is met by the first part of s alone,
+// which has the sign of s and is zero, infinite or NaN where s is (but for s below 2^-133):
+// a lower part that is zero would make NaN of the infinity.  As they are rare, all parts
+// meet all factors first, and a sum that is NaN has the wave add once more (which costs
+// the others 1 us of 79: 8192 rows, 4096 -> 12288, rank 16).
+template <int kPlanes, int kR16, int kOut, typename F>
+__device__ __forceinline__ void out_of_rank(const s16x4_t (&w)[kR16][kOut], F&& part, f32x4_t (&acc)[kOut]) {
+#pragma unroll
+  for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kR16; ++i)
+#pragma unroll
+    for (int p = kPlanes - 1; p >= 0; --p) {  // the smallest part first
+      const s16x4_t sv = part(p, i);
+#pragma unroll
+      for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(sv, w[i][o], acc[o], 0, 0, 0);
+    }
+  bool nan = false;
+#pragma unroll
+  for (int o = 0; o < kOut; ++o)
+    nan |= __builtin_isunordered(acc[o][0], acc[o][1]) | __builtin_isunordered(acc[o][2], acc[o][3]);
+  if (__ballot(nan) == 0) return;
+#pragma unroll
+  for (int o = 0; o < kOut; ++o) {
+    acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kR16; ++i) {
+      const s16x4_t finite = finite_or_zero(w[i][o]);
+#pragma unroll
+      for (int p = kPlanes - 1; p >= 0; --p)
+        acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(part(p, i), p > 0 ? finite : w[i][o], acc[o], 0, 0, 0);
+    }
+  }
+}
 
 // Outputs a lane, so that a wave's part of the factor takes 128 registers at most.
 template <typename TW, int kR16>
@@ -613,26 +657,22 @@ __global__ __launch_bounds__(kThreads, (out_waves<TW, TY, kR16>)) void lora_tile
       if (t + 16 < row_tile) load_base(t + 16, next);
       if ((rows >> t) & 0xffffull) {
         f32x4_t acc[kOut];
+        if constexpr (kPlanes == 0) {
 #pragma unroll
-        for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < kR16; ++i) {
-          if constexpr (kPlanes == 0) {
+          for (int i = 0; i < kR16; ++i) {
             const float4 f = *reinterpret_cast<const float4*>(lds + ((t + j16) * kPitch + 16 * i + 4 * q) * 4);
             const float sv[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x4f32(sv[c], wf[i][c][o], acc[o], 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int p = kPlanes - 1; p >= 0; --p) {  // the smallest part first
-              const s16x4_t sv =
-                  *reinterpret_cast<const s16x4_t*>(lds + ((p * row_tile + t + j16) * kPitch + 16 * i + 4 * q) * 2);
-#pragma unroll
-              for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(sv, wb[i][o], acc[o], 0, 0, 0);
-            }
           }
+        } else {
+          out_of_rank<kPlanes>(wb, [&](int p, int i) {
+            return *reinterpret_cast<const s16x4_t*>(lds + ((p * row_tile + t + j16) * kPitch + 16 * i + 4 * q) * 2);
+          }, acc);
         }
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -962,16 +1002,9 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
       for (int h = 0; h < kSub; ++h) {
         if (((rows >> (16 * h)) & 0xffffull) == 0) continue;
         f32x4_t acc[kOut];
-#pragma unroll
-        for (int o = 0; o < kOut; ++o) acc[o] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < kR16; ++i)
-#pragma unroll
-          for (int p = kPlanes - 1; p >= 0; --p) {  // the smallest part first
-            const s16x4_t sv = *reinterpret_cast<const s16x4_t*>(&planes[p][16 * h + j16][16 * i + 4 * q]);
-#pragma unroll
-            for (int o = 0; o < kOut; ++o) acc[o] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(sv, wb[i][o], acc[o], 0, 0, 0);
-          }
+        out_of_rank<kPlanes>(wb, [&](int p, int i) {
+          return *reinterpret_cast<const s16x4_t*>(&planes[p][16 * h + j16][16 * i + 4 * q]);
+        }, acc);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           if (((rows >> (16 * h + 4 * q + v)) & 1) == 0) continue;

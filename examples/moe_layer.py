@@ -60,8 +60,11 @@ def forward(lh, layer, x, ids, weights, quantize_x=False, adapters=None):
     # (rows of assignments without an expert are not written; nothing reads them)
     saved = (plan, ys)
     if adapters is not None:  # added in place; the rows are kept in 8 bits for the adapters' gradients
-        ys, s = lh.lh_lora(xs, *adapters, offsets=plan["offsets"], base=ys, y=ys, s=True)
-        saved = (plan, ys, s, lh.lh_checkpoint_pack(xs))
+        a, b, scale = adapters
+        if x_scale is not None:  # the adapters multiply the activations' units back as well
+            scale = scale * x_scale
+        ys, s = lh.lh_lora(xs, a, b, scale, offsets=plan["offsets"], base=ys, y=ys, s=True)
+        saved = (plan, ys, s, lh.lh_checkpoint_pack(xs)) + (() if x_scale is None else (scale,))
     return lh.lh_moe_combine(ys, plan["position"], weights), saved
 
 
@@ -73,9 +76,10 @@ def backward(lh, layer, saved, weights, dy, adapters=None):
                                          layer["global_scale"])
     if adapters is None:
         return lh.lh_moe_combine(dxs, plan["position"]), dweights
-    s, (values, scales) = saved[2:]
+    s, (values, scales) = saved[2:4]
+    scale = saved[4] if len(saved) > 4 else adapters[2]  # of the rows as they were kept: the tokens' gradient has no units
     dxs, ds = lh.lh_lora_grad(dys, *adapters, offsets=plan["offsets"], base=dxs, dx=dxs, ds=True)
-    da, db = lh.lh_lora_weight_grad(values, dys, s, ds, adapters[0].shape[0], adapters[2], offsets=plan["offsets"],
+    da, db = lh.lh_lora_weight_grad(values, dys, s, ds, adapters[0].shape[0], scale, offsets=plan["offsets"],
                                     x_scale=scales)
     return lh.lh_moe_combine(dxs, plan["position"]), dweights, da, db
 

@@ -759,7 +759,9 @@ lh_status lh_moe_combine_grad(const void *dy, int dtype, int64_t n_tokens, int64
  *                adapter i (n_segments <= n_adapters; ids_type is ignored).
  *   rank         0 .. 256, the same for all adapters (shorter ones end in
  *                zeros).
- *   scale        fp32 [n_adapters] (device), or NULL (1).
+ *   scale        fp32 [n_adapters] (device), or NULL (1).  Where x is in units of a
+ *                global scale (the values of lh_quantize_nvfp4), that scale belongs
+ *                into it, for the product and the factors' gradients.
  * ---------------------------------------------------------------------------
  */
 

@@ -1053,7 +1053,8 @@ def lh_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale: torch.Tens
     """y = base + scale[g] (x a[g]^T) b[g], row by row with the adapter g of the
     row's segment.  x [n_rows, c_in]; a [n_adapters, rank, c_in] and b
     [n_adapters, rank, c_out] (2-D: one adapter), rank-major both; scale fp32
-    [n_adapters].  offsets (device int64 [n_segments + 1]): segment i has the
+    [n_adapters], times the global scale where x is in units of one (the values
+    of lh_quantize_nvfp4).  offsets (device int64 [n_segments + 1]): segment i has the
     rows offsets[i] .. offsets[i+1]-1; without them every row is a segment (or
     all rows are one, with one adapter id or none).  adapter_ids (int32 or int64
     [n_segments], device): each segment's adapter, an id outside the adapters

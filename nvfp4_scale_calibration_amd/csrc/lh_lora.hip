@@ -47,8 +47,8 @@ __device__ __forceinline__ void tile_adapters(const SegmentArgs& g, int64_t t0, 
   __shared__ unsigned long long claim[kRows];
   const int tid = threadIdx.x;
   const int64_t t1 = min(t0 + kRows, n_rows);
-  if (!g.offsets) {
-    if (tid < kRows) of[tid] = t0 + tid < t1 ? (int)adapter_of(g, g.n == 1 ? 0 : t0 + tid) : -2;
+  if (!g.offsets) {  // all rows are one segment (a row each takes the row kernels)
+    if (tid < kRows) of[tid] = t0 + tid < t1 ? (int)adapter_of(g, 0) : -2;
     __syncthreads();
     return;
   }
@@ -882,17 +882,17 @@ constexpr int kBothWaves = 8;
 
 template <typename TY>
 __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lora_both_kernel(LoraArgs a) {
-  constexpr int kR16 = 1, kSub = 1, kRows = 16, kOut = 4, kPlanes = out_planes<uint16_t>;
-  constexpr int kPitch = 16 * kR16 + 8;  // elements of a row of a plane
-  __shared__ __attribute__((aligned(16))) char lds[kBothWaves * line_lds(kR16, kSub)];  // (the sums take a quarter of it)
+  constexpr int kRows = 16, kOut = 4, kPlanes = out_planes<uint16_t>;
+  constexpr int kPitch = 16 + 8;  // elements of a row of a plane
+  __shared__ __attribute__((aligned(16))) char lds[kBothWaves * line_lds(1, 1)];  // (the sums take a quarter of it)
   __shared__ __attribute__((aligned(16))) uint16_t planes[kPlanes][kRows][kPitch];
   __shared__ int of[kRows];
   const int64_t t0 = block_id() * kRows;
   if (t0 >= a.rows) return;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, j16 = lane & 15, q = lane >> 4;
   const int64_t rank = a.rank, t1 = min(t0 + kRows, a.rows);
-  into_rank<kR16, kSub, 2>(a, t0, 64 * wave, 64 * kBothWaves, lds + wave * line_lds(kR16, kSub), of,
-                           [&](int g, const f32x4_t (&acc)[kR16][kSub]) {
+  into_rank<1, 1, 2>(a, t0, 64 * wave, 64 * kBothWaves, lds + wave * line_lds(1, 1), of,
+                           [&](int g, const f32x4_t (&acc)[1][1]) {
                              float* const red = reinterpret_cast<float*>(lds);  // [kBothWaves][kRows][16]
                              __syncthreads();
                              *reinterpret_cast<f32x4_t*>(red + (wave * kRows + j16) * 16 + 4 * q) = acc[0][0];
@@ -927,35 +927,28 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
   // out of the rank: a wave takes 16 kOut outputs in turn, a lane kOut
   const TY* const base = static_cast<const TY*>(a.base);
   TY* const y = static_cast<TY*>(a.y);
-  Run<kOut, TY> b[kSub][4], b_next[kSub][4];
-  Run<kOut, uint16_t> w_next[kR16][4];
-  // uniform addresses and bytes of the lane's own: its outputs of the rows 16 h + 4 q + v and of the ranks 16 i + 4 q + c
-  uint32_t b_at[kSub][4], y_at[kSub][4], f_at[kR16][4];
+  Run<kOut, TY> b[4], b_next[4];
+  Run<kOut, uint16_t> w_next[4];
+  // uniform addresses and bytes of the lane's own: its outputs of the rows 4 q + v and of the ranks 4 q + v
+  uint32_t b_at[4], y_at[4], f_at[4];
 #pragma unroll
-  for (int h = 0; h < kSub; ++h)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const uint32_t t = (uint32_t)min((int64_t)(16 * h + 4 * q + v), t1 - t0 - 1);
-      b_at[h][v] = (t * (uint32_t)a.ld_base + kOut * j16) * sizeof(TY);
-      y_at[h][v] = (t * (uint32_t)a.ld_y + kOut * j16) * sizeof(TY);
-    }
-#pragma unroll
-  for (int i = 0; i < kR16; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) f_at[i][c] = (min((uint32_t)(16 * i + 4 * q + c), (uint32_t)rank - 1) * (uint32_t)a.c_y + kOut * j16) * 2;
+  for (int v = 0; v < 4; ++v) {
+    const uint32_t t = (uint32_t)min((int64_t)(4 * q + v), t1 - t0 - 1);
+    b_at[v] = (t * (uint32_t)a.ld_base + kOut * j16) * sizeof(TY);
+    y_at[v] = (t * (uint32_t)a.ld_y + kOut * j16) * sizeof(TY);
+    f_at[v] = (min((uint32_t)(4 * q + v), (uint32_t)rank - 1) * (uint32_t)a.c_y + kOut * j16) * 2;
+  }
   // At the end of a row a lane's outputs are moved back, so that all of them can
   // be loaded, and the first ones belong to another lane.
   const auto past = [&](int c_wave) { return max(c_wave + kOut * j16 + kOut - (int)a.c_y, 0); };
   const TY* const base_t = base ? base + t0 * a.ld_base : nullptr;
-  const auto load_base = [&](int c_wave, Run<kOut, TY> (&to)[kSub][4]) {
+  const auto load_base = [&](int c_wave, Run<kOut, TY> (&to)[4]) {
     const uint32_t c = (c_wave - past(c_wave)) * (int)sizeof(TY);
 #pragma unroll
-    for (int h = 0; h < kSub; ++h)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (base) __builtin_memcpy(to[h][v].w, at_byte(base_t, b_at[h][v] + c), sizeof to[h][v].w);
-        else to[h][v] = Run<kOut, TY>{};
-      }
+    for (int v = 0; v < 4; ++v) {
+      if (base) __builtin_memcpy(to[v].w, at_byte(base_t, b_at[v] + c), sizeof to[v].w);
+      else to[v] = Run<kOut, TY>{};
+    }
   };
   const int c_first = wave * 16 * kOut, c_step = 16 * kOut * kBothWaves, c_end = (int)a.c_y;
   left = all;
@@ -968,9 +961,7 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
     const auto load_w = [&](int c_wave) {
       const uint32_t at = (c_wave - past(c_wave)) * 2;
 #pragma unroll
-      for (int i = 0; i < kR16; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) __builtin_memcpy(w_next[i][c].w, at_byte(wt, f_at[i][c] + at), sizeof w_next[i][c].w);
+      for (int c = 0; c < 4; ++c) __builtin_memcpy(w_next[c].w, at_byte(wt, f_at[c] + at), sizeof w_next[c].w);
     };
     if (c_first < c_end) {
       load_w(c_first);
@@ -978,19 +969,14 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
     }
 #pragma unroll 1
     for (int c_wave = c_first; c_wave < c_end; c_wave += c_step) {
-      s16x4_t wb[kR16][kOut];
+      s16x4_t wb[1][kOut];
 #pragma unroll
-      for (int i = 0; i < kR16; ++i) {
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int o = 0; o < kOut / 2; ++o) w_next[c].w[o] = 4 * q + c < rank ? w_next[c].w[o] : 0u;
+      pair_ranks<kOut>(w_next, wb[0]);
 #pragma unroll
-          for (int o = 0; o < kOut / 2; ++o) w_next[i][c].w[o] = 16 * i + 4 * q + c < rank ? w_next[i][c].w[o] : 0u;
-        pair_ranks<kOut>(w_next[i], wb[i]);
-      }
-#pragma unroll
-      for (int h = 0; h < kSub; ++h)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) b[h][v] = b_next[h][v];
+      for (int v = 0; v < 4; ++v) b[v] = b_next[v];
       if (c_wave + c_step < c_end) {
         load_w(c_wave + c_step);
         load_base(c_wave + c_step, b_next);
@@ -998,21 +984,15 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
       const int skip = min(past(c_wave), kOut);
       TY* const y_t = y + t0 * a.ld_y;
       const uint32_t y_c = (c_wave - past(c_wave)) * (int)sizeof(TY);
+      f32x4_t acc[kOut];
+      out_of_rank<kPlanes>(wb, [&](int p, int) { return *reinterpret_cast<const s16x4_t*>(&planes[p][j16][4 * q]); }, acc);
 #pragma unroll
-      for (int h = 0; h < kSub; ++h) {
-        if (((rows >> (16 * h)) & 0xffffull) == 0) continue;
-        f32x4_t acc[kOut];
-        out_of_rank<kPlanes>(wb, [&](int p, int i) {
-          return *reinterpret_cast<const s16x4_t*>(&planes[p][16 * h + j16][16 * i + 4 * q]);
-        }, acc);
+      for (int v = 0; v < 4; ++v) {
+        if (((rows >> (4 * q + v)) & 1) == 0) continue;
+        float out[kOut];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if (((rows >> (16 * h + 4 * q + v)) & 1) == 0) continue;
-          float out[kOut];
-#pragma unroll
-          for (int o = 0; o < kOut; ++o) out[o] = __builtin_fmaf(scale, acc[o][v], b[h][v].at(o));
-          store_own<kOut>(at_byte(y_t, y_at[h][v] + y_c), skip, out);
-        }
+        for (int o = 0; o < kOut; ++o) out[o] = __builtin_fmaf(scale, acc[o][v], b[v].at(o));
+        store_own<kOut>(at_byte(y_t, y_at[v] + y_c), skip, out);
       }
     }
   }
@@ -1024,15 +1004,13 @@ __global__ __launch_bounds__(64 * kBothWaves, (sizeof(TY) == 2 ? 4 : 2)) void lo
     const uint32_t y_c = (c_wave - past(c_wave)) * (int)sizeof(TY);
     load_base(c_wave, b);
 #pragma unroll
-    for (int h = 0; h < kSub; ++h)
+    for (int v = 0; v < 4; ++v) {
+      if (((bare >> (4 * q + v)) & 1) == 0) continue;
+      float out[kOut];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (((bare >> (16 * h + 4 * q + v)) & 1) == 0) continue;
-        float out[kOut];
-#pragma unroll
-        for (int o = 0; o < kOut; ++o) out[o] = b[h][v].at(o);
-        store_own<kOut>(at_byte(y + t0 * a.ld_y, y_at[h][v] + y_c), skip, out);
-      }
+      for (int o = 0; o < kOut; ++o) out[o] = b[v].at(o);
+      store_own<kOut>(at_byte(y + t0 * a.ld_y, y_at[v] + y_c), skip, out);
+    }
   }
 }
 

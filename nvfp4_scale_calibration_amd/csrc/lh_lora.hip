@@ -490,7 +490,7 @@ __device__ __forceinline__ void store_own(T* p, int skip, const float (&v)[kN]) 
 // four ranks of one output: bf16 ones are paired across two ranks' rows by byte
 // permutation.  s comes through LDS; bf16 factors meet it in three bf16 values that
 // add up to it exactly.  8192 rows, 4096
-// -> 12288, rank 16: 80 us, 5.0 TB/s, as a copy; rank 64 (4096 x 4096) 27 us, 2.5, at
+// -> 12288, rank 16: 80 us, 5.0 TB/s, as a copy; rank 64 (4096 x 4096) 26 us, 2.6, at
 // two waves a SIMD.  128 or 256 rows a workgroup: 99 -> 105 to 111 us with both kernels.
 constexpr int kOutRows = 64;
 
@@ -827,7 +827,8 @@ __device__ __forceinline__ void into_rank(const LoraArgs& a, int64_t t0, int64_t
 }
 
 // A workgroup takes 32 rows and a share of the pieces, its waves taking them in
-// turn.
+// turn.  (Ranks of 17 to 32 are held to 128 registers, at which two are spilled: 32768
+// rows, 2048 -> 1024, 79 us with the way out, and 86 with the registers they ask for.)
 template <int kR16>
 struct LineShape {
   static constexpr int kSub = 2, kRows = 16 * kSub, kWaves = kR16 <= 4 ? 8 : 4;
@@ -1509,10 +1510,16 @@ struct LoraPlan {
 };
 constexpr int64_t kFar = int64_t(1) << 21;  // elements of a row with which a tile's byte offsets stay below 2^31
 LoraPlan lora_plan(int64_t rows, int64_t segments, int64_t c_x, int64_t c_y, int64_t rank) {
-  // The row kernels read a row's adapter for every row, the tile kernels are some 12
-  // to 26 us whatever the rows (4096 -> 4096, bf16: 64 rows of rank 16 8.7 and 15.8 us,
-  // of rank 64 12.7 and 26; 256 rows of rank 16 12.8 and 14.1, of rank 64 25.6 and
-  // 17.8, but 36 where they are 64 segments).
+  // The row kernels read a row's adapter for every row; the tile kernels take some 11 to
+  // 18 us for any few rows, and go through a tile's adapters one by one.  bf16, row and
+  // tile kernels in us, one segment:
+  //   rank 16: 1024 -> 1024   64 rows 7.1 and 10.9, 256 rows 8.5 and 11.1, 512 rows 11.7 and 11.2
+  //            4096 -> 12288  64 rows 9.9 and 12.8, 128 rows 14.5 and 14.1, 256 rows 21 and 16
+  //            17408 -> 5120  64 rows 11.2 and 16.8, 256 rows 19.8 and 18.7, 512 rows 33 and 21
+  //   rank 64: 4096 -> 12288  64 rows 14.7 and 17.3, 128 rows 23.5 and 18.1
+  // and in segments of four rows, 4096 -> 12288, rank 16: 256 rows of 8 adapters 21.5 and
+  // 25, of 64 adapters 22 and 30, 512 rows 44 and 37, 1024 rows 86 and 57.  The bound does
+  // not know widths, and segments of four rows take the row kernels at any number of rows.
   LoraPlan p{rows * ((rank + 15) / 16) <= 256 || rows <= 4 * segments || c_y < 8 || c_x >= kFar || c_y >= kFar, 1};
   if (p.rows) {  // two pieces of 512 elements a wave while the card is not full
     const int64_t units = rows * ((rank + kRowRanks - 1) / kRowRanks), most = (c_x + 4095) / 4096;
@@ -1606,7 +1613,10 @@ hipError_t launch_tiles(const LoraArgs& a, int splits, float* part, hipStream_t 
 // Whether one launch does it: for many rows, unless most of the work is the way
 // out (8192 rows, rank 16, 4096 -> 4096: 47 us, two launches 59; 12288 -> 4096: 73
 // and 86; 4096 -> 12288: 107 and 101; 32768 rows, 2048 -> 1024: 63 and 71; larger
-// ranks leave room for one workgroup a CU, 32768 rows of rank 32: 88 and 75).
+// ranks leave room for one workgroup a CU, 32768 rows of rank 32: 88 and 75).  At the
+// bounds: 2048 rows, 4096 -> 4096 22 and 24 us, 1024 rows 17 and 17, but 2048 -> 1024 is
+// 9 and 13 at 1024 rows too; with twice as many columns out, 4096 -> 8192, 8192 rows take
+// 75 and 77, 2048 rows 36 and 33, and 2048 -> 4096 39 and 53 at 8192, 18 and 19 at 2048.
 bool both_ways(const LoraArgs& a) {
   return a.x_dtype == 1 && a.w_dtype == 1 && a.rank <= 16 && a.rows >= 2048 && a.c_y <= 2 * a.c_x;
 }
